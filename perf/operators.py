@@ -1,0 +1,387 @@
+"""Workloads of the expert-layer and 4-bit operators: what is measured, on which sizes, and the plain forms.
+
+Four operators, each with its own cases:
+
+* ``quant``   microscaled 4-bit quantisation (E2M1 codes, one power-of-two scale per 32 values) and its inverse;
+* ``gemm``    the product of two tensors in that format;
+* ``route``   a mixture-of-experts router: product, softmax, top-k;
+* ``moe``     the routed experts' SiLU-gated MLP on packed weights, summed with the routing weights.
+
+With ``own`` false ``run`` computes them in elementary torch operations; with ``own`` true it makes the calls a user
+makes of the library.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda:0"
+TERNARY, INT2, INT3, MX4 = 0, 1, 2, 4
+GRIDS = {"ternary": TERNARY, "int2": INT2, "int3": INT3, "mx4": MX4}
+BYTES = {"ternary": 2.125 / 8, "int2": 2.125 / 8, "int3": 3.125 / 8, "mx4": 4.25 / 8}  # per weight, scales included
+E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+# ---- cases ------------------------------------------------------------------------------------------------------------
+def _quant(name, N, K, dtype):
+    return dict(name=name, op="quant", N=N, K=K, dtype=dtype)
+
+
+def _gemm(name, M, N, K):
+    return dict(name=name, op="gemm", M=M, N=N, K=K)
+
+
+def _route(name, T, E, H, k, renorm):
+    return dict(name=name, op="route", T=T, E=E, H=H, k=k, renorm=renorm)
+
+
+def _moe(name, T, pad, E, k, H, I, gate, up, down):
+    return dict(name=name, op="moe", T=T, pad=pad, E=E, k=k, H=H, I=I, gate=gate, up=up, down=down)
+
+
+def listed():
+    return [
+        # the activations of one decoded token on their way into a 4-bit product: launch latency
+        _quant("quant token 4096", 1, 4096, "bf16"),
+        # a ragged prefill batch's activations
+        _quant("quant batch 517x5120", 517, 5120, "bf16"),
+        # a checkpoint's largest projection, kept in fp32
+        _quant("quant weights 17408x5120", 17408, 5120, "f32"),
+        # one decoded token through a 4-bit output projection
+        _gemm("gemm token 4096x4096", 1, 4096, 4096),
+        # a decode batch of odd size through a gate projection
+        _gemm("gemm batch 61 17408x5120", 61, 17408, 5120),
+        # a prefill batch through the same projection
+        _gemm("gemm prefill 4096 17408x5120", 4096, 17408, 5120),
+        # the router of one token, of a small odd batch with an odd number of experts, and of a full decode batch
+        _route("route token 128", 1, 128, 2048, 8, True),
+        _route("route batch 13 of 60", 13, 60, 2048, 4, False),
+        _route("route batch 64 of 256", 64, 256, 4096, 8, True),
+        # one decoded token through an expert layer of ternary weights
+        _moe("moe token ternary", 1, 0, 128, 8, 2048, 768, "ternary", "ternary", "ternary"),
+        # a padded decode batch, every projection on a grid of its own
+        _moe("moe batch 16 mixed", 16, 3, 64, 6, 2048, 1408, "int2", "ternary", "int3"),
+        # the largest decode batch, 4-bit experts
+        _moe("moe batch 64 mx4", 64, 0, 128, 8, 4096, 1536, "mx4", "mx4", "mx4"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(("quant", "gemm", "route", "moe"))
+    if op == "quant":
+        K = 32 * _log(rng, 4, 544)
+        return dict(op=op, N=_log(rng, 1, 17408 * 5120 // K), K=K, dtype=rng.choice(("bf16", "f32")))
+    if op == "gemm":
+        K = 32 * _log(rng, 4, 544)
+        N = _log(rng, 64, 17408)
+        return dict(op=op, M=_log(rng, 1, max(2, min(8192, 4096 * 17408 * 5120 // (N * K)))), N=N, K=K)
+    if op == "route":
+        E = _log(rng, 8, 256)
+        return dict(op=op, T=_log(rng, 1, 64), E=E, H=128 * rng.randint(8, 32), k=rng.randint(1, 8),
+                    renorm=rng.random() < 0.5)
+    T = _log(rng, 1, 64)
+    return dict(op=op, T=T, pad=rng.choice((0, 0, T // 4)), E=_log(rng, 8, 128), k=rng.randint(1, 8),
+                H=128 * rng.randint(8, 32), I=128 * rng.randint(4, 12),
+                gate=rng.choice(sorted(GRIDS)), up=rng.choice(sorted(GRIDS)), down=rng.choice(sorted(GRIDS)))
+
+
+def work(case):
+    op = case["op"]
+    if op == "quant":
+        n = case["N"] * case["K"]
+        # the input, the codes and scales, and the values they stand for
+        return {"bytes": n * (4 if case["dtype"] == "f32" else 2) + n * BYTES["mx4"] + n * 2, "flops": 2 * n}
+    if op == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        return {"bytes": (M + N) * K * BYTES["mx4"] + 2 * M * N, "flops": 2 * M * N * K}
+    if op == "route":
+        T, E, H = case["T"], case["E"], case["H"]
+        return {"bytes": 2 * T * H + 2 * E * H + 8 * T * case["k"], "flops": 2 * T * E * H}
+    T, E, k, H, I = case["T"] - case["pad"], case["E"], case["k"], case["H"], case["I"]
+    touched = E * (1 - (1 - k / E) ** T)  # experts that some token takes, on average
+    per = sum(BYTES[case[p]] for p in ("gate", "up", "down")) * H * I
+    return {"bytes": touched * per + 4 * case["T"] * H + 8 * case["T"] * k, "flops": 6 * T * k * H * I}
+
+
+# ---- inputs -----------------------------------------------------------------------------------------------------------
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _scale_tiles(s):
+    """Scale bytes [N][K/32] -> the 512-byte tiles of 128 rows x 4 blocks the 4-bit format stores them in."""
+    N, B = s.shape
+    t, c = -(-N // 128), -(-B // 4)
+    p = torch.zeros((t * 128, c * 4), dtype=torch.uint8, device=s.device)
+    p[:N, :B] = s
+    return p.view(t, 4, 32, c, 4).permute(0, 3, 2, 1, 4).contiguous().view(-1)  # byte 16 (r % 32) + 4 (r / 32) + block
+
+
+def _mx4_weights(N, K, g, std):
+    """Codes [N][K/2] and scale tiles as quantisation leaves them for N(0, std^2) values."""
+    w = torch.randn((N, K // 32, 32), generator=g, device=DEV) * std
+    e = torch.frexp(w.abs().amax(-1))[1] - 3
+    q = (w / torch.exp2(e.float()).unsqueeze(-1)).abs()
+    c = torch.zeros_like(q, dtype=torch.uint8)
+    for i, edge in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
+        c += (q > edge) if i % 2 == 0 else (q >= edge)
+    c |= (w < 0).to(torch.uint8) << 3
+    c = c.view(N, K // 2, 2)
+    return c[..., 0] | (c[..., 1] << 4), _scale_tiles((e + 127).to(torch.uint8))
+
+
+def _expert_weights(N, K, grid, g, std=0.02):
+    """Packed codes and scales of N rows: random codewords on the grid (or quantised normals in the 4-bit format)."""
+    if grid == MX4:
+        n = 1 << 22
+        rows = max(1, n // K)
+        if N <= rows:
+            return _mx4_weights(N, K, g, std)
+        # the rows of a block of distinct random ones, again and again: what they hold does not matter to the product
+        rows = rows // 128 * 128
+        c, s = _mx4_weights(rows, K, g, std)
+        pick = torch.randint(0, rows, (-(-N // rows),), generator=g, device=DEV).tolist()
+        codes = torch.cat([c.roll(p, 0) for p in pick])[:N].contiguous()
+        sb = s.view(rows // 128, -(-K // 128), 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(rows, -1)[:, : K // 32]
+        return codes, _scale_tiles(torch.cat([sb.roll(p, 0) for p in pick])[:N])
+    words = N * K // 16 if grid != INT3 else 3 * N * K // 32
+    w = torch.randint(-(2 ** 31), 2 ** 31, (words,), generator=g, device=DEV, dtype=torch.int64).to(torch.int32)
+    if grid == TERNARY:  # the stored 0 is no ternary codeword: it becomes the one of weight 0
+        w = w | ((~(w | (w >> 1)) & 0x55555555) << 1)
+    s = (torch.randn((N, K // 128), generator=g, device=DEV).abs() * std + std / 8).to(torch.bfloat16)
+    return w.view(torch.uint8), s
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    op, s = case["op"], dict(case=case)
+    if op == "quant":
+        N, K = case["N"], case["K"]
+        w = torch.randn((N, K), generator=g, device=DEV)
+        w *= torch.exp(torch.randn((1, K), generator=g, device=DEV))  # channels of unlike size
+        s["w"] = w.to(torch.bfloat16 if case["dtype"] == "bf16" else torch.float32)
+        s["codes"] = torch.empty((N, K // 2), dtype=torch.uint8, device=DEV)
+        s["scales"] = torch.empty(512 * -(-N // 128) * -(-K // 128), dtype=torch.uint8, device=DEV)
+        s["values"] = torch.empty((N, K), dtype=torch.bfloat16, device=DEV)
+        s["bad"] = torch.empty(1, dtype=torch.int32, device=DEV)
+    elif op == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        s["w"] = _mx4_weights(N, K, g, 0.02)
+        s["x"] = _mx4_weights(M, K, g, 1.0)
+        s["y"] = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+        s["ws"] = torch.zeros(160 << 20, dtype=torch.uint8, device=DEV)
+    elif op == "route":
+        T, E, H, k = case["T"], case["E"], case["H"], case["k"]
+        s["x"] = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+        s["router"] = (torch.randn((E, H), generator=g, device=DEV) / math.sqrt(H)).to(torch.bfloat16)
+        s["ids"] = torch.empty((T, k), dtype=torch.int32, device=DEV)
+        s["weights"] = torch.empty((T, k), dtype=torch.float32, device=DEV)
+    else:
+        T, E, k, H, I = (case[n] for n in ("T", "E", "k", "H", "I"))
+        s["gate"] = _expert_weights(E * I, H, GRIDS[case["gate"]], g)
+        s["up"] = _expert_weights(E * I, H, GRIDS[case["up"]], g)
+        s["down"] = _expert_weights(E * H, I, GRIDS[case["down"]], g)
+        s["x"] = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+        p = torch.softmax(torch.randn((T, E), generator=g, device=DEV), -1)
+        top, ids = torch.sort(p, dim=-1, descending=True, stable=True)
+        ids, top = ids[:, :k].to(torch.int32).contiguous(), top[:, :k]
+        if case["pad"]:
+            ids[T - case["pad"]:] = -1  # the padding of a batch takes no expert
+        s["ids"], s["weights"] = ids, (top / top.sum(-1, keepdim=True)).contiguous()
+        s["y"] = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+        s["ws"] = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    return s
+
+
+# ---- plain forms ------------------------------------------------------------------------------------------------------
+def _plain_mx4_encode(w):
+    """[N][K] values -> (magnitude codes with the sign in bit 3, scale exponents [N][K/32], how many are not finite)."""
+    N, K = w.shape
+    v = w.float().view(N, K // 32, 32)
+    fine = torch.isfinite(v)
+    amax = torch.where(fine, v.abs(), 0.0).amax(-1)
+    e = torch.where(amax > 0, torch.frexp(amax)[1] - 3, -127).clamp(-127, 127)
+    q = torch.ldexp(v, -e.unsqueeze(-1)).abs()
+    edges = torch.tensor((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0), device=w.device)
+    code = torch.bucketize(q.contiguous(), edges, right=False)
+    code = torch.where((q == 0.75) | (q == 1.75) | (q == 3.5), code + 1, code)  # ties go to the even code
+    code = torch.where(torch.isnan(v), 0, code) | ((v < 0).to(torch.int64) << 3)
+    return code.view(N, K), e, (~fine).sum().to(torch.int32).view(1)
+
+
+def _plain_mx4_decode(codes, scales, N, K):
+    """The values of N rows of codes [N][K/2] under tiled scales, in 32 bits."""
+    lut = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=codes.device)
+    v = lut[torch.stack((codes & 15, codes >> 4), -1).view(N, K).int()]
+    t, c = -(-N // 128), -(-K // 128)
+    e = scales.view(t, c, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(t * 128, c * 4)[:N, : K // 32]
+    return (v.view(N, K // 32, 32) * torch.exp2(e.float() - 127).unsqueeze(-1)).view(N, K)
+
+
+def _plain_rows(weights, grid, rows, K):
+    """The given rows of a packed matrix in 32 bits: `rows` of any shape, the result [*rows.shape][K]."""
+    packed, scales = weights
+    if grid == MX4:
+        lut = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=packed.device)
+        c = packed[rows]
+        v = lut[torch.stack((c & 15, c >> 4), -1).flatten(-2).int()]
+        tiles = scales.view(-1, -(-K // 128), 32, 4, 4)
+        e = tiles[rows // 128, :, rows % 32, rows % 128 // 32].flatten(-2)[..., : K // 32]
+        return (v.unflatten(-1, (K // 32, 32)) * torch.exp2(e.float() - 127).unsqueeze(-1)).flatten(-2)
+    words = packed.view(torch.int32)
+    if grid == INT3:
+        w = words.view(-1, K // 32, 3)[rows]
+        m = torch.arange(16, device=w.device, dtype=torch.int32)
+        bits = torch.stack((w.unsqueeze(-1) >> m, w.unsqueeze(-1) >> (m + 16)), -1) & 1  # [..., plane, m, half]
+        u = (bits[..., 0, :, :] + 2 * bits[..., 1, :, :] + 4 * bits[..., 2, :, :]).flatten(-3)
+        c = (u - 4).float()
+    else:
+        w = words.view(-1, K // 16)[rows]
+        m = 2 * torch.arange(8, device=w.device, dtype=torch.int32)
+        c = ((torch.stack((w.unsqueeze(-1) >> m, w.unsqueeze(-1) >> (m + 16)), -1) & 3).flatten(-3) - 2).float()
+    return (c.unflatten(-1, (K // 128, 128)) * scales[rows].float().unsqueeze(-1)).flatten(-2)
+
+
+def _plain(s):
+    case = s["case"]
+    op = case["op"]
+    if op == "quant":
+        code, e, bad = _plain_mx4_encode(s["w"])
+        lut = torch.tensor(E2M1 + tuple(-v for v in E2M1), device=DEV)
+        N, K = s["w"].shape
+        v = torch.ldexp(lut[code].view(N, K // 32, 32), e.unsqueeze(-1))
+        return {"values": v.view(N, K).to(torch.bfloat16), "bad": bad}
+    if op == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        y = _plain_mx4_decode(*s["x"], M, K) @ _plain_mx4_decode(*s["w"], N, K).T
+        return y.to(torch.bfloat16)
+    if op == "route":
+        # which expert comes first is decided in 64 bits: neighbours may be closer than 32 bits tell apart
+        logits = s["x"].double() @ s["router"].double().T
+        top, ids = torch.sort(logits, dim=-1, descending=True, stable=True)
+        top, ids = top[:, :case["k"]], ids[:, :case["k"]]
+        p = torch.exp(top - top[:, :1])
+        den = p if case["renorm"] else torch.exp(logits - top[:, :1])
+        return {"ids": ids.to(torch.int32), "weights": (p / den.sum(-1, keepdim=True)).float()}
+    T, k, H, I = (case[n] for n in ("T", "k", "H", "I"))
+    x, out = s["x"].float(), []
+    step = max(1, (1 << 29) // (k * H * I))
+    for t in range(0, T, step):  # some tokens' experts at a time: their weights in 32 bits fill the memory
+        ids = s["ids"][t:t + step].long()
+        here = ids >= 0
+        e = torch.where(here, ids, 0).flatten()
+        xt = x[t:t + step].repeat_interleave(k, 0).unsqueeze(-1)
+        rows = e.unsqueeze(-1) * I + torch.arange(I, device=DEV)
+        gate = (_plain_rows(s["gate"], GRIDS[case["gate"]], rows, H) @ xt).squeeze(-1)
+        up = (_plain_rows(s["up"], GRIDS[case["up"]], rows, H) @ xt).squeeze(-1)
+        h = gate / (1 + torch.exp(-gate)) * up
+        rows = e.unsqueeze(-1) * H + torch.arange(H, device=DEV)
+        y = (_plain_rows(s["down"], GRIDS[case["down"]], rows, I) @ h.unsqueeze(-1)).view(-1, k, H)
+        out.append((torch.where(here, s["weights"][t:t + step], 0.0).unsqueeze(-1) * y).sum(1))
+    return torch.cat(out).to(torch.bfloat16)
+
+
+def run(state):
+    if not own:
+        return _plain(state)
+    from decode_gemv_tb_b200 import tb
+
+    s = state
+    case = s["case"]
+    op = case["op"]
+    if op == "quant":
+        tb.tb_mx4_quantize(s["w"], codes=s["codes"], scales=s["scales"], bad_count=s["bad"])
+        tb.tb_mx4_dequantize(s["codes"], s["scales"], case["N"], case["K"], W=s["values"])
+        return {"values": s["values"], "bad": s["bad"]}
+    if op == "gemm":
+        return tb.tb_mx4_gemm(*s["w"], *s["x"], case["M"], case["N"], case["K"], Y=s["y"], ws=s["ws"])
+    if op == "route":
+        tb.tb_moe_route(s["x"], s["router"], case["k"], renormalize=case["renorm"], ids=s["ids"], weights=s["weights"])
+        return {"ids": s["ids"], "weights": s["weights"]}
+    if "layer" not in s:
+        s["layer"] = tb.moe_layer(*((*s[p], GRIDS[case[p]]) for p in ("gate", "up", "down")), case["E"], case["H"],
+                                  case["I"])
+    return tb.tb_moe(s["layer"], s["x"], s["ids"], s["weights"], y=s["y"], ws=s["ws"])
+
+
+# ---- definitions in 64 bits -------------------------------------------------------------------------------------------
+def _value4(code):
+    """The value of a 4-bit code, from its sign, exponent and mantissa bits, in 64 bits."""
+    c = code.long()
+    ex, man = (c >> 1) & 3, (c & 1).double()
+    mag = torch.where(ex == 0, man * 0.5, (1 + man * 0.5) * 2.0 ** (ex - 1).double())
+    return torch.where(c >= 8, -mag, mag)
+
+
+def _tile_bytes(tiles, N, B, first=0):
+    """Scale bytes [N][B] of rows first .. first + N - 1, fetched by their address in the tiles."""
+    r = torch.arange(first, first + N, device=tiles.device).unsqueeze(1)
+    b = torch.arange(B, device=tiles.device).unsqueeze(0)
+    at = ((r // 128) * (-(-B // 4)) + b // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4
+    return tiles[at]
+
+
+def _matrix64(weights, grid, first, N, K):
+    """Rows first .. first + N - 1 of a packed matrix, in 64 bits."""
+    packed, scales = weights
+    k = torch.arange(K, device=packed.device)
+    if grid == MX4:
+        byte = packed[first:first + N].long()
+        v = _value4((byte[:, k // 2] >> (4 * (k % 2))) & 15)
+        e = _tile_bytes(scales, N, K // 32, first).long() - 127
+        return v * torch.pow(torch.tensor(2.0, dtype=torch.float64, device=v.device), e.double())[:, k // 32]
+    words = packed.view(torch.int32)
+    if grid == INT3:
+        w = words.view(-1, K // 32 * 3)[first:first + N].long() & 0xFFFFFFFF
+        bit = (k % 32) // 2 + 16 * (k % 2)
+        c = sum((((w[:, k // 32 * 3 + p] >> bit) & 1) << p) for p in range(3)) - 4
+    else:
+        w = words.view(-1, K // 16)[first:first + N].long() & 0xFFFFFFFF
+        c = ((w[:, k // 16] >> ((k % 16) // 2 * 2 + 16 * (k % 2))) & 3) - 2
+    return c.double() * scales[first:first + N].double()[:, k // 128]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "quant":
+        w = s["w"].double()
+        N, K = w.shape
+        b = w.view(N, K // 32, 32)
+        amax = b.abs().amax(-1, keepdim=True)
+        scale = torch.ldexp(torch.ones_like(amax), torch.frexp(amax)[1] - 3)  # frexp: amax = f 2^e, 1/2 <= f < 1
+        q = b / scale
+        mag = q.abs().clamp(max=6.0)
+        step = torch.where(mag < 2, 0.5, torch.where(mag < 4, 1.0, 2.0)).double()
+        v = torch.round(mag / step) * step  # half to even: of two neighbours the one with the even code
+        return {"values": (torch.sign(q) * v * scale).view(N, K), "bad": None}
+    if op == "gemm":
+        M, N, K = case["M"], case["N"], case["K"]
+        return _matrix64(s["x"], MX4, 0, M, K) @ _matrix64(s["w"], MX4, 0, N, K).T
+    if op == "route":
+        logits = torch.einsum("th,eh->te", s["x"].double(), s["router"].double())
+        E, k = case["E"], case["k"]
+        i = torch.arange(E, device=DEV)
+        a, b = logits.unsqueeze(2), logits.unsqueeze(1)  # expert e is beaten by f
+        rank = ((b > a) | ((b == a) & (i.view(1, 1, E) < i.view(1, E, 1)))).sum(-1)
+        ids = torch.argsort(rank, dim=-1)[:, :k]
+        p = torch.softmax(logits, -1).gather(1, ids)
+        return {"ids": ids.to(torch.int32), "weights": p / p.sum(-1, keepdim=True) if case["renorm"] else p}
+    E, H, I = case["E"], case["H"], case["I"]
+    x, y = s["x"].double(), torch.zeros((case["T"], H), dtype=torch.float64, device=DEV)
+    ids = s["ids"].cpu()
+    for e in sorted(set(ids.flatten().tolist()) - {-1}):
+        t, j = (v.to(DEV) for v in torch.nonzero(ids == e, as_tuple=True))
+        gate = x[t] @ _matrix64(s["gate"], GRIDS[case["gate"]], e * I, I, H).T
+        up = x[t] @ _matrix64(s["up"], GRIDS[case["up"]], e * I, I, H).T
+        h = gate * torch.sigmoid(gate) * up
+        y.index_add_(0, t, s["weights"][t, j].double().unsqueeze(1)
+                     * (h @ _matrix64(s["down"], GRIDS[case["down"]], e * H, H, I).T))
+    return y
