@@ -176,7 +176,6 @@ def prepare(case, seed):
         s["w"] = _mx4_weights(N, K, g, 0.02)
         s["x"] = _mx4_weights(M, K, g, 1.0)
         s["y"] = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
-        s["ws"] = torch.zeros(160 << 20, dtype=torch.uint8, device=DEV)
     elif op == "route":
         T, E, H, k = case["T"], case["E"], case["H"], case["k"]
         s["x"] = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
@@ -301,7 +300,7 @@ def run(state):
         tb.tb_mx4_dequantize(s["codes"], s["scales"], case["N"], case["K"], W=s["values"])
         return {"values": s["values"], "bad": s["bad"]}
     if op == "gemm":
-        return tb.tb_mx4_gemm(*s["w"], *s["x"], case["M"], case["N"], case["K"], Y=s["y"], ws=s["ws"])
+        return tb.tb_mx4_gemm(*s["w"], *s["x"], case["M"], case["N"], case["K"], Y=s["y"])
     if op == "route":
         tb.tb_moe_route(s["x"], s["router"], case["k"], renormalize=case["renorm"], ids=s["ids"], weights=s["weights"])
         return {"ids": s["ids"], "weights": s["weights"]}
