@@ -334,8 +334,13 @@ extern "C" {
 int tb_version(void) { return 100; }
 
 unsigned int tb_wait_timeouts(void) {
-    const unsigned int a = take_wait_timeouts(), b = take_g8_timeouts(), c = take_ss_timeouts();
-    return (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu) ? 0xFFFFFFFFu : a + b + c;
+    const unsigned int n[] = {take_wait_timeouts(), take_g8_timeouts(), take_ss_timeouts(), take_mx_timeouts()};
+    unsigned int sum = 0;
+    for (const unsigned int v : n) {
+        if (v == 0xFFFFFFFFu) return v;
+        sum += v;
+    }
+    return sum;
 }
 
 tb_status_t tb_sync_status(tb_stream_t stream) {
@@ -558,6 +563,66 @@ tb_status_t tb_gate_up_silu(const tb_linear_t* gate, const tb_linear_t* up, uint
     if (workspace_bytes < tb_gate_up_workspace_bytes(gate, up)) return TB_ERR_ARG;
     return launch_g8_items(its, 2, workspace, workspace_bytes, (flags & TB_FLAG_OVERLAP_PREVIOUS) != 0, false,
                            static_cast<cudaStream_t>(stream), 0, h);
+}
+
+}  // extern "C"
+
+// ---- microscaled 4-bit floats ------------------------------------------------
+namespace {
+
+constexpr int64_t kMx4Block = 32;
+
+// rows and columns index 32-bit tensor coordinates
+bool mx4_shape_ok(int64_t N, int64_t K) {
+    return N >= 1 && N <= INT_MAX && K >= kMx4Block && K <= INT_MAX - 256 && K % kMx4Block == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tb_mx4_code_bytes(int64_t N, int64_t K) { return mx4_shape_ok(N, K) ? (size_t)(N * (K / 2)) : 0; }
+
+size_t tb_mx4_scale_bytes(int64_t N, int64_t K) {
+    return mx4_shape_ok(N, K) ? (size_t)512 * ((N + 127) / 128) * ((K + 127) / 128) : 0;
+}
+
+tb_status_t tb_mx4_quantize(const void* W, tb_dtype_t w_dtype, int64_t ldw, int64_t N, int64_t K, void* codes,
+                            uint8_t* scales, int32_t* bad_count, tb_stream_t stream) {
+    if (!W || !codes || !scales || !dtype_ok(w_dtype)) return TB_ERR_ARG;
+    if (!mx4_shape_ok(N, K) || ldw < K) return TB_ERR_SHAPE;
+    if (!aligned(W, 16) || ldw % (w_dtype == TB_F32 ? 4 : 8) != 0 || !aligned(codes, 16) || !aligned(scales, 16) ||
+        (bad_count && !aligned(bad_count, 4)))
+        return TB_ERR_ALIGN;
+    return cuda_status(
+        launch_mx4_quantize(W, w_dtype, ldw, N, K, codes, scales, bad_count, static_cast<cudaStream_t>(stream)));
+}
+
+tb_status_t tb_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t N, int64_t K, void* W,
+                              tb_dtype_t w_dtype, int64_t ldw, tb_stream_t stream) {
+    if (!W || !codes || !scales || !dtype_ok(w_dtype)) return TB_ERR_ARG;
+    if (!mx4_shape_ok(N, K) || ldw < K) return TB_ERR_SHAPE;
+    if (!aligned(W, 16) || ldw % (w_dtype == TB_F32 ? 4 : 8) != 0 || !aligned(codes, 16) || !aligned(scales, 16))
+        return TB_ERR_ALIGN;
+    return cuda_status(
+        launch_mx4_dequantize(codes, scales, N, K, W, w_dtype, ldw, static_cast<cudaStream_t>(stream)));
+}
+
+tb_status_t tb_mx4_gemm(const void* w_codes, const uint8_t* w_scales, const void* x_codes, const uint8_t* x_scales,
+                        void* Y, tb_dtype_t y_dtype, int64_t ldy, int64_t M, int64_t N, int64_t K, unsigned flags,
+                        tb_stream_t stream) {
+    if (!w_codes || !w_scales || !x_codes || !x_scales || (flags & ~(unsigned)TB_FLAG_TEST_STALL) != 0)
+        return TB_ERR_ARG;
+    const tb_status_t s = check_out(Y, y_dtype);
+    if (s != TB_OK) return s;
+    if (!mx4_shape_ok(N, K) || M < 1 || M > kMaxGemmM || ldy < N) return TB_ERR_SHAPE;
+    if (!aligned(w_codes, 16) || !aligned(w_scales, 16) || !aligned(x_codes, 16) || !aligned(x_scales, 16))
+        return TB_ERR_ALIGN;
+    if ((N + 127) / 128 * ((M + 127) / 128) > INT_MAX) return TB_ERR_SHAPE;  // units are counted in 32 bits
+    const bool stall = (flags & TB_FLAG_TEST_STALL) != 0;
+    return cuda_status(launch_mx4_gemm(w_codes, w_scales, x_codes, x_scales, Y, y_dtype, ldy, M, N, K,
+                                       stall ? kTestWaitCycles : kWaitCycles, stall,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

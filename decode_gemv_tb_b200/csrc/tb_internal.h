@@ -74,6 +74,18 @@ cudaError_t launch_gemm_ss(const void* packed, int grid, const uint16_t* scales,
                            void* Y, int ydt, int64_t ldy, int64_t M, int64_t N, int64_t K, void* ws,
                            size_t ws_bytes, long long wait_cycles, cudaStream_t st);
 unsigned int take_ss_timeouts();
+
+// ---- microscaled 4-bit floats (tb_mx4.cu, tb_mx4_gemm.cu) ----
+cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t N, int64_t K, void* codes,
+                                uint8_t* scales, int32_t* bad, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t N, int64_t K, void* W,
+                                  int w_dtype, int64_t ldw, cudaStream_t st);
+// `stall`: test hook, nothing is copied and every wait gives up
+cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* x, const uint8_t* x_scales, void* Y,
+                            int ydt, int64_t ldy, int64_t M, int64_t N, int64_t K, long long wait_cycles, bool stall,
+                            cudaStream_t st);
+unsigned int take_mx_timeouts();
+
 // bounded device waits that gave up since the last call (clears the count;
 // synchronous); 0xFFFFFFFF if the count cannot be read
 unsigned int take_wait_timeouts();

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(PKG, "libtb_b200.so")
 
 TERNARY, INT2, INT3 = 0, 1, 2
 TERNARY_B3 = 3  # the ternary grid, 5 codes per byte
+MX4 = 4  # microscaled 4-bit floats: the expert layer and tb_mx4_*
 F32, BF16 = 0, 1
 MAX_LAYER_ITEMS = 16
 FLAG_OVERLAP_PREVIOUS = 1
@@ -46,6 +47,11 @@ SIGNATURES = {
     "tb_sync_status": (_I32, [_P]),
     "tb_gate_up_workspace_bytes": (_SZ, [_P, _P]),
     "tb_gate_up_silu": (_I32, [_P, _P, _P, ctypes.c_uint, _P, _SZ, _P]),
+    "tb_mx4_code_bytes": (_SZ, [_I64, _I64]),
+    "tb_mx4_scale_bytes": (_SZ, [_I64, _I64]),
+    "tb_mx4_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "tb_mx4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "tb_mx4_gemm": (_I32, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, ctypes.c_uint, _P]),
 }
 
 
@@ -263,3 +269,97 @@ def tb_gate_up_silu(gate, up, h: torch.Tensor, ws: torch.Tensor | None = None, f
     _check(load().tb_gate_up_silu(g_ptr, u_ptr, _dev(h, "h"), flags, ws.data_ptr(), ws.numel(), stream),
            "tb_gate_up_silu")
     return h
+
+
+# ---- microscaled 4-bit floats -------------------------------------------------
+
+def _same_device(first: torch.Tensor, *rest) -> None:
+    """The library launches on the current device: every tensor has to live there."""
+    if not first.is_cuda:
+        raise TBError("tensors must be CUDA tensors")
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise TBError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise TBError(f"tensors on different devices: {dev} and {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """Row stride of a [rows][cols] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise TBError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise TBError(f"{name}'s rows must be contiguous")
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _bytes(t: torch.Tensor, name: str, need: int) -> int:
+    if t.dtype != torch.uint8 or t.numel() < need:
+        raise TBError(f"{name} must hold at least {need} bytes as uint8")
+    return _dev(t, name)
+
+
+def mx4_code_bytes(N: int, K: int) -> int:
+    return int(load().tb_mx4_code_bytes(N, K))
+
+
+def mx4_scale_bytes(N: int, K: int) -> int:
+    return int(load().tb_mx4_scale_bytes(N, K))
+
+
+def _mx4_sizes(N: int, K: int):
+    if N < 1 or K < 32 or K % 32:
+        raise TBError(f"MX4 needs N >= 1 and K a positive multiple of 32, got {N} x {K}")
+    return N * (K // 2), 512 * (-(-N // 128)) * (-(-K // 128))
+
+
+def tb_mx4_quantize(W: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                    bad_count: torch.Tensor | None = None, stream: int | None = None):
+    """W [N][K] (rows may be strided) -> codes [N][K/2] uint8 and the scale tiles (uint8)."""
+    N, K = W.shape
+    ldw = _rows(W, "W", N, K)
+    nc, ns = _mx4_sizes(N, K)
+    _same_device(W, codes, scales, bad_count)
+    if codes is None:
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty(ns, dtype=torch.uint8, device=W.device)
+    if bad_count is not None and bad_count.dtype != torch.int32:
+        raise TBError("bad_count must be int32")
+    bc = 0 if bad_count is None else _dev(bad_count, "bad_count")
+    _check(load().tb_mx4_quantize(W.data_ptr(), _wdtype(W), ldw, N, K, _bytes(codes, "codes", nc),
+                                  _bytes(scales, "scales", ns), bc, _stream(W) if stream is None else stream),
+           "tb_mx4_quantize")
+    return codes, scales
+
+
+def tb_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, W: torch.Tensor | None = None,
+                      out_dtype=torch.bfloat16, stream: int | None = None) -> torch.Tensor:
+    """The values that MX4 codes stand for, [N][K] fp32 or bf16."""
+    nc, ns = _mx4_sizes(N, K)
+    _same_device(codes, scales, W)
+    if W is None:
+        W = torch.empty((N, K), dtype=out_dtype, device=codes.device)
+    ldw = _rows(W, "W", N, K)
+    _check(load().tb_mx4_dequantize(_bytes(codes, "codes", nc), _bytes(scales, "scales", ns), N, K, W.data_ptr(),
+                                    _ydtype(W.dtype), ldw, _stream(codes) if stream is None else stream),
+           "tb_mx4_dequantize")
+    return W
+
+
+def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Tensor, x_scales: torch.Tensor,
+                M: int, N: int, K: int, Y: torch.Tensor | None = None, out_dtype=torch.float32, flags: int = 0,
+                stream: int | None = None) -> torch.Tensor:
+    """Y [M][N] = X W^T of two MX4 tensors (N rows of W, M rows of X, K columns)."""
+    wc, wsb = _mx4_sizes(N, K)
+    xc, xsb = _mx4_sizes(M, K)
+    _same_device(w_codes, w_scales, x_codes, x_scales, Y)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
+    ldy = _rows(Y, "Y", M, N)
+    _check(load().tb_mx4_gemm(_bytes(w_codes, "w_codes", wc), _bytes(w_scales, "w_scales", wsb),
+                              _bytes(x_codes, "x_codes", xc), _bytes(x_scales, "x_scales", xsb), Y.data_ptr(),
+                              _ydtype(Y.dtype), ldy, M, N, K, flags, _stream(Y) if stream is None else stream),
+           "tb_mx4_gemm")
+    return Y

@@ -344,6 +344,68 @@ TB_API size_t tb_gate_up_workspace_bytes(const tb_linear_t *gate, const tb_linea
 TB_API tb_status_t tb_gate_up_silu(const tb_linear_t *gate, const tb_linear_t *up, uint16_t *h, unsigned flags,
                                    void *workspace, size_t workspace_bytes, tb_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * MICROSCALED 4-BIT FLOATS (MX4)
+ *
+ * A second storage format for what the scalar grids do not hold (the page
+ * keeps sensitive projections at more bits; 무엇과 다른가), and for
+ * activations.  The pages have no counterpart; the format is the public
+ * microscaling one: blocks of 32 consecutive k share a scale.
+ *   value   w = v * 2^(byte - 127), v in {0, .5, 1, 1.5, 2, 3, 4, 6} with sign
+ *   codes   [N][K/2] bytes, K % 32 == 0: code k of a row is the low (k even) or
+ *           high (k odd) half of byte k/2; bit 3 of a code is the sign, bits
+ *           2..0 the index of |v| above.
+ *   scales  tiles of 512 bytes, [ceil(N/128)][ceil(K/128)]: the byte of row n
+ *           and block b (k in [32 b, 32 b + 32)) is byte
+ *             16 (n % 32) + 4 ((n % 128) / 32) + b % 4
+ *           of tile [n / 128][b / 4].  Blocks past K in the last tile of a row
+ *           hold 0.  Bytes of rows past N are never written and never reach a
+ *           result.  255 stands for NaN.
+ *   quantization  byte = clamp(floor(log2(amax)) - 2, -127, 127) + 127 over
+ *           the block's finite values (0 when none is nonzero); code = the
+ *           nearest of w / 2^(byte - 127), ties to the even code, magnitudes
+ *           above 6 to 6.  NaN gives code 0, +-Inf +-6; both are counted.
+ *   4.25 bits per value.  Sizes: */
+
+/* N * K / 2; 0 unless N >= 1, K >= 32, K % 32 == 0. */
+TB_API size_t tb_mx4_code_bytes(int64_t N, int64_t K);
+
+/* 512 * ceil(N/128) * ceil(K/128); 0 for bad arguments. */
+TB_API size_t tb_mx4_scale_bytes(int64_t N, int64_t K);
+
+/* Quantize rows of W to MX4 (rules above).
+ *   W          [N][ldw] fp32 or bf16 (w_dtype), ldw >= K; base and row stride
+ *              multiples of 16 bytes.
+ *   codes      tb_mx4_code_bytes(N, K) bytes, 16-byte aligned, fully written.
+ *   scales     tb_mx4_scale_bytes(N, K) bytes, 16-byte aligned, written for
+ *              the rows n < N.
+ *   bad_count  device int32, or NULL; when given, OVERWRITTEN with the number
+ *              of values that are NaN or infinite. */
+TB_API tb_status_t tb_mx4_quantize(const void *W, tb_dtype_t w_dtype, int64_t ldw, int64_t N, int64_t K, void *codes,
+                                   uint8_t *scales, int32_t *bad_count, tb_stream_t stream);
+
+/* The values MX4 codes stand for, [N][ldw] fp32 or bf16 (exact in both: a
+ * result above the type's range becomes infinite; only columns < K are
+ * written). */
+TB_API tb_status_t tb_mx4_dequantize(const void *codes, const uint8_t *scales, int64_t N, int64_t K, void *W,
+                                     tb_dtype_t w_dtype, int64_t ldw, tb_stream_t stream);
+
+/* Y = X W^T of two MX4 tensors, 1 <= M <= 65536, on the block-scaled tensor
+ * cores: one launch, no workspace, W read once per 256 batch rows.
+ *   w_codes, w_scales  [N] rows, x_codes, x_scales  [M] rows, of K values;
+ *                      16-byte aligned.
+ *   Y                  [M][ldy] fp32 or bf16, ldy >= N; Y[m][n] for n < N
+ *                      written.
+ *   flags              0 (test hook: TB_FLAG_TEST_STALL).
+ * Every product is exact; the running sum is rounded to fp32 once per 64 k:
+ *   |y - y_exact| <= (K/64 + 12) 2^-23 sum_k |x_k w_k| (plus 2^-8 |y| for bf16
+ *   outputs);
+ * results are bitwise deterministic.  A NaN scale makes the outputs of its
+ * row (of W or X) NaN. */
+TB_API tb_status_t tb_mx4_gemm(const void *w_codes, const uint8_t *w_scales, const void *x_codes,
+                               const uint8_t *x_scales, void *Y, tb_dtype_t y_dtype, int64_t ldy, int64_t M,
+                               int64_t N, int64_t K, unsigned flags, tb_stream_t stream);
+
 /* Size of the fixed device scratch behind tb_gemv_noalloc (4 MiB). */
 #define TB_NOALLOC_SCRATCH_BYTES (4u << 20)
 
