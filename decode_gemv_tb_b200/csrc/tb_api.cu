@@ -627,6 +627,70 @@ tb_status_t tb_mx4_gemm(const void* w_codes, const uint8_t* w_scales, const void
 
 }  // extern "C"
 
+// ---- mixture-of-experts layer --------------------------------------------------
+namespace {
+
+constexpr int64_t kMoeMaxDim = (int64_t)1 << 20;
+
+bool moe_grid_ok(int g) { return g == TB_GRID_TERNARY || g == TB_GRID_INT2 || g == TB_GRID_INT3 || g == TB_GRID_MX4; }
+
+tb_status_t check_moe(const tb_moe_t* l, int64_t T, int k) {
+    if (!l || !l->gate || !l->up || !l->down || !l->gate_scales || !l->up_scales || !l->down_scales) return TB_ERR_ARG;
+    for (const int g : {l->gate_grid, l->up_grid, l->down_grid}) {
+        if (is_b3(g)) return TB_ERR_UNSUPPORTED;
+        if (!moe_grid_ok(g)) return TB_ERR_ARG;
+    }
+    if (k < 1 || k > TB_MOE_MAX_TOPK || l->E < 1 || l->E > TB_MOE_MAX_EXPERTS) return TB_ERR_ARG;
+    if (!shape_ok(l->I, l->H) || !shape_ok(l->H, l->I) || l->H > kMoeMaxDim || l->I > kMoeMaxDim || T < 1 ||
+        T > TB_MOE_MAX_TOKENS)
+        return TB_ERR_SHAPE;
+    for (const void* p : {l->gate, l->up, l->down, l->gate_scales, l->up_scales, l->down_scales})
+        if (!aligned(p, 16)) return TB_ERR_ALIGN;
+    return TB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tb_status_t tb_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t T, int64_t E, int64_t H, int k,
+                         int renormalize, int32_t* ids, float* weights, tb_stream_t stream) {
+    if (!x || !router || !ids || !weights) return TB_ERR_ARG;
+    if (E < 1 || E > TB_MOE_MAX_EXPERTS || k < 1 || k > TB_MOE_MAX_TOPK || k > E) return TB_ERR_ARG;
+    if (T < 1 || T > kMaxGemmM || H < 8 || H % 8 != 0 || ldx < H) return TB_ERR_SHAPE;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(router, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+        return TB_ERR_ALIGN;
+    if (!moe_route_supported((int)E, H)) return TB_ERR_UNSUPPORTED;
+    return cuda_status(launch_moe_route(x, ldx, router, T, (int)E, H, k, renormalize != 0, ids, weights,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t tb_moe_workspace_bytes(const tb_moe_t* layer, int64_t T, int k) {
+    return check_moe(layer, T, k) == TB_OK ? 2 * moe_data_bytes(T, k, layer->I) : 0;
+}
+
+tb_status_t tb_moe(const tb_moe_t* layer, const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights,
+                   int64_t T, int k, void* y, tb_dtype_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                   tb_stream_t stream) {
+    tb_status_t s = check_moe(layer, T, k);
+    if (s != TB_OK) return s;
+    if (!x || !ids || !weights || !workspace) return TB_ERR_ARG;
+    if ((s = check_out(y, y_dtype)) != TB_OK) return s;
+    if (ldx < layer->H || ldy < layer->H) return TB_ERR_SHAPE;
+    if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+        return TB_ERR_ALIGN;
+    const size_t data = moe_data_bytes(T, k, layer->I);
+    if (workspace_bytes < 2 * data) return TB_ERR_ARG;
+    char* back = static_cast<char*>(workspace) + (workspace_bytes & ~size_t(255)) - data;
+    return cuda_status(launch_moe({layer->gate, layer->gate_scales, layer->gate_grid},
+                                  {layer->up, layer->up_scales, layer->up_grid},
+                                  {layer->down, layer->down_scales, layer->down_grid}, layer->E, layer->H, layer->I, x,
+                                  ldx, ids, weights, (int)T, k, y, y_dtype, ldy, back,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
 // ---- tb_gemv_noalloc: tb_gemv over a fixed, statically allocated scratch ----
 //
 // Same kernels and results as tb_gemv; the workspace is this file-scope

@@ -86,6 +86,23 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
                             cudaStream_t st);
 unsigned int take_mx_timeouts();
 
+// ---- mixture-of-experts layer (tb_moe_route.cu, tb_moe.cu) ----
+constexpr int kMx4 = 4;  // TB_GRID_MX4
+constexpr int kMoeMaxTokens = 64, kMoeMaxK = 16, kMoeMaxExperts = 512;
+bool moe_route_supported(int E, int64_t H);  // the activations of a token fit in shared memory
+cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t T, int E, int64_t H, int k,
+                             bool renorm, int32_t* ids, float* weights, cudaStream_t st);
+struct MoeWeights {
+    const void* packed;
+    const void* scales;
+    int grid;
+};
+// bytes of the gated activations between the two kernels (written before they are read)
+size_t moe_data_bytes(int64_t T, int k, int64_t I);
+cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWeights& down, int E, int64_t H, int64_t I,
+                       const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int T, int k, void* y,
+                       int ydt, int64_t ldy, void* data, cudaStream_t st);
+
 // bounded device waits that gave up since the last call (clears the count;
 // synchronous); 0xFFFFFFFF if the count cannot be read
 unsigned int take_wait_timeouts();

@@ -1,0 +1,225 @@
+// tb_moe_route.cu -- the router of a mixture-of-experts layer: logits,
+// softmax and the k best experts of every token, in one launch.
+//
+//     l[t][e] = sum_h x[t][h] R[e][h]      (bf16 inputs, 64-bit sums)
+//     ids[t]  = the k largest l[t], the lower index first among equals
+//     w[t][j] = exp(l[t][ids[j]] - max l[t]) / (sum over the chosen, or over all, of the same)
+//
+// The sums are held in 64 bits because they decide an order: two experts'
+// logits can be closer than fp32 sums of different order agree, and an expert
+// picked by rounding is a different layer.
+//
+// A bf16 needs no more than the high word of a double (8 exponent and 7
+// mantissa bits into 11 and 20), so x is converted once into high words in
+// shared memory, and a weight's bits shifted right by 3 are, as the high
+// word of a double, w 2^-896 exactly (both exponent fields start at 0, so
+// zeros and subnormals map alike); the sums carry that factor.  A product
+// costs one DFMA, two and a half integer operations per weight shared by
+// the tokens of the cluster.
+//
+// A cluster of eight CTAs handles TB tokens: its 128 warps take one expert
+// each at a time and leave the logits in the shared memory of the CTA that
+// selects for the token.  No workspace, no atomics.
+#include "tb_async.cuh"
+#include "tb_device.cuh"
+#include "tb_internal.h"
+
+#include <cstring>
+
+namespace tb {
+
+struct RouteArgs {
+    const uint16_t* x;  // [T][ldx]
+    const uint16_t* R;  // [E][H]
+    int32_t* ids;       // [T][k]
+    float* weights;     // [T][k]
+    int64_t ldx;
+    int32_t T, E, H, k, renorm;
+};
+
+namespace {
+
+constexpr int kRtCluster = 8;
+constexpr int kRtWarps = 16;
+constexpr int kRtThreads = kRtWarps * 32;
+constexpr int kRtUnroll = 4;
+
+__device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
+// high word of w 2^-896 for the bf16 in the upper half of u
+__device__ __forceinline__ uint32_t scaled_hi(uint32_t u) { return (uint32_t)((int32_t)u >> 3) & 0x8FFFE000u; }
+
+__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+// order of the logits as unsigned integers; NaN below everything but 0, which marks a taken expert
+__device__ __forceinline__ uint64_t order_key(double l) {
+    if (l != l) return 1;
+    const uint64_t b = (uint64_t)__double_as_longlong(l + 0.0);  // -0 equals +0
+    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+// one warp: the k best of E logits, their softmax weights
+template <int NPL>
+__device__ void select_experts(const double* l, const RouteArgs& A, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    uint64_t key[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        key[i] = e < A.E ? order_key(l[e]) : 0;
+    }
+    int mine = 0;  // the expert of slot `lane`
+    double top = 0;
+    for (int j = 0; j < A.k; ++j) {
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
+        const uint32_t mhi = __reduce_max_sync(0xffffffffu, hi);
+        const uint32_t mlo = __reduce_max_sync(0xffffffffu, hi == mhi ? lo : 0u);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, (hi == mhi && lo == mlo) ? (uint32_t)(lane + 32 * at) : ~0u);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if ((uint32_t)(lane + 32 * i) == e) key[i] = 0;
+        if (lane == j) mine = (int)e;
+        if (j == 0) top = l[e];
+    }
+    const float p = lane < A.k ? expf((float)(l[mine] - top)) : 0.f;
+    float sum = p;
+    if (!A.renorm) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < A.E) sum += expf((float)(l[e] - top));
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < A.k) {
+        A.ids[t * A.k + lane] = mine;
+        A.weights[t * A.k + lane] = p / sum;
+    }
+}
+
+template <int TB>
+__global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(kRtCluster, 1, 1) k_moe_route(const RouteArgs A) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    double* logits = reinterpret_cast<double*>(smem);                 // [E]: of this CTA's token
+    uint32_t* xs = reinterpret_cast<uint32_t*>(smem + 8 * ((A.E + 1) & ~1));  // [TB][H] high words of x
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t t0 = (int64_t)(blockIdx.x / kRtCluster) * TB;
+    const int nt = (int)min((int64_t)TB, A.T - t0);
+    cluster_arrive();
+    for (int i = threadIdx.x; i < TB * (A.H / 8); i += kRtThreads) {
+        const int t = i / (A.H / 8), h = (i - t * (A.H / 8)) * 8;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (t < nt) v = *reinterpret_cast<const uint4*>(A.x + (t0 + t) * A.ldx + h);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t d[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            d[2 * j] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] << 16));
+            d[2 * j + 1] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] & 0xFFFF0000u));
+        }
+        uint4* p = reinterpret_cast<uint4*>(xs + t * A.H + h);
+        p[0] = make_uint4(d[0], d[1], d[2], d[3]);
+        p[1] = make_uint4(d[4], d[5], d[6], d[7]);
+    }
+    __syncthreads();
+    cluster_wait();  // every CTA of the cluster has begun
+    for (int e = (int)rank * kRtWarps + warp; e < A.E; e += kRtCluster * kRtWarps) {
+        const uint16_t* w = A.R + (int64_t)e * A.H;
+        double acc[TB];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[t] = 0.0;
+        for (int h0 = lane * 8; h0 < A.H; h0 += 256 * kRtUnroll) {
+            uint4 v[kRtUnroll];
+#pragma unroll
+            for (int q = 0; q < kRtUnroll; ++q)
+                v[q] = h0 + 256 * q < A.H ? __ldg(reinterpret_cast<const uint4*>(w + h0 + 256 * q))
+                                          : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int q = 0; q < kRtUnroll; ++q) {
+                const int h = h0 + 256 * q;
+                if (h >= A.H) break;
+                const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+                double wd[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    wd[2 * j] = from_hi(scaled_hi(u[j] << 16));
+                    wd[2 * j + 1] = from_hi(scaled_hi(u[j]));
+                }
+#pragma unroll
+                for (int t = 0; t < TB; ++t) {
+                    const uint4* p = reinterpret_cast<const uint4*>(xs + t * A.H + h);
+                    const uint4 a = p[0], b = p[1];
+                    const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[t] = fma(wd[j], from_hi(d[j]), acc[t]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+            // 2^896: 1023 + 896 in the exponent field
+            if (lane == 0) st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), acc[t] * from_hi(1919u << 20));
+        }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0 && (int)rank < nt) {
+        if (A.E <= 128) select_experts<4>(logits, A, t0 + rank);
+        else if (A.E <= 256) select_experts<8>(logits, A, t0 + rank);
+        else select_experts<16>(logits, A, t0 + rank);
+    }
+}
+
+size_t route_smem(int TB, int E, int H) { return (size_t)8 * ((E + 1) & ~1) + (size_t)TB * H * 4; }
+
+template <int TB>
+cudaError_t launch(const RouteArgs& A, cudaStream_t st) {
+    const size_t smem = route_smem(TB, A.E, A.H);
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    if (e != cudaSuccess) return e;
+    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * kRtCluster, kRtThreads, smem, st>>>(A);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool moe_route_supported(int E, int64_t H) { return H <= INT32_MAX && route_smem(1, E, (int)H) <= 224 * 1024; }
+
+cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t T, int E, int64_t H, int k,
+                             bool renorm, int32_t* ids, float* weights, cudaStream_t st) {
+    RouteArgs A;
+    std::memset(&A, 0, sizeof(A));
+    A.x = x;
+    A.R = router;
+    A.ids = ids;
+    A.weights = weights;
+    A.ldx = ldx;
+    A.T = (int32_t)T;
+    A.E = E;
+    A.H = (int32_t)H;
+    A.k = k;
+    A.renorm = renorm ? 1 : 0;
+    // tokens per cluster: one while sixteen clusters (128 SMs) hold them all, then as many as share a weight's
+    // conversion and its read from L2
+    int tb = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
+    while (tb > 1 && route_smem(tb, E, (int)H) > 224 * 1024) tb /= 2;
+    return tb == 1 ? launch<1>(A, st) : (tb == 2 ? launch<2>(A, st) : launch<4>(A, st));
+}
+
+}  // namespace tb

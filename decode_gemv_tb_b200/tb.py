@@ -51,6 +51,9 @@ SIGNATURES = {
     "tb_mx4_scale_bytes": (_SZ, [_I64, _I64]),
     "tb_mx4_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P]),
     "tb_mx4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "tb_moe_route": (_I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "tb_moe_workspace_bytes": (_SZ, [_P, _I64, _I32]),
+    "tb_moe": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _I64, _P, _SZ, _P]),
     "tb_mx4_gemm": (_I32, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, ctypes.c_uint, _P]),
 }
 
@@ -59,6 +62,13 @@ class Linear(ctypes.Structure):
     """tb_linear_t"""
     _fields_ = [("packed", _P), ("scales", _P), ("x", _P), ("y", _P), ("N", _I64), ("K", _I64),
                 ("grid", ctypes.c_int32), ("y_dtype", ctypes.c_int32)]
+
+
+class MoE(ctypes.Structure):
+    """tb_moe_t"""
+    _fields_ = [("gate", _P), ("up", _P), ("down", _P), ("gate_scales", _P), ("up_scales", _P), ("down_scales", _P),
+                ("gate_grid", ctypes.c_int32), ("up_grid", ctypes.c_int32), ("down_grid", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("H", _I64), ("I", _I64)]
 
 
 class TBError(RuntimeError):
@@ -363,3 +373,91 @@ def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Te
                               _ydtype(Y.dtype), ldy, M, N, K, flags, _stream(Y) if stream is None else stream),
            "tb_mx4_gemm")
     return Y
+
+
+# ---- mixture-of-experts layer ---------------------------------------------------
+
+MOE_MAX_TOKENS, MOE_MAX_TOPK, MOE_MAX_EXPERTS = 64, 16, 512
+
+
+def _bf16_rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TBError(f"{name} must hold bf16 bit patterns")
+    return _rows(t, name, rows, cols)
+
+
+def _pairs(ids: torch.Tensor, weights: torch.Tensor, T: int, k: int):
+    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+        if t.dtype != dt or t.shape != (T, k):
+            raise TBError(f"{name} must be [{T}][{k}] {dt}, got {tuple(t.shape)} {t.dtype}")
+    return _dev(ids, "ids"), _dev(weights, "weights")
+
+
+def tb_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bool = True,
+                 ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream: int | None = None):
+    """x [T][H] (rows may be strided), router [E][H], both bf16 -> the k best experts of every token, ids [T][k]
+    int32, and their softmax weights [T][k] fp32."""
+    T, H = x.shape
+    ldx = _bf16_rows(x, "x", T, H)
+    E = router.shape[0]
+    if _bf16_rows(router, "router", E, H) != H:
+        raise TBError("router must be contiguous")
+    _same_device(x, router, ids, weights)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    ip, wp = _pairs(ids, weights, T, k)
+    _check(load().tb_moe_route(x.data_ptr(), ldx, router.data_ptr(), T, E, H, k, 1 if renormalize else 0, ip, wp,
+                               _stream(x) if stream is None else stream), "tb_moe_route")
+    return ids, weights
+
+
+class MoELayer:
+    """A tb_moe_t and the tensors it points to."""
+
+    def __init__(self, desc: MoE, tensors, device):
+        self.desc, self.tensors, self.device = desc, tensors, device
+        self.ptr = ctypes.addressof(desc)
+
+
+def moe_layer(gate, up, down, E: int, H: int, I: int) -> MoELayer:
+    """Describe E stacked experts.  gate, up, down: (packed, scales, grid) of the [E*I][H], [E*I][H] and [E*H][I]
+    matrices, as tb_pack (or tb_mx4_quantize) leaves them."""
+    mats = []
+    for name, (packed, scales, grid), (N, K) in zip(("gate", "up", "down"), (gate, up, down),
+                                                    ((E * I, H), (E * I, H), (E * H, I))):
+        _same_device(gate[0], packed, scales)
+        if grid == MX4:
+            nc, ns = _mx4_sizes(N, K)
+            mats.append((_bytes(packed, name, nc), _bytes(scales, f"{name} scales", ns)))
+        else:
+            if grid != TERNARY_B3 and scales.numel() < N * (K // 128):
+                raise TBError(f"{name} scales must hold {N} x {K // 128} values")
+            mats.append((_bytes(packed, name, packed_bytes(grid, N, K)), _bits(scales, f"{name} scales")))
+    desc = MoE(*(m[0] for m in mats), *(m[1] for m in mats), gate[2], up[2], down[2], E, H, I)
+    return MoELayer(desc, (gate, up, down), gate[0].device)
+
+
+def moe_workspace_bytes(layer: MoELayer, T: int, k: int) -> int:
+    return int(load().tb_moe_workspace_bytes(layer.ptr, T, k))
+
+
+def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None,
+           out_dtype=torch.float32, ws: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor:
+    """y [T][H] = the routed experts' MLP of x [T][H] (bf16, rows may be strided), summed with the weights."""
+    T, k = ids.shape
+    H = layer.desc.H
+    ldx = _bf16_rows(x, "x", T, H)
+    ip, wp = _pairs(ids, weights, T, k)
+    if x.device != layer.device:
+        raise TBError(f"x on {x.device}, the layer on {layer.device}")
+    _same_device(x, ids, weights, y, ws)
+    if y is None:
+        y = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    ldy = _rows(y, "y", T, H)
+    if ws is None:
+        ws = workspace(moe_workspace_bytes(layer, T, k), x.device)
+    _check(load().tb_moe(layer.ptr, x.data_ptr(), ldx, ip, wp, T, k, y.data_ptr(), _ydtype(y.dtype), ldy,
+                         _dev(ws, "workspace"), ws.numel(), _stream(x) if stream is None else stream), "tb_moe")
+    return y

@@ -114,7 +114,8 @@ typedef enum {
     TB_GRID_TERNARY = 0, /* {-1, 0, 1}, 2-bit container, offset 2 */
     TB_GRID_INT2 = 1,    /* {-2, -1, 0, 1}, offset 2 */
     TB_GRID_INT3 = 2,    /* {-4, ..., 3}, three bit-planes, offset 4 */
-    TB_GRID_TERNARY_B3 = 3 /* {-1, 0, 1}, 5 trits per byte (optional denser ternary layout) */
+    TB_GRID_TERNARY_B3 = 3, /* {-1, 0, 1}, 5 trits per byte (optional denser ternary layout) */
+    TB_GRID_MX4 = 4 /* microscaled 4-bit floats (below): tb_moe only, its scales are tb_mx4_quantize's tiles */
 } tb_grid_t;
 
 typedef enum { TB_F32 = 0, TB_BF16 = 1 } tb_dtype_t;
@@ -405,6 +406,73 @@ TB_API tb_status_t tb_mx4_dequantize(const void *codes, const uint8_t *scales, i
 TB_API tb_status_t tb_mx4_gemm(const void *w_codes, const uint8_t *w_scales, const void *x_codes,
                                const uint8_t *x_scales, void *Y, tb_dtype_t y_dtype, int64_t ldy, int64_t M,
                                int64_t N, int64_t K, unsigned flags, tb_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * MIXTURE-OF-EXPERTS LAYER
+ *
+ * A decoder layer whose MLP is E experts, of which a router picks k per
+ * token, for the few tokens of a decode batch.  The pages quantize dense
+ * layers; an expert is such a layer's gate, up and down (the SiLU-gated MLP
+ * of tb_gate_up_silu), each projection on a grid of its own. */
+
+#define TB_MOE_MAX_TOKENS 64  /* tokens of one tb_moe call */
+#define TB_MOE_MAX_TOPK 16    /* experts of a token */
+#define TB_MOE_MAX_EXPERTS 512
+
+/* The router: logits l[t][e] = sum_h x[t][h] router[e][h], ids[t][0 .. k) the
+ * experts of the k largest in descending order (of equal ones the lower
+ * index first; a NaN ranks last), and their softmax weights
+ *     p(e) = exp(l[t][e] - max l[t]),  weights[t][j] = p(ids[t][j]) / Z,
+ * Z the sum of p over the k chosen (renormalize != 0) or over all E.
+ * Logits are summed in 64 bits, so the order is that of the exact values
+ * unless they differ by less than H 2^-53 sum |x r|.
+ *   x        [T][ldx] bf16, ldx >= H, ldx % 8 == 0, 16-byte aligned;
+ *            1 <= T <= 65536.
+ *   router   [E][H] bf16, 16-byte aligned, finite; 1 <= E <=
+ *            TB_MOE_MAX_EXPERTS, H % 8 == 0 (H <= 56000, or
+ *            TB_ERR_UNSUPPORTED).
+ *   k        1 .. min(E, TB_MOE_MAX_TOPK).
+ *   ids      [T][k] int32, weights [T][k] fp32, written. */
+TB_API tb_status_t tb_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64_t T, int64_t E, int64_t H,
+                                int k, int renormalize, int32_t *ids, float *weights, tb_stream_t stream);
+
+/* The experts of a layer, E matrices stacked by rows: gate and up [E*I][H],
+ * down [E*H][I], packed and scaled as tb_pack and tb_scales_absmax (or, for
+ * TB_GRID_MX4, tb_mx4_quantize: scales = its tiles) leave such a matrix. */
+typedef struct {
+    const void *gate, *up, *down;                         /* device, packed codes */
+    const void *gate_scales, *up_scales, *down_scales;    /* device */
+    int32_t gate_grid, up_grid, down_grid;                /* tb_grid_t, not TB_GRID_TERNARY_B3 */
+    int32_t E;                                            /* 1 .. TB_MOE_MAX_EXPERTS */
+    int64_t H, I;                                         /* positive multiples of 128, at most 2^20 */
+} tb_moe_t;
+
+/* Workspace bytes of tb_moe: 2 * ceil256(4 T k I) (data only); 0 for bad
+ * arguments. */
+TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
+
+/* The routed experts of T tokens in two launches:
+ *     h = silu(Wgate[e] x[t]) * (Wup[e] x[t]),  y[t] = sum_j weights[t][j] Wdown[e] h,  e = ids[t][j].
+ *   layer      HOST descriptor.
+ *   x          [T][ldx] bf16, ldx >= H, ldx % 8 == 0, 16-byte aligned; finite,
+ *              |x| < 2^120; 1 <= T <= TB_MOE_MAX_TOKENS.
+ *   ids        [T][k] int32 (tb_moe_route's, or any): an id outside [0, E)
+ *              takes no expert (padding, experts of another rank), an id that
+ *              a token names twice counts with both weights.  A token
+ *              without experts gets y = 0.
+ *   weights    [T][k] fp32.
+ *   y          [T][ldy] fp32 or bf16, ldy >= H, written for columns < H.
+ *   workspace  tb_moe_workspace_bytes(layer, T, k) bytes (rules above).
+ * Codes (times their scale, for MX4) are decoded exactly, sums are fp32, h
+ * keeps 16 significant bits; bitwise deterministic.  With u = 2^-24 and A(v)
+ * the same sums over absolute values:
+ *     |dg|, |du| <= (H/8 + 16) u A(x),
+ *     |dh| <= 1.1 |dg| (|u| + |du|) + |silu(g)| |du| + 2^-16 |h|,
+ *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/4 + k + 16) u A_down(|h| + |dh|))
+ * (plus 2^-8 |y| for bf16 outputs). */
+TB_API tb_status_t tb_moe(const tb_moe_t *layer, const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
+                          int64_t T, int k, void *y, tb_dtype_t y_dtype, int64_t ldy, void *workspace,
+                          size_t workspace_bytes, tb_stream_t stream);
 
 /* Size of the fixed device scratch behind tb_gemv_noalloc (4 MiB). */
 #define TB_NOALLOC_SCRATCH_BYTES (4u << 20)

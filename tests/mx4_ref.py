@@ -60,3 +60,69 @@ def random_mx4(N, K, rng, lo=110, hi=130):
 def to_gpu(codes, scale_bytes, dev="cuda:0"):
     N, K = codes.shape
     return (torch.from_numpy(pack(codes)).to(dev), torch.from_numpy(tiles(scale_bytes, N, K)).to(dev))
+
+
+# ---- the expert layer -----------------------------------------------------------------
+TERNARY, INT2, INT3, MX4 = 0, 1, 2, 4
+
+
+def pack_codes(codes, grid):
+    """Codewords [N][K] -> the packed bytes of the scalar grids."""
+    N, K = codes.shape
+    if grid == INT3:
+        u = (codes + 4).astype(np.uint32).reshape(N, K // 32, 16, 2)
+        m = np.arange(16, dtype=np.uint32)
+        planes = [(((u[..., 0] >> p) & 1) << m | ((u[..., 1] >> p) & 1) << (m + 16)).sum(-1, dtype=np.uint32)
+                  for p in range(3)]
+        return np.stack(planes, -1).reshape(N, -1)
+    u = (codes + 2).astype(np.uint32).reshape(N, K // 16, 8, 2)
+    m = 2 * np.arange(8, dtype=np.uint32)
+    return (u[..., 0] << m | u[..., 1] << (m + 16)).sum(-1, dtype=np.uint32)
+
+
+def random_matrix(N, K, grid, rng, dev="cuda:0", std=0.02):
+    """(float64 weights on `dev`, (packed, scales, grid) for the library)."""
+    if grid == MX4:
+        c, b = random_mx4(N, K, rng, 118, 123)
+        p, s = to_gpu(c, b, dev)
+        return torch.from_numpy(values(c, b)).to(dev), (p, s, grid)
+    lo, hi = {TERNARY: (-1, 1), INT2: (-2, 1), INT3: (-4, 3)}[grid]
+    c = rng.integers(lo, hi + 1, (N, K))
+    s = torch.from_numpy(np.abs(rng.standard_normal((N, K // 128))) * std + 1e-3).to(torch.bfloat16).to(dev)
+    p = torch.from_numpy(pack_codes(c, grid).view(np.uint8).reshape(-1)).to(dev)
+    w = torch.from_numpy(c).to(dev).double() * s.double().repeat_interleave(128, 1)
+    return w, (p, s, grid)
+
+
+def moe(wg, wu, wd, E, x, ids, weights):
+    """(y, bound) in float64: wg, wu [E*I][H], wd [E*H][I], x [T][H], ids / weights [T][k]; the bound is that of
+    include/tb.h for fp32 outputs."""
+    T, H = x.shape
+    I, k, u = wd.shape[1], ids.shape[1], 2.0 ** -24
+    x, weights = x.double(), weights.double()
+    y, tol = torch.zeros_like(x), torch.zeros_like(x)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if not 0 <= e < E:
+                continue
+            G, U, D = wg[e * I:(e + 1) * I], wu[e * I:(e + 1) * I], wd[e * H:(e + 1) * H]
+            g, up = G @ x[t], U @ x[t]
+            dg, du = ((H / 8 + 16) * u * (m.abs() @ x[t].abs()) for m in (G, U))
+            s = g / (1 + torch.exp(-g))
+            h = s * up
+            dh = 1.1 * dg * (up.abs() + du) + s.abs() * du + 2.0 ** -16 * h.abs()
+            y[t] += weights[t, j] * (D @ h)
+            tol[t] += weights[t, j].abs() * (D.abs() @ dh + (I / 4 + k + 16) * u * (D.abs() @ (h.abs() + dh)))
+    return y, tol
+
+
+def route(x, router, k, renorm):
+    """(ids, weights, all logits) in float64."""
+    l = x.double() @ router.double().T
+    key = torch.nan_to_num(l, nan=-np.inf, posinf=np.inf, neginf=-np.inf)
+    ids = torch.sort(key, dim=-1, descending=True, stable=True)[1][:, :k]
+    top = l.gather(1, ids)
+    p = torch.exp(top - top[:, :1])
+    z = p.sum(-1, keepdim=True) if renorm else torch.exp(l - top[:, :1]).sum(-1, keepdim=True)
+    return ids, p / z, l

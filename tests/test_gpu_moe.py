@@ -1,0 +1,277 @@
+"""The router and the expert layer on the GPU against 64-bit
+implementations (tests/mx4_ref.py).  Expert ids have to be equal; weights
+within (E + 16) 2^-22 of their value (E terms of fp32 sums and an
+exponential); layer outputs within the bound of include/tb.h, which the
+reference computes from its own 64-bit values."""
+import numpy as np
+import pytest
+import torch
+
+from decode_gemv_tb_b200 import tb
+from tests import mx4_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    tb.load()
+
+
+# ---- router -----------------------------------------------------------------------------
+def check_route(x, router, k, renorm, extra=0):
+    T, H = x.shape
+    E = router.shape[0]
+    xb = torch.full((T, H + extra), 5.0, dtype=torch.bfloat16, device=DEV)
+    xb[:, :H] = x
+    ids, w = tb.tb_moe_route(xb[:, :H], router.to(DEV), k, renormalize=renorm)
+    rid, rw, _ = R.route(x.to(DEV), router.to(DEV), k, renorm)
+    assert torch.equal(ids.long(), rid), (T, E, H, k)
+    assert torch.all((w.double() - rw).abs() <= (E + 16) * 2.0 ** -22 * rw)
+    return ids, w
+
+
+@pytest.mark.parametrize("T,E,H,k", [(1, 1, 8, 1), (1, 128, 2048, 8), (5, 60, 1000, 4), (16, 8, 64, 8), (17, 200, 264, 3),
+                                     (32, 512, 512, 16), (33, 16, 4096, 2), (64, 256, 4096, 8), (101, 33, 128, 16),
+                                     (3, 130, 56000, 5)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route(T, E, H, k, renorm):
+    g = torch.Generator().manual_seed(T * 1000 + E)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16)
+    r = (torch.randn((E, H), generator=g) / H ** 0.5).to(torch.bfloat16)
+    check_route(x, r, k, renorm, extra=8 if T % 2 else 0)
+
+
+def test_route_ties_take_the_lower_index():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((7, 256), generator=g).to(torch.bfloat16)
+    base = torch.randn((5, 256), generator=g).to(torch.bfloat16)
+    r = base[torch.tensor([4, 1, 1, 0, 3, 4, 2, 0, 1, 3, 2, 2])]
+    check_route(x, r, 9, True)
+    ids, w = check_route(x, torch.zeros(300, 256, dtype=torch.bfloat16), 4, True)  # every logit is 0
+    assert torch.equal(ids.cpu(), torch.arange(4, dtype=torch.int32).repeat(7, 1)) and torch.all(w == 0.25)
+    signs = torch.zeros(4, 256, dtype=torch.bfloat16)
+    signs[0], signs[2] = -0.0, -0.0  # zeros of both signs are equal
+    ids, _ = check_route(x.abs(), signs, 4, False)
+    assert torch.equal(ids.cpu(), torch.arange(4, dtype=torch.int32).repeat(7, 1))
+
+
+def test_route_order_beyond_fp32():
+    """Logits that agree in fp32 and differ in their 30th bit; subnormal weights decide among equals."""
+    H = 64
+    r = torch.zeros(6, H)
+    r[:, 0] = 1024.0
+    for e, v in enumerate((0.0, 1.0, -1.0, 3.0, 2.0, 0.5)):
+        r[e, 1] = v * 2.0 ** -20
+    r = r.to(torch.bfloat16)
+    x = torch.zeros(2, H)
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    ids, _ = check_route(x.to(torch.bfloat16), r, 6, True)
+    assert ids[0].tolist() == [3, 4, 1, 5, 0, 2]
+    tiny = torch.zeros(4, H)
+    for e, v in enumerate((1, 3, 0, 2)):
+        tiny[e, 5] = v * 2.0 ** -133
+    x2 = torch.full((1, H), 2.0)
+    ids, _ = check_route(x2.to(torch.bfloat16), tiny.to(torch.bfloat16), 4, False)
+    assert ids[0].tolist() == [1, 3, 0, 2]
+
+
+def test_route_non_finite_token_stays_in_its_row():
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn((6, 128), generator=g).to(torch.bfloat16)
+    r = torch.randn((20, 128), generator=g).to(torch.bfloat16)
+    want, ww = tb.tb_moe_route(x.to(DEV), r.to(DEV), 4)
+    x[2, 7] = float("nan")
+    ids, w = tb.tb_moe_route(x.to(DEV), r.to(DEV), 4)
+    keep = torch.tensor([0, 1, 3, 4, 5], device=DEV)
+    assert torch.equal(ids[keep], want[keep]) and torch.equal(w[keep], ww[keep])
+    assert ids[2].tolist() == [0, 1, 2, 3] and torch.isnan(w[2]).all()
+
+
+# ---- experts ------------------------------------------------------------------------------
+def make_layer(E, H, I, grids, seed):
+    rng = np.random.default_rng(seed)
+    wg, g = R.random_matrix(E * I, H, grids[0], rng)
+    wu, u = R.random_matrix(E * I, H, grids[1], rng)
+    wd, d = R.random_matrix(E * H, I, grids[2], rng)
+    return (wg, wu, wd), tb.moe_layer(g, u, d, E, H, I)
+
+
+def check_moe(mats, layer, x, ids, weights, dt=torch.float32, extra=0, ws=None):
+    T, H = x.shape
+    E = layer.desc.E
+    xb = torch.full((T, H + 8 * extra), 5.0, dtype=torch.bfloat16, device=DEV)
+    xb[:, :H] = x
+    y = torch.full((T, H + extra), 7.0, dtype=dt, device=DEV)
+    tb.tb_moe(layer, xb[:, :H], ids.to(DEV), weights.to(DEV), y=y[:, :H], ws=ws)
+    torch.cuda.synchronize()
+    assert torch.all(y[:, H:] == 7.0)
+    ref, tol = R.moe(*mats, E, x.to(DEV), ids, weights.to(DEV))
+    if dt == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * ref.abs()
+    err = (y[:, :H].double() - ref).abs()
+    assert torch.all(err <= tol), (T, E, (err / tol.clamp(min=1e-300)).max().item())
+    return y
+
+
+def draw_ids(T, k, E, g):
+    return torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+
+
+GRIDS = [(0, 0, 0), (2, 2, 2), (4, 4, 4), (1, 2, 4), (4, 0, 2), (2, 4, 1)]
+
+
+@pytest.mark.parametrize("grids", GRIDS)
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 256, 128), (1, 4, 4, 128, 640), (3, 16, 8, 384, 256), (13, 5, 3, 512, 384),
+                                       (64, 6, 2, 128, 128)])
+def test_moe(T, E, k, H, I, grids):
+    g = torch.Generator().manual_seed(T + E)
+    mats, layer = make_layer(E, H, I, grids, T * 100 + E)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16)
+    ids = draw_ids(T, k, E, g)
+    w = torch.rand((T, k), generator=g)
+    check_moe(mats, layer, x, ids, w, torch.bfloat16 if T == 3 else torch.float32, extra=T % 2)
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 8, 9, 16, 17, 63, 64])
+def test_moe_one_expert_takes_every_token(T):
+    """Blocks of up to four, of up to eight and several blocks of one expert."""
+    g = torch.Generator().manual_seed(T)
+    mats, layer = make_layer(1, 256, 256, (0, 4, 2), 7)
+    x = torch.randn((T, 256), generator=g).to(torch.bfloat16)
+    check_moe(mats, layer, x, torch.zeros(T, 1, dtype=torch.int32), torch.randn((T, 1), generator=g))
+
+
+def test_moe_empty_and_odd_ids():
+    """Tokens without experts give 0; ids outside the range are skipped; a repeated id counts every time."""
+    g = torch.Generator().manual_seed(4)
+    mats, layer = make_layer(6, 256, 128, (1, 1, 1), 8)
+    x = torch.randn((7, 256), generator=g).to(torch.bfloat16)
+    ids = draw_ids(7, 4, 6, g)
+    ids[0] = -1
+    ids[1] = torch.tensor([6, 2 ** 31 - 1, -(2 ** 31), 512])
+    ids[2] = torch.tensor([3, 3, 3, 3])
+    ids[3] = torch.tensor([2, -1, 2, 5])
+    ids[6, 1:] = -1
+    w = torch.rand((7, 4), generator=g)
+    y = check_moe(mats, layer, x, ids, w)
+    assert torch.all(y[:2] == 0)
+    y = check_moe(mats, layer, x, torch.full_like(ids, -1), w, torch.bfloat16)
+    assert torch.all(y == 0)
+
+
+def test_moe_many_experts_and_the_largest_batch():
+    g = torch.Generator().manual_seed(5)
+    mats, layer = make_layer(512, 128, 128, (0, 1, 4), 9)
+    x = torch.randn((64, 128), generator=g).to(torch.bfloat16)
+    check_moe(mats, layer, x, draw_ids(64, 16, 512, g), torch.rand((64, 16), generator=g))
+
+
+@pytest.mark.parametrize("grids", [(0, 2, 4), (4, 4, 2)])
+def test_moe_decode_sizes(grids):
+    """Long rows (K split between the warps of a CTA at one token, and not at many)."""
+    g = torch.Generator().manual_seed(6)
+    mats, layer = make_layer(8, 2048, 1408, grids, 10)
+    for T, k in ((1, 2), (2, 8), (24, 4)):
+        x = torch.randn((T, 2048), generator=g).to(torch.bfloat16)
+        check_moe(mats, layer, x, draw_ids(T, k, 8, g), torch.rand((T, k), generator=g))
+
+
+def test_moe_outlier_activations():
+    g = torch.Generator().manual_seed(7)
+    mats, layer = make_layer(4, 256, 128, (2, 2, 2), 11)
+    x = torch.randn((3, 256), generator=g)
+    x[:, 17], x[1, 90] = 2.0 ** 12, -2.0 ** 14
+    check_moe(mats, layer, x.to(torch.bfloat16), draw_ids(3, 2, 4, g), torch.rand((3, 2), generator=g))
+
+
+def test_moe_repeats_bitwise_shares_a_workspace_and_replays():
+    """Same bits from call to call, on another stream and in a graph; a workspace shared with a dense product keeps
+    that product's control words zero."""
+    g = torch.Generator().manual_seed(8)
+    mats, layer = make_layer(16, 512, 256, (0, 1, 2), 12)
+    x = torch.randn((9, 512), generator=g).to(torch.bfloat16).to(DEV)
+    ids, w = draw_ids(9, 4, 16, g).to(DEV), torch.rand((9, 4), generator=g).to(DEV)
+    wd, dense = R.random_matrix(8192, 4096, R.INT2, np.random.default_rng(13))
+    xd = torch.randn(4096, generator=g).to(torch.bfloat16).to(DEV)
+    ws = tb.workspace(max(tb.moe_workspace_bytes(layer, 9, 4), tb.workspace_bytes(1, 8192, 4096)), DEV)
+    y0 = tb.tb_gemv(dense[0], dense[2], dense[1], xd, 8192, 4096, ws=ws)
+    first = tb.tb_moe(layer, x, ids, w, ws=ws)
+    for _ in range(3):
+        assert torch.equal(first, tb.tb_moe(layer, x, ids, w, ws=ws))
+        assert torch.equal(y0, tb.tb_gemv(dense[0], dense[2], dense[1], xd, 8192, 4096, ws=ws))
+    assert tb.sync_status() == 0
+    y = torch.zeros_like(first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        tb.tb_moe(layer, x, ids, w, y=y, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tb.tb_moe(layer, x, ids, w, y=y, ws=ws)
+    other = ids.clone()
+    y.zero_()
+    graph.replay()
+    assert torch.equal(first, y)
+    ids[0] = -1  # a replay reads the ids of its own time
+    graph.replay()
+    assert torch.all(y[0] == 0) and torch.equal(first[1:], y[1:])
+    ids.copy_(other)
+    graph.replay()
+    assert torch.equal(first, y)
+
+
+def test_moe_batch_rows_are_independent():
+    """A token's result does not depend on its neighbours beyond rounding; with the same grouping it is the same."""
+    g = torch.Generator().manual_seed(9)
+    mats, layer = make_layer(8, 256, 256, (0, 2, 4), 14)
+    x = torch.randn((6, 256), generator=g).to(torch.bfloat16)
+    ids, w = draw_ids(6, 3, 8, g), torch.rand((6, 3), generator=g)
+    x2 = x.clone()
+    x2[3] = float("nan")
+    y = check_moe(mats, layer, x, ids, w)
+    y2 = tb.tb_moe(layer, x2.to(DEV), ids.to(DEV), w.to(DEV))
+    keep = torch.tensor([0, 1, 2, 4, 5], device=DEV)
+    assert torch.equal(y[keep, :256], y2[keep]) and torch.isnan(y2[3]).all()
+
+
+def test_routed_layer_run():
+    """The operators as a decoder uses them: weights quantised and packed by the library (scalar grid for gate and up,
+    4-bit floats for down), tokens routed, experts applied -- in one stream, captured and replayed."""
+    E, H, I, T, k = 12, 512, 384, 10, 3
+    g = torch.Generator().manual_seed(15)
+    wg, wu = (torch.randn((E * I, H), generator=g).mul_(0.05).to(torch.bfloat16).to(DEV) for _ in range(2))
+    wd = torch.randn((E * H, I), generator=g).mul_(0.05).to(torch.bfloat16).to(DEV)
+    sg, su = tb.tb_scales_absmax(wg, tb.INT3), tb.tb_scales_absmax(wu, tb.INT2)
+    pg, pu = tb.tb_pack(wg, tb.INT3, sg), tb.tb_pack(wu, tb.INT2, su)
+    cd, td = tb.tb_mx4_quantize(wd)
+    layer = tb.moe_layer((pg, sg, tb.INT3), (pu, su, tb.INT2), (cd, td, tb.MX4), E, H, I)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).to(DEV)
+    r = torch.randn((E, H), generator=g).mul_(H ** -0.5).to(torch.bfloat16).to(DEV)
+    ws = tb.workspace(tb.moe_workspace_bytes(layer, T, k), DEV)
+    ids, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    y = torch.empty((T, H), device=DEV)
+
+    def step():
+        tb.tb_moe_route(x, r, k, ids=ids, weights=w)
+        tb.tb_moe(layer, x, ids, w, y=y, ws=ws)
+    step()
+    first = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(first, y) and tb.sync_status() == 0
+    G = tb.tb_unpack(pg, tb.INT3, E * I, H).double() * sg.double().repeat_interleave(128, 1)
+    U = tb.tb_unpack(pu, tb.INT2, E * I, H).double() * su.double().repeat_interleave(128, 1)
+    D = tb.tb_mx4_dequantize(cd, td, E * H, I, out_dtype=torch.float32).double()
+    rid, rw, _ = R.route(x, r, k, True)
+    assert torch.equal(ids.long(), rid)
+    ref, tol = R.moe(G, U, D, E, x, ids, w)
+    assert torch.all((y.double() - ref).abs() <= tol)
