@@ -3,26 +3,26 @@
 //
 //     h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   y[t] = sum_j w[t,j] Wd[ids[t,j]] h[t,ids[t,j]]
 //
-// Every expert that some token takes is read once per eight of its tokens:
+// Every expert that some token takes is read once per sixteen of its tokens:
 // with few tokens the layer is bound by the bytes of the experts it touches
-// (and, from there, by decoding them).
+// and by decoding them.
 //
 // Both kernels group the (token, choice) pairs by expert themselves, in
 // shared memory (a 64-bit token mask per expert, a prefix sum over the
 // experts): at most 1024 pairs, no extra launch, no atomics on floats.  A
-// block is an expert with up to eight of its tokens -- the MMA's columns.
+// block is an expert with up to sixteen of its tokens.
 //
 // The products run on mma.sync m16n8k16: 16 weight rows decoded in registers
-// to bf16 (tb_device.cuh; exact, 4-bit codes with their power-of-two scale
-// too), the tokens' activations as B fragments read as they are.  A lane of a
-// quad owns 32 consecutive k of every 128-group in both operands, so a row's
-// group is one 8-, 12- or 16-byte read per lane and no code is moved between
-// lanes.  Weights stream through a private cp.async ring per warp.
+// to bf16 (exact, 4-bit codes with their power-of-two scale too), the
+// activations as B fragments read as they are, in sets of eight columns that
+// share the decode.  A lane of a quad owns 32 consecutive k of every
+// 128-group in both operands, so a row's group is one 8-, 12- or 16-byte read
+// per lane, free of bank conflicts, and no code moves between lanes.  Weights
+// stream through a private cp.async ring per warp, a group per stage.
 //
 // h is kept as two bf16 (high and low part, 16 significant bits together), so
 // that the second product sees it as exactly as the fp32 sums it came from
-// are worth; with at most four tokens both parts share one MMA (columns 0-3
-// and 4-7).
+// are worth: the parts of a token are neighbouring columns of a set.
 //
 // k_moe_up: a unit is (block, 16 rows of gate and of up); S warps of a CTA
 // split K when units are few.  k_moe_down: a cluster of C CTAs holds 64 rows
@@ -55,25 +55,25 @@ struct MoeArgs {
     int64_t ldx, ldy;
     int32_t T, k, E, H, I, ydt;
     int32_t S, C;
+    int32_t hperm;  // h in the order of the 4-bit decode's pairs
 };
 
 namespace {
 
 constexpr int kMoeWarps = 4;
 constexpr int kMoeThreads = kMoeWarps * 32;
-constexpr int kCG = 2;     // 128-groups per step
-constexpr int kStages = 3;
+constexpr int kStages = 4;
+constexpr int kBlockTokens = 16;
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxK;
-constexpr int kScaleBytes = 128;  // per matrix and step: 16 rows x 8 bytes
+constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / kBlockTokens;
 
-// packed bytes of a row's group, and of a step's row in shared memory (padded: a quad-row read of eight rows
-// touches every bank once)
+// packed bytes of a row's group (also its stride in shared memory: with 32, 48 and 64 bytes the reads of eight rows
+// by a quad each touch every bank once); a stage's bytes: 16 rows and their scale words
 __host__ __device__ constexpr int group_bytes(int kind) { return kind == 0 ? 32 : (kind == 1 ? 48 : 64); }
-__host__ __device__ constexpr int row_stride(int kind) { return kind == 0 ? 96 : (kind == 1 ? 112 : 192); }
-__host__ __device__ constexpr int mat_bytes(int kind) { return 16 * row_stride(kind) + kScaleBytes; }
+__host__ __device__ constexpr int mat_bytes(int kind) { return 16 * group_bytes(kind) + 64; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // 4 bytes, of which the first n (2 or 4) are read
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t n) {
@@ -97,11 +97,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -130,135 +125,160 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-
-// byte permute whose selector nibbles replicate a byte's sign where their top bit is set
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t d;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
     return d;
 }
-// Eight 4-bit codes (nibble j: code j) as four bf16 pairs in order, times the scale pair s: the codes' magnitudes
-// index the two bytes of the bf16 values in a byte permute, the sign bits follow as bit 7 of the high bytes.
-__device__ __forceinline__ void decode_mx4(uint32_t w, uint32_t s, uint32_t (&r)[4]) {
-    constexpr uint32_t kHi0 = 0x3F3F3F00u, kHi1 = 0x40404040u;  // 0 .5 1 1.5 | 2 3 4 6
-    constexpr uint32_t kLo0 = 0xC0800000u, kLo1 = 0xC0804000u;
-    const uint32_t m = w & 0x77777777u;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const uint32_t sel = p ? m >> 16 : m, raw = p ? w >> 16 : w;
-        // a byte with its top bit set, replicated where the code's sign bit is: 0xFF, else 0x80
-        const uint32_t sg = prmt(0x80808080u, 0x80808080u, raw) << 1;
-        const uint32_t hi = and_or(sg, 0x80808080u, prmt(kHi0, kHi1, sel));
-        const uint32_t lo = prmt(kLo0, kLo1, sel);
-        r[2 * p] = mul_bf16x2(prmt(lo, hi, 0x5140), s);
-        r[2 * p + 1] = mul_bf16x2(prmt(lo, hi, 0x7362), s);
-    }
+
+// Eight 4-bit codes (nibble j: code j) as the bf16 pairs (0,4), (1,5), (2,6), (3,7), times f 2^-126: a code's
+// exponent and mantissa bits put at the bottom of a bf16's exponent and the top of its mantissa are its magnitude
+// times 2^-126 (both formats agree below their normal range), one multiplication by 2^a + 2^b moves them and the
+// sign of two codes to their places.
+__device__ __forceinline__ void decode_mx4(uint32_t w, uint32_t f, uint32_t (&r)[4]) {
+    const uint32_t w8 = w >> 8;
+    r[0] = mul_bf16x2(((w & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f);
+    r[1] = mul_bf16x2(((w & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f);
+    r[2] = mul_bf16x2(((w8 & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f);
+    r[3] = mul_bf16x2(((w8 & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f);
 }
-// 2^(byte - 127) as a bf16 pair: below the normal range at 0, no number at 255
-__device__ __forceinline__ uint32_t mx4_scale_pair(uint32_t byte) {
-    const uint32_t b = byte == 0 ? 0x0040u : (byte == 255 ? 0x7FC0u : byte << 7);
-    return b | (b << 16);
+// eight consecutive activations (four pairs) in the order of those pairs
+__device__ __forceinline__ void pair_up(uint32_t (&x)[16], const uint32_t (&v)[16]) {
+#pragma unroll
+    for (int q = 0; q < 16; q += 4) {
+        x[q] = prmt(v[q], v[q + 2], 0x5410);
+        x[q + 1] = prmt(v[q], v[q + 2], 0x7632);
+        x[q + 2] = prmt(v[q + 1], v[q + 3], 0x5410);
+        x[q + 3] = prmt(v[q + 1], v[q + 3], 0x7632);
+    }
 }
 
-// One 128-group of 16 rows times the columns in xf (and, with TWO, in xg): acc += s W x.  `row`: shared address of
-// row lane/4 of the group, `sc`: of its scales (row r's are 8 r bytes on).
-template <bool TWO>
-__device__ __forceinline__ void group_product(int kind, uint32_t row, uint32_t sc, int t, const uint32_t (&xf)[16],
-                                              const uint32_t (&xg)[16], float (&acc)[4]) {
-    if (kind == 2) {
-        const uint4 a = lds128(row + 16 * t), b = lds128(row + 8 * row_stride(2) + 16 * t);
-        const uint32_t sa = mx4_scale_pair(lds8(sc + t)), sb = mx4_scale_pair(lds8(sc + 64 + t));
-        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t ra[4], rb[4];
-            decode_mx4(wa[i], sa, ra);
-            decode_mx4(wb[i], sb, rb);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mma_bf16(acc, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xf[4 * i + 2 * j],
-                         xf[4 * i + 2 * j + 1]);
-                if (TWO)
-                    mma_bf16(acc, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xg[4 * i + 2 * j],
-                             xg[4 * i + 2 * j + 1]);
-            }
-        }
-        return;
+template <int NS, bool BIG>
+__device__ __forceinline__ void mx4_product(uint32_t row, int t, uint32_t ba, uint32_t bb,
+                                            const uint32_t (&x)[NS][16], float (&acc)[NS][4]) {
+    const uint4 a = lds128(row + 16 * t), b = lds128(row + 8 * group_bytes(2) + 16 * t);
+    const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+    // 2^(byte - 1) as a pair; above 2^127 in two factors; 255 is no number
+    const uint32_t fa = ((BIG ? min(ba, 128u) : ba) + 126u) * 0x00800080u;
+    const uint32_t fb = ((BIG ? min(bb, 128u) : bb) + 126u) * 0x00800080u;
+    uint32_t ga = 0, gb = 0;
+    if (BIG) {
+        ga = ba == 255u ? 0x7FC07FC0u : (max(ba, 128u) - 1u) * 0x00800080u;
+        gb = bb == 255u ? 0x7FC07FC0u : (max(bb, 128u) - 1u) * 0x00800080u;
     }
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    if (kind == 0) {
-        const uint2 a = lds64(row + 8 * t), b = lds64(row + 8 * row_stride(0) + 8 * t);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t ra[8], rb[8];
-            decode2_signed<2>(i ? a.y : a.x, ra);
-            decode2_signed<2>(i ? b.y : b.x, rb);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t ra[4], rb[4];
+        decode_mx4(wa[i], fa, ra);
+        decode_mx4(wb[i], fb, rb);
+        if (BIG) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                mma_bf16(d, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xf[8 * i + 2 * j],
-                         xf[8 * i + 2 * j + 1]);
-                if (TWO)
-                    mma_bf16(d, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xg[8 * i + 2 * j],
-                             xg[8 * i + 2 * j + 1]);
+                ra[j] = mul_bf16x2(ra[j], ga);
+                rb[j] = mul_bf16x2(rb[j], gb);
             }
         }
-    } else {
-        uint32_t ra[16], rb[16];
-        const uint32_t ar = row + 12 * t, br = ar + 8 * row_stride(1);
-        decode3_signed(lds32(ar), lds32(ar + 4), lds32(ar + 8), ra);
-        decode3_signed(lds32(br), lds32(br + 4), lds32(br + 8), rb);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            mma_bf16(d, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xf[2 * j], xf[2 * j + 1]);
-            if (TWO) mma_bf16(d, ra[2 * j], rb[2 * j], ra[2 * j + 1], rb[2 * j + 1], xg[2 * j], xg[2 * j + 1]);
-        }
+        for (int j = 0; j < 4; j += 2)
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+                mma_bf16(acc[n], ra[j], rb[j], ra[j + 1], rb[j + 1], x[n][4 * i + j], x[n][4 * i + j + 1]);
     }
-    const float s0 = bf16_bits_to_float(lds16(sc)), s1 = bf16_bits_to_float(lds16(sc + 64));
-    acc[0] = fmaf(s0, d[0], acc[0]);
-    acc[1] = fmaf(s0, d[1], acc[1]);
-    acc[2] = fmaf(s1, d[2], acc[2]);
-    acc[3] = fmaf(s1, d[3], acc[3]);
 }
 
-// Requests rows row0 .. row0 + 15, groups g .. g + n - 1 (n = 1, 2) of a matrix into a stage.
-__device__ __forceinline__ void load_step(const MoeMat& m, int64_t row0, int g, int n, uint32_t dst, int lane) {
-    const int gb = group_bytes(m.kind), rs = row_stride(m.kind), cpr = kCG * gb / 16;  // 16-byte pieces of a row
-    const uint8_t* src = m.packed + row0 * m.rb + (int64_t)g * gb;
-    for (int c = lane; c < 16 * cpr; c += 32) {
-        const int r = c / cpr, o = (c - r * cpr) * 16;
-        if (o < n * gb) cp16(dst + r * rs + o, src + r * m.rb + o);
-    }
-    const uint32_t sd = dst + 16 * rs;
-    if (m.kind == 2) {  // a word per row and group
-        const int r = lane >> 1, i = lane & 1;
-        const int64_t row = row0 + r;
-        if (i < n)
-            cp4(sd + r * 8 + i * 4, m.scales + (((row >> 7) * m.G + g + i) * 128 + (row & 31) * 4 + ((row >> 5) & 3)) * 4,
-                4);
-    } else if (lane < 16) {  // two bytes per row and group: one or two aligned words
-        const int64_t at = (row0 + lane) * m.G + g;
-        const bool odd = (at & 1) != 0;
-        cp4(sd + lane * 8, m.scales + (at & ~(int64_t)1) * 2, odd || n == 2 ? 4 : 2);
-        if (odd && n == 2) cp4(sd + lane * 8 + 4, m.scales + (at + 1) * 2, 2);
+// One 128-group of 16 rows times NS sets of eight columns: acc += s W x.  `row`: shared address of row lane/4 of the
+// group, `sc`: of its scale word, `odd`: the scale is the word's upper half.
+template <int KIND, int NS>
+__device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool odd, int t, const uint32_t (&x)[NS][16],
+                                              float (&acc)[NS][4]) {
+    if constexpr (KIND == 2) {
+        const uint32_t ba = lds8(sc + t), bb = lds8(sc + 32 + t);
+        if (__any_sync(0xffffffffu, max(ba, bb) > 128u)) mx4_product<NS, true>(row, t, ba, bb, x, acc);
+        else mx4_product<NS, false>(row, t, ba, bb, x, acc);
+    } else {
+        float d[NS][4];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
+        if constexpr (KIND == 0) {
+            const uint2 a = lds64(row + 8 * t), b = lds64(row + 8 * group_bytes(0) + 8 * t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t ra[8], rb[8];
+                decode2_signed<2>(i ? a.y : a.x, ra);
+                decode2_signed<2>(i ? b.y : b.x, rb);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        mma_bf16(d[n], ra[j], rb[j], ra[j + 1], rb[j + 1], x[n][8 * i + j], x[n][8 * i + j + 1]);
+            }
+        } else {
+            uint32_t ra[16], rb[16];
+            const uint32_t ar = row + 12 * t, br = ar + 8 * group_bytes(1);
+            decode3_signed(lds32(ar), lds32(ar + 4), lds32(ar + 8), ra);
+            decode3_signed(lds32(br), lds32(br + 4), lds32(br + 8), rb);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    mma_bf16(d[n], ra[j], rb[j], ra[j + 1], rb[j + 1], x[n][j], x[n][j + 1]);
+        }
+        const uint32_t w0 = lds32(sc), w1 = lds32(sc + 32);
+        const float s0 = __uint_as_float(odd ? w0 & 0xFFFF0000u : w0 << 16);
+        const float s1 = __uint_as_float(odd ? w1 & 0xFFFF0000u : w1 << 16);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
+            acc[n][1] = fmaf(s0, d[n][1], acc[n][1]);
+            acc[n][2] = fmaf(s1, d[n][2], acc[n][2]);
+            acc[n][3] = fmaf(s1, d[n][3], acc[n][3]);
+        }
     }
 }
-// shared address of the scales of group g + i (i = 0, 1) of row `r` of a stage whose first group is g
-__device__ __forceinline__ uint32_t scale_at(const MoeMat& m, int64_t row0, int g, int i, uint32_t dst, int r) {
-    const uint32_t sd = dst + 16 * row_stride(m.kind) + r * 8;
-    if (m.kind == 2) return sd + i * 4;
-    return sd + ((uint32_t)(((row0 + r) * m.G + g) & 1) + i) * 2;
+
+// Requests group g of rows row0 .. row0 + 15 into a stage; lane_off: the lane's 16-byte pieces of 16 rows (their
+// offsets from the first row's group).
+template <int KIND>
+__device__ __forceinline__ void piece_offsets(const MoeMat& m, int lane, uint32_t (&off)[2]) {
+    constexpr int P = group_bytes(KIND) / 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = lane + 32 * i;
+        off[i] = (uint32_t)((c / P) * m.rb + (c % P) * 16);
+    }
+}
+template <int KIND>
+__device__ __forceinline__ void load_codes(const MoeMat& m, int64_t row0, int g, uint32_t dst, int lane,
+                                           const uint32_t (&off)[2]) {
+    const uint8_t* src = m.packed + row0 * m.rb + (int64_t)g * group_bytes(KIND);
+    cp16(dst + lane * 16, src + off[0]);
+    if (KIND == 2 || (KIND == 1 && lane < 16)) cp16(dst + (lane + 32) * 16, src + off[1]);
+}
+// the scale word of row row0 + i: two bytes (in an aligned word) or the four bytes of a 4-bit group
+template <int KIND>
+__device__ __forceinline__ void load_scale(const MoeMat& m, int64_t row0, int g, uint32_t dst, int i) {
+    const int64_t row = row0 + i;
+    if constexpr (KIND == 2) {
+        cp4(dst + 4 * i, m.scales + (((row >> 7) * m.G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3)) * 4, 4);
+    } else {
+        const int64_t at = row * m.G + g;
+        cp4(dst + 4 * i, m.scales + (at & ~(int64_t)1) * 2, (at & 1) ? 4 : 2);
+    }
 }
 
 // ---- the pairs grouped by expert ---------------------------------------------------
 struct MoeList {
     unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
-    uint16_t blk_expert[kMaxPairs];
-    uint16_t blk_slot[kMaxPairs];  // first slot of a block
-    uint8_t blk_count[kMaxPairs];
+    uint32_t blk[kMaxBlocks];                 // expert, first slot << 10, tokens << 20
     uint8_t slot_token[kMaxPairs];
     int scan[2][kMoeWarps];
     int blocks, slots;
 };
+__device__ __forceinline__ int blk_expert(uint32_t b) { return (int)(b & 1023u); }
+__device__ __forceinline__ int blk_slot(uint32_t b) { return (int)(b >> 10 & 1023u); }
+__device__ __forceinline__ int blk_count(uint32_t b) { return (int)(b >> 20); }
 
 __device__ void build_list(MoeList& L, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -274,7 +294,7 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
     for (int e = e0; e < e1; ++e) {
         const int c = __popcll(L.mask[e]);
         slots += c;
-        blocks += (c + 7) >> 3;
+        blocks += (c + kBlockTokens - 1) / kBlockTokens;
     }
     int s = slots, b = blocks;
 #pragma unroll
@@ -302,11 +322,9 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
     b -= blocks;
     for (int e = e0; e < e1; ++e) {
         unsigned long long m = L.mask[e];
-        for (int left = __popcll(m); left > 0; left -= 8) {
-            L.blk_expert[b] = (uint16_t)e;
-            L.blk_slot[b] = (uint16_t)s;
-            const int n = min(8, left);
-            L.blk_count[b++] = (uint8_t)n;
+        for (int left = __popcll(m); left > 0; left -= kBlockTokens) {
+            const int n = min(kBlockTokens, left);
+            L.blk[b++] = (uint32_t)e | (uint32_t)s << 10 | (uint32_t)n << 20;
             for (int i = 0; i < n; ++i) {
                 L.slot_token[s++] = (uint8_t)(__ffsll((long long)m) - 1);
                 m &= m - 1;
@@ -317,29 +335,29 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
 }
 
 // ---- gate and up -----------------------------------------------------------------------
-__global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ MoeArgs A) {
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeList L;
-    __shared__ float part[2][kMoeWarps][256];  // K split: partial sums of gate and up, two units deep
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const int gbytes = mat_bytes(A.gate.kind), stage = gbytes + mat_bytes(A.up.kind);
-    const uint32_t base = sm_addr(ring) + warp * kStages * stage;
-    pdl_wait();
-    build_list(L, A);
-    pdl_trigger();
-    const int S = A.S, s = warp % S, ui = warp / S, per = kMoeWarps / S;
-    const int tiles = A.I / 16, units = L.blocks * tiles;
-    const int g0 = A.gate.G * s / S, g1 = A.gate.G * (s + 1) / S, steps = (g1 - g0 + kCG - 1) / kCG;
-    const int ustep = (int)gridDim.x * per;
-    int pu = (int)blockIdx.x * per + ui, ps = 0, issued = 0;  // the next step to request
-    auto issue = [&]() {
+template <int KG, int KU>
+struct MoeUp {
+    static constexpr int kGate = 16 * group_bytes(KG), kUp = 16 * group_bytes(KU);
+    static constexpr int kStage = kGate + kUp + 128;  // codes of gate and up, their scale words
+    static constexpr int kRing = kMoeWarps * kStages * kStage;
+
+    const MoeArgs& A;
+    MoeList& L;
+    float* part;    // [2][warps][sets][256]: partial sums of gate and up, two units deep
+    uint32_t base;  // this warp's ring
+    int lane, warp, r, t, S, s, ui, g0, steps, tiles, units, ustep, sets;
+    int pu, ps, issued, used, flip;
+    uint32_t og[2], ou[2];
+
+    __device__ __forceinline__ void issue() {
         if (pu < units) {
-            const int blk = pu / tiles, tile = pu - blk * tiles, g = g0 + ps * kCG;
-            const int64_t row0 = (int64_t)L.blk_expert[blk] * A.I + tile * 16;
-            const uint32_t dst = base + (issued % kStages) * stage;
-            const int n = min(kCG, g1 - g);
-            load_step(A.gate, row0, g, n, dst, lane);
-            load_step(A.up, row0, g, n, dst + gbytes, lane);
+            const int blk = pu / tiles, tile = pu - blk * tiles, g = g0 + ps;
+            const int64_t row0 = (int64_t)blk_expert(L.blk[blk]) * A.I + tile * 16;
+            const uint32_t dst = base + (uint32_t)(issued % kStages) * kStage;
+            load_codes<KG>(A.gate, row0, g, dst, lane, og);
+            load_codes<KU>(A.up, row0, g, dst + kGate, lane, ou);
+            if (lane < 16) load_scale<KG>(A.gate, row0, g, dst + kGate + kUp, lane);
+            else load_scale<KU>(A.up, row0, g, dst + kGate + kUp + 64, lane - 16);
             if (++ps == steps) {
                 ps = 0;
                 pu += ustep;
@@ -347,74 +365,124 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
         }
         ++issued;
         cp_commit_group();
-    };
-    for (int i = 0; i < kStages - 1; ++i) issue();
-    int used = 0, flip = 0;
-    for (int u = (int)blockIdx.x * per + ui; u < units; u += ustep, flip ^= 1) {
-        const int blk = u / tiles, tile = u - blk * tiles, count = L.blk_count[blk], slot0 = L.blk_slot[blk];
-        const int64_t row0 = (int64_t)L.blk_expert[blk] * A.I + tile * 16;
-        const uint16_t* xr = A.x + (int64_t)(r < count ? L.slot_token[slot0 + r] : 0) * A.ldx + 32 * t;
-        float ag[4] = {0.f, 0.f, 0.f, 0.f}, au[4] = {0.f, 0.f, 0.f, 0.f};
+    }
+
+    template <int NS>
+    __device__ __forceinline__ void unit(uint32_t block, int tile) {
+        const int count = blk_count(block), slot0 = blk_slot(block);
+        const int64_t row0 = (int64_t)blk_expert(block) * A.I + tile * 16;
+        const uint16_t* xr[NS];
+        bool have[NS];
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            have[n] = 8 * n + r < count;
+            xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + g0 * 128 + 32 * t;
+        }
+        // parity of the scale's place in its word, for the first group
+        const int pg = (int)((row0 + r) * A.gate.G + g0) & 1;
+        float ag[NS][4], au[NS][4];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = 0.f;
         for (int st = 0; st < steps; ++st) {
+            uint32_t v[NS][16];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 u = have[n] ? ld_act_u4(xr[n] + st * 128 + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+                    v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                }
             cp_wait_groups<kStages - 2>();
             __syncwarp();
-            const int g = g0 + st * kCG, n = min(kCG, g1 - g);
-            const uint32_t src = base + (used % kStages) * stage;
+            const uint32_t src = base + (uint32_t)(used % kStages) * kStage;
+            const bool odd = ((pg + st) & 1) != 0;
+            uint32_t p[NS][16];
+            if constexpr (KG == 2 || KU == 2) {
 #pragma unroll
-            for (int i = 0; i < kCG; ++i) {
-                if (i >= n) break;
-                uint32_t xf[16];
-                if (r < count) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 v = ld_act_u4(xr + (int64_t)(g + i) * 128 + 8 * q);
-                        xf[4 * q] = v.x, xf[4 * q + 1] = v.y, xf[4 * q + 2] = v.z, xf[4 * q + 3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) xf[q] = 0u;
-                }
-                group_product<false>(A.gate.kind, src + r * row_stride(A.gate.kind) + i * group_bytes(A.gate.kind),
-                                     scale_at(A.gate, row0, g, i, src, r), t, xf, xf, ag);
-                group_product<false>(A.up.kind, src + gbytes + r * row_stride(A.up.kind) + i * group_bytes(A.up.kind),
-                                     scale_at(A.up, row0, g, i, src + gbytes, r), t, xf, xf, au);
+                for (int n = 0; n < NS; ++n) pair_up(p[n], v[n]);
             }
+            group_product<KG, NS>(src + r * group_bytes(KG), src + kGate + kUp + 4 * r, odd, t, KG == 2 ? p : v, ag);
+            group_product<KU, NS>(src + kGate + r * group_bytes(KU), src + kGate + kUp + 64 + 4 * r, odd, t,
+                                  KU == 2 ? p : v, au);
             ++used;
             __syncwarp();
             issue();
         }
         if (S > 1) {
-            float* p = part[flip][warp];
+            float* mine = part + ((flip * kMoeWarps + warp) * sets) * 256 + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i * 32 + lane] = ag[i];
-                p[128 + i * 32 + lane] = au[i];
-            }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + ui), "r"(S * 32) : "memory");
-            // warp s of the unit finishes registers i = s, s + S, ...
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i % S != s) continue;
-                float sg = 0.f, su = 0.f;
-                for (int w = 0; w < S; ++w) {
-                    sg += part[flip][ui * S + w][i * 32 + lane];
-                    su += part[flip][ui * S + w][128 + i * 32 + lane];
+                for (int i = 0; i < 4; ++i) {
+                    mine[n * 256 + i * 32] = ag[n][i];
+                    mine[n * 256 + 128 + i * 32] = au[n][i];
                 }
-                ag[i] = sg;
-                au[i] = su;
-            }
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + ui), "r"(S * 32) : "memory");
+            // warp s of the unit finishes registers s, s + S, ... of every set
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if ((i & (S - 1)) != s) continue;
+                    float sg = 0.f, su = 0.f;
+                    for (int w = 0; w < S; ++w) {
+                        const float* q = part + ((flip * kMoeWarps + ui * S + w) * sets + n) * 256 + i * 32 + lane;
+                        sg += q[0];
+                        su += q[128];
+                    }
+                    ag[n][i] = sg;
+                    au[n][i] = su;
+                }
+            flip ^= 1;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int col = 2 * t + (i & 1);
-            if ((S > 1 && i % S != s) || col >= count) continue;
-            const float h = ag[i] / (1.f + expf(-ag[i])) * au[i];
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-            const int64_t at = (int64_t)(slot0 + col) * A.I + tile * 16 + r + 8 * (i >> 1);
-            A.h_hi[at] = __bfloat16_as_ushort(hi);
-            const float rest = h - __bfloat162float(hi);  // no number where hi is infinite
-            A.h_lo[at] = fabsf(rest) < INFINITY ? __bfloat16_as_ushort(__float2bfloat16_rn(rest)) : (uint16_t)0;
-        }
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = 8 * n + 2 * t + (i & 1);
+                if ((i & (S - 1)) != s || col >= count) continue;
+                const float g = ag[n][i], h = g / (1.f + expf(-g)) * au[n][i];
+                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                const float rest = h - __bfloat162float(hi);  // no number where hi is infinite
+                int c = tile * 16 + r + 8 * (i >> 1);
+                if (A.hperm) c = (c & ~7) | (c & 3) << 1 | (c >> 2 & 1);
+                const int64_t at = (int64_t)(slot0 + col) * A.I + c;
+                A.h_hi[at] = __bfloat16_as_ushort(hi);
+                A.h_lo[at] = fabsf(rest) < INFINITY ? __bfloat16_as_ushort(__float2bfloat16_rn(rest)) : (uint16_t)0;
+            }
+    }
+};
+
+template <int KG, int KU>
+__global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ MoeArgs A) {
+    using Up = MoeUp<KG, KU>;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ MoeList L;
+    pdl_wait();
+    build_list(L, A);
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = A.S, per = kMoeWarps / S;
+    Up u{A, L, reinterpret_cast<float*>(ring + Up::kRing), sm_addr(ring) + (uint32_t)(warp * kStages * Up::kStage)};
+    u.lane = lane, u.warp = warp, u.r = lane >> 2, u.t = lane & 3;
+    u.S = S, u.s = warp & (S - 1), u.ui = warp / S;
+    u.g0 = A.gate.G * u.s / S;
+    u.steps = A.gate.G * (u.s + 1) / S - u.g0;
+    u.tiles = A.I / 16;
+    u.units = L.blocks * u.tiles;
+    u.ustep = (int)gridDim.x * per;
+    u.sets = A.T > 8 ? 2 : 1;
+    u.pu = (int)blockIdx.x * per + u.ui;
+    u.ps = u.issued = u.used = u.flip = 0;
+    piece_offsets<KG>(A.gate, lane, u.og);
+    piece_offsets<KU>(A.up, lane, u.ou);
+    for (int i = 0; i < kStages - 1; ++i) u.issue();
+    for (int v = (int)blockIdx.x * per + u.ui; v < u.units; v += u.ustep) {
+        const int blk = v / u.tiles;
+        const uint32_t block = L.blk[blk];
+        if (blk_count(block) > 8) u.template unit<2>(block, v - blk * u.tiles);
+        else u.template unit<1>(block, v - blk * u.tiles);
     }
     cp_wait_groups<0>();
 }
@@ -422,96 +490,124 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
 // ---- down and the weighted sum ------------------------------------------------------------
 constexpr int kDownRows = 16 * kMoeWarps;
 
-__global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant__ MoeArgs A) {
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeList L;
-    __shared__ float slot_w[kMaxPairs];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const int stage = mat_bytes(A.down.kind);
-    const uint32_t base = sm_addr(ring) + warp * kStages * stage;
-    float* sum = reinterpret_cast<float*>(ring + kMoeWarps * kStages * stage);  // [T][kDownRows]
-    const int C = A.C;
-    const int rank = C > 1 ? (int)cluster_rank() : 0;
-    const int tile = (int)blockIdx.x / C;
-    // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list(L, A);
-    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads)
-        for (int i = 0; i < L.blk_count[b]; ++i) {
-            const int slot = L.blk_slot[b] + i, tok = L.slot_token[slot];
-            float w = 0.f;  // a token may name an expert more than once
-            for (int j = 0; j < A.k; ++j)
-                if (A.ids[tok * A.k + j] == (int)L.blk_expert[b]) w += A.weights[tok * A.k + j];
-            slot_w[slot] = w;
-        }
-    for (int i = threadIdx.x; i < A.T * kDownRows; i += kMoeThreads) sum[i] = 0.f;
-    __syncthreads();
-    const int G = A.down.G, steps = (G + kCG - 1) / kCG, blocks = L.blocks;
-    const int64_t wrow = (int64_t)tile * kDownRows + warp * 16;
-    int pb = rank, ps = 0, issued = 0;
-    auto issue = [&]() {
+template <int KIND>
+struct MoeDown {
+    static constexpr int kStage = mat_bytes(KIND);
+    static constexpr int kRing = kMoeWarps * kStages * kStage;
+
+    const MoeArgs& A;
+    MoeList& L;
+    const float* slot_w;
+    float* sum;     // [T][kDownRows]
+    uint32_t base;  // this warp's ring
+    int lane, warp, r, t, G, blocks;
+    int64_t wrow;
+    int pb, ps, issued, used;
+    uint32_t off[2];
+
+    __device__ __forceinline__ void issue() {
         if (pb < blocks) {
-            const int g = ps * kCG;
-            load_step(A.down, (int64_t)L.blk_expert[pb] * A.H + wrow, g, min(kCG, G - g),
-                      base + (issued % kStages) * stage, lane);
-            if (++ps == steps) {
+            const int64_t row0 = (int64_t)blk_expert(L.blk[pb]) * A.H + wrow;
+            const uint32_t dst = base + (uint32_t)(issued % kStages) * kStage;
+            load_codes<KIND>(A.down, row0, ps, dst, lane, off);
+            if (lane < 16) load_scale<KIND>(A.down, row0, ps, dst + 16 * group_bytes(KIND), lane);
+            if (++ps == G) {
                 ps = 0;
-                pb += C;
+                pb += A.C;
             }
         }
         ++issued;
         cp_commit_group();
-    };
-    for (int i = 0; i < kStages - 1; ++i) issue();
-    pdl_wait();
-    int used = 0;
-    for (int blk = rank; blk < blocks; blk += C) {
-        const int count = L.blk_count[blk], slot0 = L.blk_slot[blk];
-        const int64_t row0 = (int64_t)L.blk_expert[blk] * A.H + wrow;
-        // with at most four tokens columns 4-7 hold the low parts of columns 0-3
-        const bool packed = count <= 4;
-        const int col = packed ? r & 3 : r;
-        const bool have = col < count;
-        const uint16_t* hp = (packed && r >= 4 ? A.h_lo : A.h_hi) + (int64_t)(slot0 + (have ? col : 0)) * A.I + 32 * t;
-        const uint16_t* lp = A.h_lo + (int64_t)(slot0 + (have ? col : 0)) * A.I + 32 * t;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int st = 0; st < steps; ++st) {
-            cp_wait_groups<kStages - 2>();
-            __syncwarp();
-            const int g = st * kCG, n = min(kCG, G - g);
-            const uint32_t src = base + (used % kStages) * stage;
+    }
+
+    // a set: the high and low parts of four tokens, in turn
+    template <int NS>
+    __device__ __forceinline__ void block(uint32_t b) {
+        const int count = blk_count(b), slot0 = blk_slot(b);
+        const int64_t row0 = (int64_t)blk_expert(b) * A.H + wrow;
+        const int pg = (int)((row0 + r) * A.down.G) & 1;
+        const uint16_t* hp[NS];
+        bool have[NS];
 #pragma unroll
-            for (int i = 0; i < kCG; ++i) {
-                if (i >= n) break;
-                uint32_t xf[16], xg[16];
+        for (int n = 0; n < NS; ++n) {
+            const int tok = 4 * n + (r >> 1);
+            have[n] = tok < count;
+            hp[n] = ((r & 1) ? A.h_lo : A.h_hi) + (int64_t)(slot0 + (have[n] ? tok : 0)) * A.I + 32 * t;
+        }
+        float acc[NS][4];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        for (int g = 0; g < G; ++g) {
+            uint32_t v[NS][16];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 v = have ? ldg_plain(hp + (g + i) * 128 + 8 * q) : z;
-                    xf[4 * q] = v.x, xf[4 * q + 1] = v.y, xf[4 * q + 2] = v.z, xf[4 * q + 3] = v.w;
-                    const uint4 l = have && !packed ? ldg_plain(lp + (g + i) * 128 + 8 * q) : z;
-                    xg[4 * q] = l.x, xg[4 * q + 1] = l.y, xg[4 * q + 2] = l.z, xg[4 * q + 3] = l.w;
+                    const uint4 u = have[n] ? ldg_plain(hp[n] + g * 128 + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+                    v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
                 }
-                const uint32_t row = src + r * row_stride(A.down.kind) + i * group_bytes(A.down.kind);
-                const uint32_t sc = scale_at(A.down, row0, g, i, src, r);
-                if (packed) group_product<false>(A.down.kind, row, sc, t, xf, xf, acc);
-                else group_product<true>(A.down.kind, row, sc, t, xf, xg, acc);
-            }
+            cp_wait_groups<kStages - 2>();
+            __syncwarp();
+            const uint32_t src = base + (uint32_t)(used % kStages) * kStage;
+            group_product<KIND, NS>(src + r * group_bytes(KIND), src + 16 * group_bytes(KIND) + 4 * r,
+                                    ((pg + g) & 1) != 0, t, v, acc);
             ++used;
             __syncwarp();
             issue();
         }
-        if (packed) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = 2 * t + (i & 1);
-            if (c >= count) continue;
-            float* p = sum + L.slot_token[slot0 + c] * kDownRows + warp * 16 + r + 8 * (i >> 1);
-            *p = fmaf(slot_w[slot0 + c], acc[i], *p);  // this warp's rows: no other writes them
+        for (int n = 0; n < NS; ++n) {
+            const int tok = 4 * n + t;
+            if (tok >= count) continue;
+            const float w = slot_w[slot0 + tok];
+            float* p = sum + L.slot_token[slot0 + tok] * kDownRows + warp * 16 + r;  // no other warp's rows
+            p[0] = fmaf(w, acc[n][0] + acc[n][1], p[0]);
+            p[8] = fmaf(w, acc[n][2] + acc[n][3], p[8]);
         }
         __syncwarp();
+    }
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant__ MoeArgs A) {
+    using Down = MoeDown<KIND>;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ MoeList L;
+    __shared__ float slot_w[kMaxPairs];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = A.C;
+    const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
+    float* sum = reinterpret_cast<float*>(ring + Down::kRing);
+    // the kernel before waited for its inputs: ids and weights are final, only h is not
+    build_list(L, A);
+    Down d{A, L, slot_w, sum, sm_addr(ring) + (uint32_t)(warp * kStages * Down::kStage)};
+    d.lane = lane, d.warp = warp, d.r = lane >> 2, d.t = lane & 3;
+    d.G = A.down.G, d.blocks = L.blocks;
+    d.wrow = (int64_t)tile * kDownRows + warp * 16;
+    d.pb = rank;
+    d.ps = d.issued = d.used = 0;
+    piece_offsets<KIND>(A.down, lane, d.off);
+    for (int i = 0; i < kStages - 1; ++i) d.issue();
+    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
+        const uint32_t blk = L.blk[b];
+        for (int i = 0; i < blk_count(blk); ++i) {
+            const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
+            float w = 0.f;  // a token may name an expert more than once
+            for (int j = 0; j < A.k; ++j)
+                if (A.ids[tok * A.k + j] == blk_expert(blk)) w += A.weights[tok * A.k + j];
+            slot_w[slot] = w;
+        }
+    }
+    for (int i = threadIdx.x; i < A.T * kDownRows; i += kMoeThreads) sum[i] = 0.f;
+    __syncthreads();
+    pdl_wait();
+    for (int b = rank; b < L.blocks; b += C) {
+        const uint32_t blk = L.blk[b];
+        const int count = blk_count(blk);
+        if (count <= 4) d.template block<1>(blk);
+        else if (count <= 8) d.template block<2>(blk);
+        else d.template block<4>(blk);
     }
     cp_wait_groups<0>();
     if (C > 1) {
@@ -529,7 +625,10 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant_
         for (int q = 0; q < C; ++q) {
             float pq;
             if (C > 1)
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(pq) : "r"(map_rank(sum_s + 4 * i, (uint32_t)q)) : "memory");
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(pq)
+                             : "r"(map_rank(sum_s + 4 * i, (uint32_t)q))
+                             : "memory");
             else
                 pq = sum[i];
             v += pq;
@@ -542,6 +641,29 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant_
         cluster_arrive();
         cluster_wait();
     }
+}
+
+struct KernelOf {
+    const void* fn;
+    int ring;
+};
+template <int KG, int KU>
+KernelOf up_of() {
+    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU>), MoeUp<KG, KU>::kRing};
+}
+KernelOf up_kernel(int kg, int ku) {
+    static const KernelOf table[3][3] = {{up_of<0, 0>(), up_of<0, 1>(), up_of<0, 2>()},
+                                         {up_of<1, 0>(), up_of<1, 1>(), up_of<1, 2>()},
+                                         {up_of<2, 0>(), up_of<2, 1>(), up_of<2, 2>()}};
+    return table[kg][ku];
+}
+template <int KIND>
+KernelOf down_of() {
+    return {reinterpret_cast<const void*>(&k_moe_down<KIND>), MoeDown<KIND>::kRing};
+}
+KernelOf down_kernel(int kind) {
+    static const KernelOf table[3] = {down_of<0>(), down_of<1>(), down_of<2>()};
+    return table[kind];
 }
 
 int moe_sms() {
@@ -595,18 +717,20 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.I = (int32_t)I;
     A.ydt = ydt;
     // units that the pairs can make at most; warps split K while they would leave the GPU's warps idle
-    const int64_t units = (int64_t)std::min(T * k, E + T * k / 8) * (I / 16);
+    const int64_t units = (int64_t)std::min(T * k, E + T * k / kBlockTokens) * (I / 16);
     A.S = 1;
     while (A.S < kMoeWarps && units * A.S < (int64_t)sms * 16 && A.gate.G >= 2 * A.S) A.S *= 2;
     A.C = 8;
-    const int up_smem = kMoeWarps * kStages * (mat_bytes(A.gate.kind) + mat_bytes(A.up.kind));
-    const int down_smem = kMoeWarps * kStages * mat_bytes(A.down.kind) + T * kDownRows * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_moe_up, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    A.hperm = A.down.kind == 2 ? 1 : 0;
+    const KernelOf ku = up_kernel(A.gate.kind, A.up.kind), kd = down_kernel(A.down.kind);
+    const int up_smem = ku.ring + (A.S > 1 ? 2 * kMoeWarps * (T > 8 ? 2 : 1) * 1024 : 0);
+    const int down_smem = kd.ring + T * kDownRows * 4;
+    cudaError_t e = cudaFuncSetAttribute(ku.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(k_moe_down, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    e = cudaFuncSetAttribute(kd.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_moe_up, kMoeThreads, (size_t)up_smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ku.fn, kMoeThreads, (size_t)up_smem);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     const int64_t ctas = std::min<int64_t>((units * A.S + kMoeWarps - 1) / kMoeWarps, (int64_t)sms * per_sm);
@@ -622,7 +746,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     cfg.dynamicSmemBytes = (size_t)up_smem;
     cfg.numAttrs = 0;
     void* args[] = {&A};
-    e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&k_moe_up), args);
+    e = cudaLaunchKernelExC(&cfg, ku.fn, args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
     cfg.dynamicSmemBytes = (size_t)down_smem;
@@ -632,7 +756,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     at[1].val.clusterDim.x = (unsigned)A.C;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&k_moe_down), args);
+    return cudaLaunchKernelExC(&cfg, kd.fn, args);
 }
 
 }  // namespace tb
