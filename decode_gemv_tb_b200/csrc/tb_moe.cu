@@ -193,7 +193,7 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
                                               float (&acc)[NS][4]) {
     if constexpr (KIND == 2) {
         const uint32_t ba = lds8(sc + t), bb = lds8(sc + 32 + t);
-        if (__any_sync(0xffffffffu, max(ba, bb) > 128u)) mx4_product<NS, true>(row, t, ba, bb, x, acc);
+        if (__builtin_expect(__any_sync(0xffffffffu, max(ba, bb) > 128u), 0)) mx4_product<NS, true>(row, t, ba, bb, x, acc);
         else mx4_product<NS, false>(row, t, ba, bb, x, acc);
     } else {
         float d[NS][4];
@@ -238,34 +238,52 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
     }
 }
 
-// Requests group g of rows row0 .. row0 + 15 into a stage; lane_off: the lane's 16-byte pieces of 16 rows (their
-// offsets from the first row's group).
+// A warp's place in the packed rows of a matrix: group after group of the 16 rows row0 .., each lane with its own
+// 16-byte pieces.
 template <int KIND>
-__device__ __forceinline__ void piece_offsets(const MoeMat& m, int lane, uint32_t (&off)[2]) {
-    constexpr int P = group_bytes(KIND) / 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int c = lane + 32 * i;
-        off[i] = (uint32_t)((c / P) * m.rb + (c % P) * 16);
+struct CodeCursor {
+    const uint8_t* p;
+    uint32_t second;  // from the lane's first piece to its second
+    __device__ __forceinline__ void init(const MoeMat& m, int lane) {
+        constexpr int P = group_bytes(KIND) / 16;
+        const int a = lane, b = lane + 32;
+        second = (uint32_t)((b / P - a / P) * m.rb + (b % P - a % P) * 16);
     }
-}
-template <int KIND>
-__device__ __forceinline__ void load_codes(const MoeMat& m, int64_t row0, int g, uint32_t dst, int lane,
-                                           const uint32_t (&off)[2]) {
-    const uint8_t* src = m.packed + row0 * m.rb + (int64_t)g * group_bytes(KIND);
-    cp16(dst + lane * 16, src + off[0]);
-    if (KIND == 2 || (KIND == 1 && lane < 16)) cp16(dst + (lane + 32) * 16, src + off[1]);
-}
-// the scale word of row row0 + i: two bytes (in an aligned word) or the four bytes of a 4-bit group
-template <int KIND>
-__device__ __forceinline__ void load_scale(const MoeMat& m, int64_t row0, int g, uint32_t dst, int i) {
-    const int64_t row = row0 + i;
-    if constexpr (KIND == 2) {
-        cp4(dst + 4 * i, m.scales + (((row >> 7) * m.G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3)) * 4, 4);
-    } else {
-        const int64_t at = row * m.G + g;
-        cp4(dst + 4 * i, m.scales + (at & ~(int64_t)1) * 2, (at & 1) ? 4 : 2);
+    __device__ __forceinline__ void at(const MoeMat& m, int64_t row0, int g, int lane) {
+        constexpr int P = group_bytes(KIND) / 16;
+        p = m.packed + (row0 + lane / P) * m.rb + (int64_t)g * group_bytes(KIND) + (lane % P) * 16;
     }
+    __device__ __forceinline__ void load(uint32_t dst, int lane) {
+        cp16(dst + lane * 16, p);
+        if (KIND == 2 || (KIND == 1 && lane < 16)) cp16(dst + (lane + 32) * 16, p + second);
+        p += group_bytes(KIND);
+    }
+};
+// The same for a row's scales: two bytes per group, fetched with the aligned word they lie in, or a word per 4-bit
+// group.
+struct ScaleCursor {
+    const uint8_t* p;
+    uint32_t step, n;
+    template <int KIND>
+    __device__ __forceinline__ void at(const MoeMat& m, int64_t row, int g) {
+        if constexpr (KIND == 2) {
+            p = m.scales + (((row >> 7) * m.G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3)) * 4;
+            step = 512, n = 4;
+        } else {
+            p = m.scales + (row * m.G + g) * 2;
+            step = 2, n = 2;
+        }
+    }
+    __device__ __forceinline__ void load(uint32_t dst) {
+        const uintptr_t v = reinterpret_cast<uintptr_t>(p);
+        cp4(dst, reinterpret_cast<const void*>(v & ~(uintptr_t)3), (v & 2) ? 4 : n);
+        p += step;
+    }
+};
+// the next stage of a ring
+__device__ __forceinline__ uint32_t next_stage(uint32_t at, uint32_t base, uint32_t stage) {
+    at += stage;
+    return at == base + kStages * stage ? base : at;
 }
 
 // ---- the pairs grouped by expert ---------------------------------------------------
@@ -280,16 +298,17 @@ __device__ __forceinline__ int blk_expert(uint32_t b) { return (int)(b & 1023u);
 __device__ __forceinline__ int blk_slot(uint32_t b) { return (int)(b >> 10 & 1023u); }
 __device__ __forceinline__ int blk_count(uint32_t b) { return (int)(b >> 20); }
 
+template <int THREADS>
 __device__ void build_list(MoeList& L, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < A.E; e += kMoeThreads) L.mask[e] = 0ull;
+    for (int e = tid; e < A.E; e += THREADS) L.mask[e] = 0ull;
     __syncthreads();
-    for (int p = tid; p < A.T * A.k; p += kMoeThreads) {
+    for (int p = tid; p < A.T * A.k; p += THREADS) {
         const int e = A.ids[p];
         if (e >= 0 && e < A.E) atomicOr(&L.mask[e], 1ull << (p / A.k));  // a set: the order does not matter
     }
     __syncthreads();
-    const int per = (A.E + kMoeThreads - 1) / kMoeThreads, e0 = tid * per, e1 = min(A.E, e0 + per);
+    const int per = (A.E + THREADS - 1) / THREADS, e0 = tid * per, e1 = min(A.E, e0 + per);
     int slots = 0, blocks = 0;
     for (int e = e0; e < e1; ++e) {
         const int c = __popcll(L.mask[e]);
@@ -314,7 +333,7 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
         s += L.scan[0][w];
         b += L.scan[1][w];
     }
-    if (tid == kMoeThreads - 1) {
+    if (tid == THREADS - 1) {
         L.slots = s;
         L.blocks = b;
     }
@@ -346,24 +365,34 @@ struct MoeUp {
     float* part;    // [2][warps][sets][256]: partial sums of gate and up, two units deep
     uint32_t base;  // this warp's ring
     int lane, warp, r, t, S, s, ui, g0, steps, tiles, units, ustep, sets;
-    int pu, ps, issued, used, flip;
-    uint32_t og[2], ou[2];
+    int pu, ps, flip;
+    uint32_t to, from;  // the stages to be filled and read next
+    CodeCursor<KG> cg;
+    CodeCursor<KU> cu;
+    ScaleCursor sc;
 
+    // the first request of unit pu: cursors to its rows
+    __device__ __forceinline__ void seek() {
+        if (pu >= units) return;
+        const int blk = pu / tiles, tile = pu - blk * tiles;
+        const int64_t row0 = (int64_t)blk_expert(L.blk[blk]) * A.I + tile * 16;
+        cg.at(A.gate, row0, g0, lane);
+        cu.at(A.up, row0, g0, lane);
+        if (lane < 16) sc.at<KG>(A.gate, row0 + lane, g0);
+        else sc.at<KU>(A.up, row0 + lane - 16, g0);
+        ps = 0;
+    }
     __device__ __forceinline__ void issue() {
         if (pu < units) {
-            const int blk = pu / tiles, tile = pu - blk * tiles, g = g0 + ps;
-            const int64_t row0 = (int64_t)blk_expert(L.blk[blk]) * A.I + tile * 16;
-            const uint32_t dst = base + (uint32_t)(issued % kStages) * kStage;
-            load_codes<KG>(A.gate, row0, g, dst, lane, og);
-            load_codes<KU>(A.up, row0, g, dst + kGate, lane, ou);
-            if (lane < 16) load_scale<KG>(A.gate, row0, g, dst + kGate + kUp, lane);
-            else load_scale<KU>(A.up, row0, g, dst + kGate + kUp + 64, lane - 16);
+            cg.load(to, lane);
+            cu.load(to + kGate, lane);
+            sc.load(to + kGate + kUp + 4 * lane);
             if (++ps == steps) {
-                ps = 0;
                 pu += ustep;
+                seek();
             }
         }
-        ++issued;
+        to = next_stage(to, base, kStage);
         cp_commit_group();
     }
 
@@ -385,28 +414,43 @@ struct MoeUp {
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = 0.f;
-        for (int st = 0; st < steps; ++st) {
-            uint32_t v[NS][16];
+        uint32_t v[NS][16];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[n][q] = 0u;
+        auto load_x = [&](int st) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
+                if (have[n]) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 u = have[n] ? ld_act_u4(xr[n] + st * 128 + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
-                    v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 u = ld_act_u4(xr[n] + st * 128 + 8 * q);
+                        v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                    }
                 }
+        };
+        load_x(0);
+        for (int st = 0; st < steps; ++st) {
+            // this group's activations in the order of the decoders' pairs; then the next group's are requested
+            uint32_t p[NS][16], w[NS][16];
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                if constexpr (KG == 2 || KU == 2) pair_up(p[n], v[n]);
+                if constexpr (KG != 2 || KU != 2) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
+                }
+            }
+            if (NS == 1 && st + 1 < steps) load_x(st + 1);
             cp_wait_groups<kStages - 2>();
             __syncwarp();
-            const uint32_t src = base + (uint32_t)(used % kStages) * kStage;
             const bool odd = ((pg + st) & 1) != 0;
-            uint32_t p[NS][16];
-            if constexpr (KG == 2 || KU == 2) {
-#pragma unroll
-                for (int n = 0; n < NS; ++n) pair_up(p[n], v[n]);
-            }
-            group_product<KG, NS>(src + r * group_bytes(KG), src + kGate + kUp + 4 * r, odd, t, KG == 2 ? p : v, ag);
-            group_product<KU, NS>(src + kGate + r * group_bytes(KU), src + kGate + kUp + 64 + 4 * r, odd, t,
-                                  KU == 2 ? p : v, au);
-            ++used;
+            group_product<KG, NS>(from + r * group_bytes(KG), from + kGate + kUp + 4 * r, odd, t, KG == 2 ? p : w, ag);
+            group_product<KU, NS>(from + kGate + r * group_bytes(KU), from + kGate + kUp + 64 + 4 * r, odd, t,
+                                  KU == 2 ? p : w, au);
+            if (NS > 1 && st + 1 < steps) load_x(st + 1);
+            from = next_stage(from, base, kStage);
             __syncwarp();
             issue();
         }
@@ -461,7 +505,7 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeList L;
     pdl_wait();
-    build_list(L, A);
+    build_list<kMoeThreads>(L, A);
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = A.S, per = kMoeWarps / S;
     Up u{A, L, reinterpret_cast<float*>(ring + Up::kRing), sm_addr(ring) + (uint32_t)(warp * kStages * Up::kStage)};
@@ -474,9 +518,11 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
     u.ustep = (int)gridDim.x * per;
     u.sets = A.T > 8 ? 2 : 1;
     u.pu = (int)blockIdx.x * per + u.ui;
-    u.ps = u.issued = u.used = u.flip = 0;
-    piece_offsets<KG>(A.gate, lane, u.og);
-    piece_offsets<KU>(A.up, lane, u.ou);
+    u.ps = u.flip = 0;
+    u.to = u.from = u.base;
+    u.cg.init(A.gate, lane);
+    u.cu.init(A.up, lane);
+    u.seek();
     for (int i = 0; i < kStages - 1; ++i) u.issue();
     for (int v = (int)blockIdx.x * per + u.ui; v < u.units; v += u.ustep) {
         const int blk = v / u.tiles;
@@ -488,12 +534,14 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
 }
 
 // ---- down and the weighted sum ------------------------------------------------------------
-constexpr int kDownRows = 16 * kMoeWarps;
+constexpr int kDownWarps = 2;
+constexpr int kDownThreads = kDownWarps * 32;
+constexpr int kDownRows = 16 * kDownWarps;
 
 template <int KIND>
 struct MoeDown {
     static constexpr int kStage = mat_bytes(KIND);
-    static constexpr int kRing = kMoeWarps * kStages * kStage;
+    static constexpr int kRing = kDownWarps * kStages * kStage;
 
     const MoeArgs& A;
     MoeList& L;
@@ -502,76 +550,105 @@ struct MoeDown {
     uint32_t base;  // this warp's ring
     int lane, warp, r, t, G, blocks;
     int64_t wrow;
-    int pb, ps, issued, used;
-    uint32_t off[2];
+    int pb, ps;
+    uint32_t to, from;  // the stages to be filled and read next
+    CodeCursor<KIND> codes;
+    ScaleCursor sc;
 
+    __device__ __forceinline__ void seek() {
+        if (pb >= blocks) return;
+        const int64_t row0 = (int64_t)blk_expert(L.blk[pb]) * A.H + wrow;
+        codes.at(A.down, row0, 0, lane);
+        sc.at<KIND>(A.down, row0 + (lane & 15), 0);
+        ps = 0;
+    }
     __device__ __forceinline__ void issue() {
         if (pb < blocks) {
-            const int64_t row0 = (int64_t)blk_expert(L.blk[pb]) * A.H + wrow;
-            const uint32_t dst = base + (uint32_t)(issued % kStages) * kStage;
-            load_codes<KIND>(A.down, row0, ps, dst, lane, off);
-            if (lane < 16) load_scale<KIND>(A.down, row0, ps, dst + 16 * group_bytes(KIND), lane);
+            codes.load(to, lane);
+            if (lane < 16) sc.load(to + 16 * group_bytes(KIND) + 4 * lane);
             if (++ps == G) {
-                ps = 0;
                 pb += A.C;
+                seek();
             }
         }
-        ++issued;
+        to = next_stage(to, base, kStage);
         cp_commit_group();
     }
 
-    // a set: the high and low parts of four tokens, in turn
-    template <int NS>
+    // A set: the high and low parts of four tokens, in turn.  More than eight tokens take the decode twice (four sets
+    // of fragments would not fit beside it in 128 registers).
+    template <int NS, int HALVES>
     __device__ __forceinline__ void block(uint32_t b) {
         const int count = blk_count(b), slot0 = blk_slot(b);
         const int64_t row0 = (int64_t)blk_expert(b) * A.H + wrow;
         const int pg = (int)((row0 + r) * A.down.G) & 1;
-        const uint16_t* hp[NS];
-        bool have[NS];
+        const uint16_t* hp = ((r & 1) ? A.h_lo : A.h_hi) + (int64_t)(slot0 + (r >> 1)) * A.I + 32 * t;
+        float acc[HALVES][NS][4];
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int tok = 4 * n + (r >> 1);
-            have[n] = tok < count;
-            hp[n] = ((r & 1) ? A.h_lo : A.h_hi) + (int64_t)(slot0 + (have[n] ? tok : 0)) * A.I + 32 * t;
-        }
-        float acc[NS][4];
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-        for (int g = 0; g < G; ++g) {
-            uint32_t v[NS][16];
+        for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 u = have[n] ? ldg_plain(hp[n] + g * 128 + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
-                    v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                for (int i = 0; i < 4; ++i) acc[h][n][i] = 0.f;
+        uint32_t v[NS][16];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[n][q] = 0u;
+        auto load_h = [&](int g, int h) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const int tok = 4 * (h * NS + n);
+                if (tok + (r >> 1) < count) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 u = ldg_plain(hp + (int64_t)tok * A.I + g * 128 + 8 * q);
+                        v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                    }
+                } else if (HALVES > 1) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) v[n][q] = 0u;
                 }
+            }
+        };
+        load_h(0, 0);
+        for (int g = 0; g < G; ++g) {
             cp_wait_groups<kStages - 2>();
             __syncwarp();
-            const uint32_t src = base + (uint32_t)(used % kStages) * kStage;
-            group_product<KIND, NS>(src + r * group_bytes(KIND), src + 16 * group_bytes(KIND) + 4 * r,
-                                    ((pg + g) & 1) != 0, t, v, acc);
-            ++used;
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                uint32_t w[NS][16];
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
+                const int gn = h + 1 < HALVES ? g : g + 1, hn = h + 1 < HALVES ? h + 1 : 0;
+                if (NS == 1 && gn < G) load_h(gn, hn);
+                group_product<KIND, NS>(from + r * group_bytes(KIND), from + 16 * group_bytes(KIND) + 4 * r,
+                                        ((pg + g) & 1) != 0, t, w, acc[h]);
+                if (NS > 1 && gn < G) load_h(gn, hn);
+            }
+            from = next_stage(from, base, kStage);
             __syncwarp();
             issue();
         }
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int tok = 4 * n + t;
-            if (tok >= count) continue;
-            const float w = slot_w[slot0 + tok];
-            float* p = sum + L.slot_token[slot0 + tok] * kDownRows + warp * 16 + r;  // no other warp's rows
-            p[0] = fmaf(w, acc[n][0] + acc[n][1], p[0]);
-            p[8] = fmaf(w, acc[n][2] + acc[n][3], p[8]);
-        }
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                const int tok = 4 * (h * NS + n) + t;
+                if (tok >= count) continue;
+                const float w = slot_w[slot0 + tok];
+                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + warp * 16 + r;  // no other warp's rows
+                p[0] = fmaf(w, acc[h][n][0] + acc[h][n][1], p[0]);
+                p[8] = fmaf(w, acc[h][n][2] + acc[h][n][3], p[8]);
+            }
         __syncwarp();
     }
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kDownThreads, 7) k_moe_down(const __grid_constant__ MoeArgs A) {
     using Down = MoeDown<KIND>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeList L;
@@ -580,16 +657,18 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant_
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
     float* sum = reinterpret_cast<float*>(ring + Down::kRing);
     // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list(L, A);
+    build_list<kDownThreads>(L, A);
     Down d{A, L, slot_w, sum, sm_addr(ring) + (uint32_t)(warp * kStages * Down::kStage)};
     d.lane = lane, d.warp = warp, d.r = lane >> 2, d.t = lane & 3;
     d.G = A.down.G, d.blocks = L.blocks;
     d.wrow = (int64_t)tile * kDownRows + warp * 16;
     d.pb = rank;
-    d.ps = d.issued = d.used = 0;
-    piece_offsets<KIND>(A.down, lane, d.off);
+    d.ps = 0;
+    d.to = d.from = d.base;
+    d.codes.init(A.down, lane);
+    d.seek();
     for (int i = 0; i < kStages - 1; ++i) d.issue();
-    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
+    for (int b = threadIdx.x; b < L.blocks; b += kDownThreads) {
         const uint32_t blk = L.blk[b];
         for (int i = 0; i < blk_count(blk); ++i) {
             const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
@@ -599,15 +678,15 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant_
             slot_w[slot] = w;
         }
     }
-    for (int i = threadIdx.x; i < A.T * kDownRows; i += kMoeThreads) sum[i] = 0.f;
+    for (int i = threadIdx.x; i < A.T * kDownRows; i += kDownThreads) sum[i] = 0.f;
     __syncthreads();
     pdl_wait();
     for (int b = rank; b < L.blocks; b += C) {
         const uint32_t blk = L.blk[b];
         const int count = blk_count(blk);
-        if (count <= 4) d.template block<1>(blk);
-        else if (count <= 8) d.template block<2>(blk);
-        else d.template block<4>(blk);
+        if (count <= 4) d.template block<1, 1>(blk);
+        else if (count <= 8) d.template block<2, 1>(blk);
+        else d.template block<2, 2>(blk);
     }
     cp_wait_groups<0>();
     if (C > 1) {
@@ -618,7 +697,7 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_down(const __grid_constant_
     }
     // the ranks' sums in rank order; rank q finishes tokens q, q + C, ...
     const uint32_t sum_s = sm_addr(sum);
-    for (int i = threadIdx.x; i < A.T * kDownRows; i += kMoeThreads) {
+    for (int i = threadIdx.x; i < A.T * kDownRows; i += kDownThreads) {
         const int tok = i / kDownRows, row = i - tok * kDownRows;
         if (tok % C != rank) continue;
         float v = 0.f;
@@ -749,6 +828,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     e = cudaLaunchKernelExC(&cfg, ku.fn, args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
+    cfg.blockDim = dim3(kDownThreads);
     cfg.dynamicSmemBytes = (size_t)down_smem;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
