@@ -500,7 +500,7 @@ struct MoeUp {
 };
 
 template <int KG, int KU>
-__global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant__ MoeArgs A) {
     using Up = MoeUp<KG, KU>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeList L;
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kMoeThreads) k_moe_up(const __grid_constant__ 
 }
 
 // ---- down and the weighted sum ------------------------------------------------------------
-constexpr int kDownWarps = 2;
+constexpr int kDownWarps = 4, kDownSub = 2;  // warps: kDownSub subsets of the blocks for each tile of 16 rows
 constexpr int kDownThreads = kDownWarps * 32;
-constexpr int kDownRows = 16 * kDownWarps;
+constexpr int kDownRows = 16 * (kDownWarps / kDownSub);
 
 template <int KIND>
 struct MoeDown {
@@ -546,9 +546,9 @@ struct MoeDown {
     const MoeArgs& A;
     MoeList& L;
     const float* slot_w;
-    float* sum;     // [T][kDownRows]
+    float* sum;     // this warp's subset's [T][kDownRows]
     uint32_t base;  // this warp's ring
-    int lane, warp, r, t, G, blocks;
+    int lane, wr, r, t, G, blocks, bstep;
     int64_t wrow;
     int pb, ps;
     uint32_t to, from;  // the stages to be filled and read next
@@ -567,7 +567,7 @@ struct MoeDown {
             codes.load(to, lane);
             if (lane < 16) sc.load(to + 16 * group_bytes(KIND) + 4 * lane);
             if (++ps == G) {
-                pb += A.C;
+                pb += bstep;
                 seek();
             }
         }
@@ -639,7 +639,7 @@ struct MoeDown {
                 const int tok = 4 * (h * NS + n) + t;
                 if (tok >= count) continue;
                 const float w = slot_w[slot0 + tok];
-                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + warp * 16 + r;  // no other warp's rows
+                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + wr * 16 + r;  // no other warp's
                 p[0] = fmaf(w, acc[h][n][0] + acc[h][n][1], p[0]);
                 p[8] = fmaf(w, acc[h][n][2] + acc[h][n][3], p[8]);
             }
@@ -648,7 +648,7 @@ struct MoeDown {
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(kDownThreads, 7) k_moe_down(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kDownThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
     using Down = MoeDown<KIND>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeList L;
@@ -658,11 +658,12 @@ __global__ void __launch_bounds__(kDownThreads, 7) k_moe_down(const __grid_const
     float* sum = reinterpret_cast<float*>(ring + Down::kRing);
     // the kernel before waited for its inputs: ids and weights are final, only h is not
     build_list<kDownThreads>(L, A);
-    Down d{A, L, slot_w, sum, sm_addr(ring) + (uint32_t)(warp * kStages * Down::kStage)};
-    d.lane = lane, d.warp = warp, d.r = lane >> 2, d.t = lane & 3;
-    d.G = A.down.G, d.blocks = L.blocks;
-    d.wrow = (int64_t)tile * kDownRows + warp * 16;
-    d.pb = rank;
+    const int sub = warp % kDownSub, subs = C * kDownSub;
+    Down d{A, L, slot_w, sum + sub * A.T * kDownRows, sm_addr(ring) + (uint32_t)(warp * kStages * Down::kStage)};
+    d.lane = lane, d.wr = warp / kDownSub, d.r = lane >> 2, d.t = lane & 3;
+    d.G = A.down.G, d.blocks = L.blocks, d.bstep = subs;
+    d.wrow = (int64_t)tile * kDownRows + d.wr * 16;
+    d.pb = rank * kDownSub + sub;
     d.ps = 0;
     d.to = d.from = d.base;
     d.codes.init(A.down, lane);
@@ -678,10 +679,10 @@ __global__ void __launch_bounds__(kDownThreads, 7) k_moe_down(const __grid_const
             slot_w[slot] = w;
         }
     }
-    for (int i = threadIdx.x; i < A.T * kDownRows; i += kDownThreads) sum[i] = 0.f;
+    for (int i = threadIdx.x; i < kDownSub * A.T * kDownRows; i += kDownThreads) sum[i] = 0.f;
     __syncthreads();
     pdl_wait();
-    for (int b = rank; b < L.blocks; b += C) {
+    for (int b = rank * kDownSub + sub; b < L.blocks; b += subs) {
         const uint32_t blk = L.blk[b];
         const int count = blk_count(blk);
         if (count <= 4) d.template block<1, 1>(blk);
@@ -701,15 +702,16 @@ __global__ void __launch_bounds__(kDownThreads, 7) k_moe_down(const __grid_const
         const int tok = i / kDownRows, row = i - tok * kDownRows;
         if (tok % C != rank) continue;
         float v = 0.f;
-        for (int q = 0; q < C; ++q) {
+        for (int q = 0; q < subs; ++q) {
+            const int j = q % kDownSub * A.T * kDownRows + i;
             float pq;
             if (C > 1)
                 asm volatile("ld.shared::cluster.f32 %0, [%1];"
                              : "=f"(pq)
-                             : "r"(map_rank(sum_s + 4 * i, (uint32_t)q))
+                             : "r"(map_rank(sum_s + 4 * j, (uint32_t)(q / kDownSub)))
                              : "memory");
             else
-                pq = sum[i];
+                pq = sum[j];
             v += pq;
         }
         const int64_t at = (int64_t)tok * A.ldy + (int64_t)tile * kDownRows + row;
@@ -803,7 +805,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.hperm = A.down.kind == 2 ? 1 : 0;
     const KernelOf ku = up_kernel(A.gate.kind, A.up.kind), kd = down_kernel(A.down.kind);
     const int up_smem = ku.ring + (A.S > 1 ? 2 * kMoeWarps * (T > 8 ? 2 : 1) * 1024 : 0);
-    const int down_smem = kd.ring + T * kDownRows * 4;
+    const int down_smem = kd.ring + T * kDownSub * kDownRows * 4;
     cudaError_t e = cudaFuncSetAttribute(ku.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kd.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
