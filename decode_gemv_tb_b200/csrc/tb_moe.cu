@@ -20,9 +20,8 @@
 // per lane, free of bank conflicts, and no code moves between lanes.  Weights
 // stream through a private cp.async ring per warp, a group per stage.
 //
-// h is kept as two bf16 (high and low part, 16 significant bits together), so
-// that the second product sees it as exactly as the fp32 sums it came from
-// are worth: the parts of a token are neighbouring columns of a set.
+// h is rounded to bf16 between the two products, as tb_gate_up_silu's is: the
+// MMA's operand, and half the activations a second part would cost.
 //
 // k_moe_up: a unit is (block, 16 rows of gate and of up); S warps of a CTA
 // split K when units are few.  k_moe_down: a cluster of C CTAs holds 64 rows
@@ -33,6 +32,7 @@
 #include "tb_internal.h"
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 namespace tb {
@@ -50,7 +50,7 @@ struct MoeArgs {
     const uint16_t* x;       // [T][ldx]
     const int32_t* ids;      // [T][k]
     const float* weights;    // [T][k]
-    uint16_t *h_hi, *h_lo;   // [slots][I]
+    uint16_t* h;             // [slots][I] bf16
     void* y;                 // [T][ldy]
     int64_t ldx, ldy;
     int32_t T, k, E, H, I, ydt;
@@ -68,9 +68,8 @@ constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxK;
 constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / kBlockTokens;
 
 // packed bytes of a row's group (also its stride in shared memory: with 32, 48 and 64 bytes the reads of eight rows
-// by a quad each touch every bank once); a stage's bytes: 16 rows and their scale words
+// by a quad each touch every bank once)
 __host__ __device__ constexpr int group_bytes(int kind) { return kind == 0 ? 32 : (kind == 1 ? 48 : 64); }
-__host__ __device__ constexpr int mat_bytes(int kind) { return 16 * group_bytes(kind) + 64; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -488,13 +487,9 @@ struct MoeUp {
                 const int col = 8 * n + 2 * t + (i & 1);
                 if ((i & (S - 1)) != s || col >= count) continue;
                 const float g = ag[n][i], h = g / (1.f + expf(-g)) * au[n][i];
-                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                const float rest = h - __bfloat162float(hi);  // no number where hi is infinite
                 int c = tile * 16 + r + 8 * (i >> 1);
                 if (A.hperm) c = (c & ~7) | (c & 3) << 1 | (c >> 2 & 1);
-                const int64_t at = (int64_t)(slot0 + col) * A.I + c;
-                A.h_hi[at] = __bfloat16_as_ushort(hi);
-                A.h_lo[at] = fabsf(rest) < INFINITY ? __bfloat16_as_ushort(__float2bfloat16_rn(rest)) : (uint16_t)0;
+                A.h[(int64_t)(slot0 + col) * A.I + c] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
             }
     }
 };
@@ -534,142 +529,160 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
 }
 
 // ---- down and the weighted sum ------------------------------------------------------------
-constexpr int kDownWarps = 4, kDownSub = 2;  // warps: kDownSub subsets of the blocks for each tile of 16 rows
-constexpr int kDownThreads = kDownWarps * 32;
-constexpr int kDownRows = 16 * (kDownWarps / kDownSub);
+constexpr int kDownRows = 32;    // of a CTA: each warp holds all of them, two tiles that share h's fragments
+constexpr int kDownStages = 3;
 
 template <int KIND>
 struct MoeDown {
-    static constexpr int kStage = mat_bytes(KIND);
-    static constexpr int kRing = kDownWarps * kStages * kStage;
+    static constexpr int kCodes = 16 * group_bytes(KIND);
+    static constexpr int kStage = 2 * kCodes + 128;
+    static constexpr int kRing = kMoeWarps * kDownStages * kStage;
 
     const MoeArgs& A;
     MoeList& L;
     const float* slot_w;
-    float* sum;     // this warp's subset's [T][kDownRows]
+    float* sum;     // this warp's [T][kDownRows]
     uint32_t base;  // this warp's ring
-    int lane, wr, r, t, G, blocks, bstep;
+    int lane, r, t, G, tasks, KS, step;
     int64_t wrow;
-    int pb, ps;
+    int pq, ps, pend;   // the next request: task, group, end of the task's groups
     uint32_t to, from;  // the stages to be filled and read next
     CodeCursor<KIND> codes;
+    int64_t tile2;  // from a piece of the first tile to that of the second
     ScaleCursor sc;
 
+    __device__ __forceinline__ void range(int q, int& b, int& g0, int& g1) const {
+        b = q / KS;
+        const int k = q - b * KS;
+        g0 = G * k / KS;
+        g1 = G * (k + 1) / KS;
+    }
     __device__ __forceinline__ void seek() {
-        if (pb >= blocks) return;
-        const int64_t row0 = (int64_t)blk_expert(L.blk[pb]) * A.H + wrow;
-        codes.at(A.down, row0, 0, lane);
-        sc.at<KIND>(A.down, row0 + (lane & 15), 0);
-        ps = 0;
+        if (pq >= tasks) return;
+        int b;
+        range(pq, b, ps, pend);
+        const int64_t row0 = (int64_t)blk_expert(L.blk[b]) * A.H + wrow;
+        codes.at(A.down, row0, ps, lane);
+        sc.at<KIND>(A.down, row0 + lane, ps);
     }
     __device__ __forceinline__ void issue() {
-        if (pb < blocks) {
+        if (pq < tasks) {
+            CodeCursor<KIND> second = codes;
+            second.p += tile2;
+            second.load(to + kCodes, lane);
             codes.load(to, lane);
-            if (lane < 16) sc.load(to + 16 * group_bytes(KIND) + 4 * lane);
-            if (++ps == G) {
-                pb += bstep;
+            sc.load(to + 2 * kCodes + 4 * lane);
+            if (++ps == pend) {
+                pq += step;
                 seek();
             }
         }
-        to = next_stage(to, base, kStage);
+        to += kStage;
+        if (to == base + kDownStages * kStage) to = base;
         cp_commit_group();
     }
 
-    // A set: the high and low parts of four tokens, in turn.  More than eight tokens take the decode twice (four sets
-    // of fragments would not fit beside it in 128 registers).
-    template <int NS, int HALVES>
-    __device__ __forceinline__ void block(uint32_t b) {
+    template <int NS>
+    __device__ __forceinline__ void block(uint32_t b, int g0, int g1) {
         const int count = blk_count(b), slot0 = blk_slot(b);
         const int64_t row0 = (int64_t)blk_expert(b) * A.H + wrow;
-        const int pg = (int)((row0 + r) * A.down.G) & 1;
-        const uint16_t* hp = ((r & 1) ? A.h_lo : A.h_hi) + (int64_t)(slot0 + (r >> 1)) * A.I + 32 * t;
-        float acc[HALVES][NS][4];
+        const int pg = (int)((row0 + r) * A.down.G) & 1;  // 16 rows on it is the same
+        const uint16_t* hp[NS];
+        bool have[NS];
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h)
+        for (int n = 0; n < NS; ++n) {
+            have[n] = 8 * n + r < count;
+            hp[n] = A.h + (int64_t)(slot0 + (have[n] ? 8 * n + r : 0)) * A.I + 32 * t;
+        }
+        float acc[2][NS][4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[h][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
         uint32_t v[NS][16];
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int q = 0; q < 16; ++q) v[n][q] = 0u;
-        auto load_h = [&](int g, int h) {
+        auto load_h = [&](int g) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const int tok = 4 * (h * NS + n);
-                if (tok + (r >> 1) < count) {
+            for (int n = 0; n < NS; ++n)
+                if (have[n]) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint4 u = ldg_plain(hp + (int64_t)tok * A.I + g * 128 + 8 * q);
+                        const uint4 u = ldg_plain(hp[n] + g * 128 + 8 * q);
                         v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
                     }
-                } else if (HALVES > 1) {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[n][q] = 0u;
                 }
-            }
         };
-        load_h(0, 0);
-        for (int g = 0; g < G; ++g) {
-            cp_wait_groups<kStages - 2>();
+        load_h(g0);
+        for (int g = g0; g < g1; ++g) {
+            uint32_t w[NS][16];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
+            if (NS == 1 && g + 1 < g1) load_h(g + 1);
+            cp_wait_groups<kDownStages - 2>();
             __syncwarp();
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-                uint32_t w[NS][16];
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
-                const int gn = h + 1 < HALVES ? g : g + 1, hn = h + 1 < HALVES ? h + 1 : 0;
-                if (NS == 1 && gn < G) load_h(gn, hn);
-                group_product<KIND, NS>(from + r * group_bytes(KIND), from + 16 * group_bytes(KIND) + 4 * r,
-                                        ((pg + g) & 1) != 0, t, w, acc[h]);
-                if (NS > 1 && gn < G) load_h(gn, hn);
-            }
-            from = next_stage(from, base, kStage);
+            const bool odd = ((pg + g) & 1) != 0;
+            group_product<KIND, NS>(from + r * group_bytes(KIND), from + 2 * kCodes + 4 * r, odd, t, w, acc[0]);
+            group_product<KIND, NS>(from + kCodes + r * group_bytes(KIND), from + 2 * kCodes + 64 + 4 * r, odd, t, w,
+                                    acc[1]);
+            if (NS > 1 && g + 1 < g1) load_h(g + 1);
+            from += kStage;
+            if (from == base + kDownStages * kStage) from = base;
             __syncwarp();
             issue();
         }
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h)
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const int tok = 4 * (h * NS + n) + t;
+            for (int j = 0; j < 2; ++j) {
+                const int tok = 8 * n + 2 * t + j;
                 if (tok >= count) continue;
                 const float w = slot_w[slot0 + tok];
-                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + wr * 16 + r;  // no other warp's
-                p[0] = fmaf(w, acc[h][n][0] + acc[h][n][1], p[0]);
-                p[8] = fmaf(w, acc[h][n][2] + acc[h][n][3], p[8]);
+                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + r;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    p[16 * m] = fmaf(w, acc[m][n][j], p[16 * m]);
+                    p[16 * m + 8] = fmaf(w, acc[m][n][2 + j], p[16 * m + 8]);
+                }
             }
         __syncwarp();
     }
 };
 
 template <int KIND>
-__global__ void __launch_bounds__(kDownThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
     using Down = MoeDown<KIND>;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ MoeList L;
     __shared__ float slot_w[kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = A.C;
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
-    float* sum = reinterpret_cast<float*>(ring + Down::kRing);
+    float* sum = reinterpret_cast<float*>(ring + Down::kRing);  // [warps][T][kDownRows]
+    const int sums = A.T * kDownRows;
     // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list<kDownThreads>(L, A);
-    const int sub = warp % kDownSub, subs = C * kDownSub;
-    Down d{A, L, slot_w, sum + sub * A.T * kDownRows, sm_addr(ring) + (uint32_t)(warp * kStages * Down::kStage)};
-    d.lane = lane, d.wr = warp / kDownSub, d.r = lane >> 2, d.t = lane & 3;
-    d.G = A.down.G, d.blocks = L.blocks, d.bstep = subs;
-    d.wrow = (int64_t)tile * kDownRows + d.wr * 16;
-    d.pb = rank * kDownSub + sub;
-    d.ps = 0;
+    build_list<kMoeThreads>(L, A);
+    Down d{A, L, slot_w, sum + warp * sums, sm_addr(ring) + (uint32_t)(warp * kDownStages * Down::kStage)};
+    d.lane = lane, d.r = lane >> 2, d.t = lane & 3;
+    d.G = A.down.G;
+    d.step = C * kMoeWarps;
+    // blocks fewer than the warps that share them: their groups are split too
+    d.KS = max(1, min(d.G, d.step / max(1, L.blocks)));
+    d.tasks = L.blocks * d.KS;
+    d.wrow = (int64_t)tile * kDownRows;
+    d.tile2 = 16 * A.down.rb;
+    const int q0 = rank * kMoeWarps + warp;
+    d.pq = q0;
     d.to = d.from = d.base;
     d.codes.init(A.down, lane);
     d.seek();
-    for (int i = 0; i < kStages - 1; ++i) d.issue();
-    for (int b = threadIdx.x; b < L.blocks; b += kDownThreads) {
+    for (int i = 0; i < kDownStages - 1; ++i) d.issue();
+    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
         const uint32_t blk = L.blk[b];
         for (int i = 0; i < blk_count(blk); ++i) {
             const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
@@ -679,15 +692,15 @@ __global__ void __launch_bounds__(kDownThreads, 4) k_moe_down(const __grid_const
             slot_w[slot] = w;
         }
     }
-    for (int i = threadIdx.x; i < kDownSub * A.T * kDownRows; i += kDownThreads) sum[i] = 0.f;
+    for (int i = threadIdx.x; i < kMoeWarps * sums; i += kMoeThreads) sum[i] = 0.f;
     __syncthreads();
     pdl_wait();
-    for (int b = rank * kDownSub + sub; b < L.blocks; b += subs) {
+    for (int q = q0; q < d.tasks; q += d.step) {
+        int b, g0, g1;
+        d.range(q, b, g0, g1);
         const uint32_t blk = L.blk[b];
-        const int count = blk_count(blk);
-        if (count <= 4) d.template block<1, 1>(blk);
-        else if (count <= 8) d.template block<2, 1>(blk);
-        else d.template block<2, 2>(blk);
+        if (blk_count(blk) > 8) d.template block<2>(blk, g0, g1);
+        else d.template block<1>(blk, g0, g1);
     }
     cp_wait_groups<0>();
     if (C > 1) {
@@ -696,24 +709,26 @@ __global__ void __launch_bounds__(kDownThreads, 4) k_moe_down(const __grid_const
     } else {
         __syncthreads();
     }
-    // the ranks' sums in rank order; rank q finishes tokens q, q + C, ...
+    // the warps' sums, rank by rank; rank q finishes tokens q, q + C, ...
     const uint32_t sum_s = sm_addr(sum);
-    for (int i = threadIdx.x; i < A.T * kDownRows; i += kDownThreads) {
+    for (int i = threadIdx.x; i < sums; i += kMoeThreads) {
         const int tok = i / kDownRows, row = i - tok * kDownRows;
         if (tok % C != rank) continue;
         float v = 0.f;
-        for (int q = 0; q < subs; ++q) {
-            const int j = q % kDownSub * A.T * kDownRows + i;
-            float pq;
-            if (C > 1)
-                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                             : "=f"(pq)
-                             : "r"(map_rank(sum_s + 4 * j, (uint32_t)(q / kDownSub)))
-                             : "memory");
-            else
-                pq = sum[j];
-            v += pq;
-        }
+        for (int q = 0; q < C; ++q)
+#pragma unroll
+            for (int w = 0; w < kMoeWarps; ++w) {
+                const int j = w * sums + i;
+                float pq;
+                if (C > 1)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(pq)
+                                 : "r"(map_rank(sum_s + 4 * j, (uint32_t)q))
+                                 : "memory");
+                else
+                    pq = sum[j];
+                v += pq;
+            }
         const int64_t at = (int64_t)tok * A.ldy + (int64_t)tile * kDownRows + row;
         if (A.ydt == kF32) static_cast<float*>(A.y)[at] = v;
         else static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(v);
@@ -771,7 +786,7 @@ MoeMat make_mat(const MoeWeights& w, int64_t K) {
 
 }  // namespace
 
-size_t moe_data_bytes(int64_t T, int k, int64_t I) { return (size_t)((T * k * I * 4 + 255) / 256 * 256); }
+size_t moe_data_bytes(int64_t T, int k, int64_t I) { return (size_t)((T * k * I * 2 + 255) / 256 * 256); }
 
 cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWeights& down, int E, int64_t H, int64_t I,
                        const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int T, int k, void* y,
@@ -786,8 +801,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.x = x;
     A.ids = ids;
     A.weights = weights;
-    A.h_hi = static_cast<uint16_t*>(data);
-    A.h_lo = A.h_hi + (int64_t)T * k * I;
+    A.h = static_cast<uint16_t*>(data);
     A.y = y;
     A.ldx = ldx;
     A.ldy = ldy;
@@ -801,19 +815,32 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     const int64_t units = (int64_t)std::min(T * k, E + T * k / kBlockTokens) * (I / 16);
     A.S = 1;
     while (A.S < kMoeWarps && units * A.S < (int64_t)sms * 16 && A.gate.G >= 2 * A.S) A.S *= 2;
-    A.C = 8;
     A.hperm = A.down.kind == 2 ? 1 : 0;
     const KernelOf ku = up_kernel(A.gate.kind, A.up.kind), kd = down_kernel(A.down.kind);
     const int up_smem = ku.ring + (A.S > 1 ? 2 * kMoeWarps * (T > 8 ? 2 : 1) * 1024 : 0);
-    const int down_smem = kd.ring + T * kDownSub * kDownRows * 4;
+    const int down_smem = kd.ring + T * kMoeWarps * kDownRows * 4;
     cudaError_t e = cudaFuncSetAttribute(ku.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kd.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) return e;
-    int per_sm = 0;
+    int per_sm = 0, down_per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ku.fn, kMoeThreads, (size_t)up_smem);
     if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&down_per_sm, kd.fn, kMoeThreads, (size_t)down_smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1 || down_per_sm < 1) return cudaErrorInvalidConfiguration;
+    // CTAs per cluster of the down kernel: the count whose waves, each as long as a warp's share of the blocks that
+    // the tokens are expected to fill (in sixteenths of a block), end first
+    const double filled = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T)) + T * k / (double)(2 * kBlockTokens);
+    double best = 0;
+    for (int c = 1; c <= 8; ++c) {
+        const int64_t waves = (H / kDownRows * c + (int64_t)sms * down_per_sm - 1) / ((int64_t)sms * down_per_sm);
+        const double cost = (double)waves * (std::ceil(16 * filled / (c * kMoeWarps)) + 4);
+        if (c == 1 || cost < best) {
+            best = cost;
+            A.C = c;
+        }
+    }
     const int64_t ctas = std::min<int64_t>((units * A.S + kMoeWarps - 1) / kMoeWarps, (int64_t)sms * per_sm);
 
     cudaLaunchConfig_t cfg;
@@ -830,7 +857,6 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     e = cudaLaunchKernelExC(&cfg, ku.fn, args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
-    cfg.blockDim = dim3(kDownThreads);
     cfg.dynamicSmemBytes = (size_t)down_smem;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

@@ -447,12 +447,12 @@ typedef struct {
     int64_t H, I;                                         /* positive multiples of 128, at most 2^20 */
 } tb_moe_t;
 
-/* Workspace bytes of tb_moe: 2 * ceil256(4 T k I) (data only); 0 for bad
+/* Workspace bytes of tb_moe: 2 * ceil256(2 T k I) (data only); 0 for bad
  * arguments. */
 TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
 
 /* The routed experts of T tokens in two launches:
- *     h = silu(Wgate[e] x[t]) * (Wup[e] x[t]),  y[t] = sum_j weights[t][j] Wdown[e] h,  e = ids[t][j].
+ *     h = bf16(silu(Wgate[e] x[t]) * (Wup[e] x[t])),  y[t] = sum_j weights[t][j] Wdown[e] h,  e = ids[t][j].
  *   layer      HOST descriptor.
  *   x          [T][ldx] bf16, ldx >= H, ldx % 8 == 0, 16-byte aligned; finite,
  *              |x| < 2^120; 1 <= T <= TB_MOE_MAX_TOKENS.
@@ -463,12 +463,12 @@ TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
  *   weights    [T][k] fp32.
  *   y          [T][ldy] fp32 or bf16, ldy >= H, written for columns < H.
  *   workspace  tb_moe_workspace_bytes(layer, T, k) bytes (rules above).
- * Codes (times their scale, for MX4) are decoded exactly, sums are fp32, h
- * keeps 16 significant bits; bitwise deterministic.  With u = 2^-24 and A(v)
+ * Codes (times their scale, for MX4) are decoded exactly, sums are fp32;
+ * bitwise deterministic.  With u = 2^-24 and A(v)
  * the same sums over absolute values:
  *     |dg|, |du| <= (H/8 + 16) u A(x),
- *     |dh| <= 1.1 |dg| (|u| + |du|) + |silu(g)| |du| + 2^-16 |h|,
- *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/4 + k + 16) u A_down(|h| + |dh|))
+ *     |dh| <= 1.1 |dg| (|u| + |du|) + |silu(g)| |du| + 2^-8 |h|,
+ *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/8 + k + 24) u A_down(|h| + |dh|))
  * (plus 2^-8 |y| for bf16 outputs). */
 TB_API tb_status_t tb_moe(const tb_moe_t *layer, const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
                           int64_t T, int k, void *y, tb_dtype_t y_dtype, int64_t ldy, void *workspace,

@@ -111,9 +111,9 @@ def moe(wg, wu, wd, E, x, ids, weights):
             dg, du = ((H / 8 + 16) * u * (m.abs() @ x[t].abs()) for m in (G, U))
             s = g / (1 + torch.exp(-g))
             h = s * up
-            dh = 1.1 * dg * (up.abs() + du) + s.abs() * du + 2.0 ** -16 * h.abs()
+            dh = 1.1 * dg * (up.abs() + du) + s.abs() * du + 2.0 ** -8 * h.abs()
             y[t] += weights[t, j] * (D @ h)
-            tol[t] += weights[t, j].abs() * (D.abs() @ dh + (I / 4 + k + 16) * u * (D.abs() @ (h.abs() + dh)))
+            tol[t] += weights[t, j].abs() * (D.abs() @ dh + (I / 8 + k + 24) * u * (D.abs() @ (h.abs() + dh)))
     return y, tol
 
 

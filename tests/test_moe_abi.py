@@ -30,7 +30,7 @@ def layer(**kw):
 
 def test_workspace(lib):
     for T, k, I in ((1, 1, 128), (1, 8, 768), (64, 16, 1536), (7, 3, 640)):
-        want = 2 * (-(-4 * T * k * I // 256) * 256)
+        want = 2 * (-(-2 * T * k * I // 256) * 256)
         assert lib.tb_moe_workspace_bytes(ctypes.addressof(l := layer(I=I, E=16)), T, k) == want, l
     assert lib.tb_moe_workspace_bytes(0, 1, 1) == 0
     assert lib.tb_moe_workspace_bytes(ctypes.addressof(l := layer()), 65, 1) == 0
@@ -46,7 +46,7 @@ def test_moe_refusals(lib):
     for n in ("gate_grid", "up_grid", "down_grid"):
         assert f(**{n: 3}) == UNSUPPORTED and f(**{n: 5}) == ARG and f(**{n: -1}) == ARG
     assert f(k=0) == ARG and f(k=17) == ARG and f(E=0) == ARG and f(E=513) == ARG and f(dt=2) == ARG
-    assert f(nws=2 * 4096 - 1) == ARG
+    assert f(nws=2 * 2048 - 1) == ARG
     assert f(T=0) == SHAPE and f(T=65) == SHAPE and f(H=200) == SHAPE and f(I=64) == SHAPE and f(I=0) == SHAPE
     assert f(H=(1 << 20) + 128, ldx=1 << 21, ldy=1 << 21) == SHAPE and f(ldx=248) == SHAPE and f(ldy=255) == SHAPE
     assert f(x=A + 8) == ALIGN and f(ldx=260) == ALIGN and f(ids=A + 2) == ALIGN and f(w=A + 1) == ALIGN
