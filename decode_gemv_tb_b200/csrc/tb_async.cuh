@@ -93,12 +93,15 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 // ---- tcgen05 -------------------------------------------------------------------------
 __device__ __forceinline__ void tc5_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc5_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// the tcgen05 work issued so far by the warp's elected lane, once complete, arrives on bar
-__device__ __forceinline__ void tc5_commit(uint32_t bar) {
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
-        : "memory");
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(p));
+    return p != 0;
+}
+// the tcgen05 work issued so far by this thread, once complete, arrives on bar
+__device__ __forceinline__ void tc5_commit_one(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // 16 consecutive columns of this thread's TMEM lane; the registers are valid after tc5_ld_done
 __device__ __forceinline__ void tc5_ld16(uint32_t taddr, uint32_t (&r)[16]) {

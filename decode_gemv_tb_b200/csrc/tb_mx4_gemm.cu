@@ -94,18 +94,14 @@ __host__ __device__ constexpr uint32_t mx_idesc(int nt, int id) {
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                        uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred e, p;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %6, 0;\n"
-        " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
         : "memory");
 }
 // a scale tile from shared memory to four columns of all four 32-lane parts of tensor memory
 __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(taddr),
-        "l"(desc)
-        : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 template <class C>
@@ -116,7 +112,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
     __shared__ uint32_t tmem_sh;
     __shared__ int abort_sh;
     volatile int* abort = &abort_sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (sm_addr(smem_raw) + 1023u) & ~1023u;
     const uint32_t red = base + ST * C::kStage;  // S > 1: partial sums [source rank][column of the slice][row]
     const uint32_t rank = S > 1 ? cluster_rank() : 0u;
@@ -143,7 +139,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
     __syncthreads();
     tc5_fence_after();
     if (S > 1) cluster_arrive();  // every CTA of the cluster has begun before any writes into another
-    const uint32_t tmem = tmem_sh;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
     int issued = 0, committed = 0;
 
     if (warp == 0) {
@@ -176,43 +172,52 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA ----------------
-        bool ok = true;
-        int n = 0;
-        for (uint32_t u = cid; u < A.units && ok; u += ncl, ++n) {
-            if (n > 0 && !__all_sync(0xffffffffu, mb_wait(sm_addr(&dfree), (uint32_t)(n - 1) & 1u, A.wait_cycles,
-                                                          abort, &g_mx_timeouts)))
-                break;
-            for (int c = c0; c < c1; ++c) {
-                const int s = committed % ST;
-                if (!__all_sync(0xffffffffu, mb_wait(sm_addr(&full[s]), (uint32_t)(committed / ST) & 1u,
-                                                     A.wait_cycles, abort, &g_mx_timeouts))) {
-                    ok = false;
+        // ---------------- MMA: one elected lane waits and issues ----------------
+        if (elect_one()) {
+            bool ok = true;
+            int n = 0, s = 0;
+            uint32_t phase = 0;
+            for (uint32_t u = cid; u < A.units && ok; u += ncl, ++n) {
+                if (n > 0 && !mb_wait(sm_addr(&dfree), (uint32_t)(n - 1) & 1u, A.wait_cycles, abort, &g_mx_timeouts))
                     break;
-                }
-                tc5_fence_after();
-                const uint32_t sa = base + s * C::kStage, sb = sa + kABytes, sf = sb + C::kB;
-                const uint32_t ta = tmem + C::kDCols + s * C::kSfCols, tb = ta + 8;
-                const int left = A.K - c * kChunkK;
-                const int nk = left >= 256 ? 4 : (left + 63) >> 6;
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
-                    if (kt * 2 < nk) {
-                        cp_scales(ta + kt * 4, desc_scales(sf + kt * 512));
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            cp_scales(tb + kt * 4 * NB + nb * 4, desc_scales(sf + 1024 + nb * 1024 + kt * 512));
+                for (int c = c0; c < c1; ++c) {
+                    if (!mb_wait(sm_addr(&full[s]), phase, A.wait_cycles, abort, &g_mx_timeouts)) {
+                        ok = false;
+                        break;
                     }
+                    tc5_fence_after();
+                    const uint32_t sa = base + s * C::kStage, sb = sa + kABytes, sf = sb + C::kB;
+                    const uint32_t ta = tmem + C::kDCols + s * C::kSfCols, tb = ta + 8;
+                    const int left = A.K - c * kChunkK;
+                    const int nk = left >= 256 ? 4 : (left + 63) >> 6;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < nk)
-                        mma_mx(tmem, desc_sw128(sa + j * 32), desc_sw128(sb + j * 32), mx_idesc(NT, 2 * (j & 1)),
-                               ta + (j >> 1) * 4, tb + (j >> 1) * 4 * NB, (c > c0 || j > 0) ? 1u : 0u);
-                tc5_commit(sm_addr(&empty[s]));
-                ++committed;
+                    for (int kt = 0; kt < 2; ++kt)
+                        if (kt * 2 < nk) {
+                            cp_scales(ta + kt * 4, desc_scales(sf + kt * 512));
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                cp_scales(tb + kt * 4 * NB + nb * 4, desc_scales(sf + 1024 + nb * 1024 + kt * 512));
+                        }
+                    const uint64_t da = desc_sw128(sa), db = desc_sw128(sb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < nk)
+                            mma_mx(tmem, da + 2 * j, db + 2 * j, mx_idesc(NT, 2 * (j & 1)), ta + (j >> 1) * 4,
+                                   tb + (j >> 1) * 4 * NB, (c > c0 || j > 0) ? 1u : 0u);
+                    tc5_commit_one(sm_addr(&empty[s]));
+                    ++committed;
+                    if (++s == ST) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) tc5_commit_one(sm_addr(&dfull));
             }
-            if (ok) tc5_commit(sm_addr(&dfull));
+            // what is in flight ends before the exit (every commit follows the ones before it)
+            if (*abort != 0 && committed > 0)
+                mb_drain(sm_addr(&empty[(committed - 1) % ST]), (uint32_t)((committed - 1) / ST) & 1u, A.wait_cycles);
         }
+        __syncwarp();
     } else {
         // ---------------- epilogue: rows 32 (warp % 4) .. + 31, columns EC e .. + EC - 1 ----------------
         constexpr int EC = NT / (C::EPI / 4);
@@ -298,8 +303,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         if (warp == 0 && lane == 0)
             for (int k = issued > ST ? issued - ST : 0; k < issued; ++k)
                 mb_drain(sm_addr(&full[k % ST]), (uint32_t)(k / ST) & 1u, A.wait_cycles);
-        if (warp == 1 && committed > 0)
-            mb_drain(sm_addr(&empty[(committed - 1) % ST]), (uint32_t)((committed - 1) / ST) & 1u, A.wait_cycles);
     }
     tc5_fence_before();
     __syncthreads();
