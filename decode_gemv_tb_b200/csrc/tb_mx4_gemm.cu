@@ -69,10 +69,9 @@ struct MxCfg {
     static_assert(kCols <= 512 && kStage % 1024 == 0, "tensor memory, swizzle atoms");
 };
 using Mx16 = MxCfg<16, 4, 4>;
-using Mx32 = MxCfg<32, 4, 4>;
-using Mx64 = MxCfg<64, 3, 4>;
-using Mx128 = MxCfg<128, 4, 4>;
-using Mx256 = MxCfg<256, 4, 8>;
+using Mx32 = MxCfg<32, 4, 8>;
+using Mx64 = MxCfg<64, 3, 8>;
+using Mx128 = MxCfg<128, 4, 8>;
 
 constexpr float kMxNaN = __builtin_nanf("");
 
@@ -223,20 +222,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         constexpr int EC = NT / (C::EPI / 4);
         const int e = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
         const uint32_t tcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(e * EC);
+        const int lg = 31 - __clz(NT / S);  // S > 1: columns of a rank's slice, as a shift
         int n = 0;
         bool failed = false;
         for (uint32_t u = cid; u < A.units; u += ncl, ++n) {
             const uint32_t t = u / (uint32_t)A.MB, b = u - t * (uint32_t)A.MB;
             const int64_t row = (int64_t)t * kRows + r;
-            const int m0 = (int)b * NT, mcount = min(NT, A.M - m0);
+            const int m0 = (int)b * NT + e * EC, count = min(EC, A.M - m0);  // this warp's columns
             if (!failed)
                 failed = !__all_sync(0xffffffffu, mb_wait(sm_addr(&dfull), (uint32_t)n & 1u, A.wait_cycles, abort,
                                                           &g_mx_timeouts));
             tc5_fence_after();
             if (S > 1) cluster_wait();
+            const int64_t at = (int64_t)m0 * A.ldy + row;
+            float* yf = static_cast<float*>(A.Y) + at;
+            __nv_bfloat16* yb = static_cast<__nv_bfloat16*>(A.Y) + at;
 #pragma unroll 1
-            for (int cc = 0; cc < EC; cc += 16) {
-                if (e * EC + cc >= mcount) break;
+            for (int cc = 0; cc < count; cc += 16) {
                 uint32_t v[16];
                 if (!failed) {
                     tc5_ld16(tcol + cc, v);
@@ -247,25 +249,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
                     for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(kMxNaN);
                 }
                 if (S > 1) {
-                    // column m of this rank's partial sums goes to rank m / (NT / S)
-                    const uint32_t cw = (uint32_t)NT / (uint32_t)S;
+                    // a column of this rank's partial sums goes to the rank whose slice it is in
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint32_t m = (uint32_t)(e * EC + cc + i), to = m / cw;
-                        if ((int)m < mcount)
-                            st_cluster_f32(map_rank(red + (((rank * cw + m - to * cw) * kRows + (uint32_t)r) << 2), to),
+                        const uint32_t m = (uint32_t)(e * EC + cc + i), to = m >> lg;
+                        if (cc + i < count)
+                            st_cluster_f32(map_rank(red + ((((rank - to) << lg) + m) * kRows + (uint32_t)r) * 4, to),
                                            __uint_as_float(v[i]));
                     }
                 } else if (row < A.N) {
-                    const int64_t at = (int64_t)(m0 + e * EC + cc) * A.ldy + row;
+                    if (A.ydt == kF32) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (e * EC + cc + i < mcount) {
-                            if (A.ydt == kF32) static_cast<float*>(A.Y)[at + i * A.ldy] = __uint_as_float(v[i]);
-                            else
-                                static_cast<__nv_bfloat16*>(A.Y)[at + i * A.ldy] =
-                                    __float2bfloat16_rn(__uint_as_float(v[i]));
-                        }
+                        for (int i = 0; i < 16; ++i, yf += A.ldy)
+                            if (cc + i < count) *yf = __uint_as_float(v[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, yb += A.ldy)
+                            if (cc + i < count) *yb = __float2bfloat16_rn(__uint_as_float(v[i]));
                     }
                 }
             }
@@ -283,17 +283,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         cluster_wait();
         if (warp >= 2) {
             const uint32_t t = cid / (uint32_t)A.MB, b = cid - t * (uint32_t)A.MB;
-            const int r = 32 * (warp & 3) + lane, cw = NT / S;
-            const int64_t row = (int64_t)t * kRows + r;
+            const int e = (warp - 2) >> 2, r = 32 * (warp & 3) + lane, cw = NT / S;
+            const int64_t row = (int64_t)t * kRows + r, m0 = (int64_t)b * NT + (int64_t)rank * cw;
+            const int count = (int)min((int64_t)cw, (int64_t)A.M - m0);
             const float* p = reinterpret_cast<const float*>(smem_raw + (red - sm_addr(smem_raw))) + r;
-            for (int c = 0; c < cw; ++c) {
-                const int64_t m = (int64_t)b * NT + (int64_t)rank * cw + c;
-                if (m >= A.M || row >= A.N) break;
-                float sum = 0.f;
-                for (int q = 0; q < S; ++q) sum += p[(q * cw + c) * kRows];
-                if (A.ydt == kF32) static_cast<float*>(A.Y)[m * A.ldy + row] = sum;
-                else static_cast<__nv_bfloat16*>(A.Y)[m * A.ldy + row] = __float2bfloat16_rn(sum);
-            }
+            if (row < A.N)
+                for (int c = e; c < count; c += C::EPI / 4) {
+                    float sum = 0.f;
+                    for (int q = 0; q < S; ++q) sum += p[(q * cw + c) * kRows];
+                    const int64_t at = (m0 + c) * A.ldy + row;
+                    if (A.ydt == kF32) static_cast<float*>(A.Y)[at] = sum;
+                    else static_cast<__nv_bfloat16*>(A.Y)[at] = __float2bfloat16_rn(sum);
+                }
         }
     }
 
@@ -311,6 +312,249 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kTmem)
                      : "memory");
 }
+
+// ---- prefill: batches of whole tiles -----------------------------------------------------
+// The same product with the roles exchanged: X's rows are the MMA's A (128 of them) and W's its B (NW = 128 or 256), so
+// a thread of the epilogue holds consecutive outputs of a batch row.  They are rounded into a swizzled tile of shared
+// memory and leave by tensor stores while the next unit's MMAs run (the accumulator is free as soon as it has been
+// read; its 256 columns and the scales leave no room for a second one).  Y's rows and their used part have to be
+// multiples of 16 bytes.
+constexpr int kPreEpi = 8;
+constexpr int kPreThreads = (2 + kPreEpi) * 32;
+constexpr int kPreOut = 65536;  // staged outputs: 128 rows x 256 bf16 or 128 fp32
+
+template <int NW_, int STAGES_>
+struct PreCfg {
+    static constexpr int NW = NW_, STAGES = STAGES_;
+    static constexpr int NB = NW / 128;
+    static constexpr int kB = NW * kChunkK / 2;
+    static constexpr int kStage = kABytes + kB + 1024 + 1024 * NB;
+    static constexpr int kSfCols = 8 + 8 * NB;
+    static constexpr int kTmem = NW + STAGES * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kOut = NW == 256 ? kPreOut : kPreOut / 2;
+    static constexpr int kSmem = STAGES * kStage + kOut + 1024;
+    static_assert(NW + STAGES * kSfCols <= 512 && kSmem + 1024 <= 227 * 1024, "tensor and shared memory");
+};
+
+struct PreArgs {
+    CUtensorMap xmap, wmap;  // codes, boxes {128, 128} and {128, NW}
+    CUtensorMap ymap;        // outputs: {N, M}, box {128 bytes, 128 rows}, 128-byte swizzle
+    const uint8_t* xsf;
+    const uint8_t* wsf;
+    long long wait_cycles;
+    int64_t N;
+    int32_t M, K, KC, KT, TW, ydt, stall;  // TW: tiles of W
+    uint32_t units, group;                 // units run over the batch tiles within groups of W tiles
+};
+
+template <class C>
+__global__ void __launch_bounds__(kPreThreads, 1) k_mx4_prefill(const __grid_constant__ PreArgs A) {
+    constexpr int NW = C::NW, ST = C::STAGES, NB = C::NB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[ST], empty[ST], dfull, dfree;
+    __shared__ uint32_t tmem_sh;
+    __shared__ int abort_sh;
+    volatile int* abort = &abort_sh;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t base = (sm_addr(smem_raw) + 1023u) & ~1023u, out = base + ST * C::kStage;
+    const uint32_t MB = (uint32_t)((A.M + kRows - 1) / kRows);
+    // unit u: groups of A.group tiles of W, in a group every batch tile with each of its tiles
+    auto place = [&](uint32_t u, uint32_t& m, uint32_t& w) {
+        const uint32_t per = A.group * MB, g = u / per, in = u - g * per;
+        const uint32_t width = min(A.group, (uint32_t)A.TW - g * A.group);
+        m = in / width;
+        w = g * A.group + in - m * width;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mb_init(sm_addr(&full[s]), 1);
+            mb_init(sm_addr(&empty[s]), 1);
+        }
+        mb_init(sm_addr(&dfull), 1);
+        mb_init(sm_addr(&dfree), kPreEpi);
+        abort_sh = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&tmem_sh)),
+                     "r"((uint32_t)C::kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc5_fence_before();
+    __syncthreads();
+    tc5_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
+    int issued = 0;
+
+    if (warp == 0) {
+        // ---------------- producer ----------------
+        if (lane == 0 && !A.stall) {
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; u < A.units && ok; u += gridDim.x) {
+                uint32_t m, w;
+                place(u, m, w);
+                const bool two = NB == 2 && (int64_t)w * NW + 128 < A.N;
+                const uint8_t* xs = A.xsf + (int64_t)m * A.KT * 512;
+                const uint8_t* ws = A.wsf + (int64_t)w * NB * A.KT * 512;
+                for (int c = 0; c < A.KC; ++c) {
+                    const int s = issued % ST;
+                    if (issued >= ST && !mb_wait(sm_addr(&empty[s]), (uint32_t)(issued / ST - 1) & 1u, A.wait_cycles,
+                                                 abort, &g_mx_timeouts)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = base + s * C::kStage, bar = sm_addr(&full[s]), sf = st + kABytes + C::kB;
+                    const uint32_t sfb = 512u * (uint32_t)min(2, A.KT - 2 * c);
+                    mb_arrive_expect(bar, (uint32_t)(kABytes + C::kB) + sfb * (two ? 3u : 2u));
+                    tma_load_2d(st, &A.xmap, c * (kChunkK / 2), (int)(m * kRows), bar);
+                    tma_load_2d(st + kABytes, &A.wmap, c * (kChunkK / 2), (int)(w * NW), bar);
+                    bulk_load(sf, xs + (int64_t)c * 1024, sfb, bar);
+                    bulk_load(sf + 1024, ws + (int64_t)c * 1024, sfb, bar);
+                    if (two) bulk_load(sf + 2048, ws + ((int64_t)A.KT + 2 * c) * 512, sfb, bar);
+                    ++issued;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA ----------------
+        if (elect_one()) {
+            bool ok = true;
+            int n = 0, s = 0, last = -1;
+            uint32_t phase = 0;
+            for (uint32_t u = blockIdx.x; u < A.units && ok; u += gridDim.x, ++n) {
+                if (n > 0 && !mb_wait(sm_addr(&dfree), (uint32_t)(n - 1) & 1u, A.wait_cycles, abort, &g_mx_timeouts))
+                    break;
+                for (int c = 0; c < A.KC; ++c) {
+                    if (!mb_wait(sm_addr(&full[s]), phase, A.wait_cycles, abort, &g_mx_timeouts)) {
+                        ok = false;
+                        break;
+                    }
+                    tc5_fence_after();
+                    const uint32_t sa = base + s * C::kStage, sb = sa + kABytes, sf = sb + C::kB;
+                    const uint32_t ta = tmem + NW + s * C::kSfCols, tb = ta + 8;
+                    const int left = A.K - c * kChunkK;
+                    const int nk = left >= 256 ? 4 : (left + 63) >> 6;
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt)
+                        if (kt * 2 < nk) {
+                            cp_scales(ta + kt * 4, desc_scales(sf + kt * 512));
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                cp_scales(tb + kt * 4 * NB + nb * 4, desc_scales(sf + 1024 + nb * 1024 + kt * 512));
+                        }
+                    const uint64_t da = desc_sw128(sa), db = desc_sw128(sb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < nk)
+                            mma_mx(tmem, da + 2 * j, db + 2 * j, mx_idesc(NW, 2 * (j & 1)), ta + (j >> 1) * 4,
+                                   tb + (j >> 1) * 4 * NB, (c > 0 || j > 0) ? 1u : 0u);
+                    tc5_commit_one(sm_addr(&empty[s]));
+                    last = s | (int)phase << 8;
+                    if (++s == ST) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) tc5_commit_one(sm_addr(&dfull));
+            }
+            if (*abort != 0 && last >= 0)
+                mb_drain(sm_addr(&empty[last & 255]), (uint32_t)last >> 8, A.wait_cycles);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue ----------------
+        const int e = (warp - 2) >> 2, r = 32 * (warp & 3) + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const int per = A.ydt == kF32 ? 32 : 64;                  // outputs of a 128-byte row of a box
+        const int cp = C::kOut / 128 / (A.ydt == kF32 ? 4 : 2);  // columns staged at once
+        const uint32_t rowp = out + (uint32_t)r * 128u;
+        const uint32_t sw = (uint32_t)(r & 7);
+        int n = 0;
+        bool failed = false, pending = false;
+        for (uint32_t u = blockIdx.x; u < A.units; u += gridDim.x, ++n) {
+            uint32_t m, w;
+            place(u, m, w);
+            if (!failed)
+                failed = !__all_sync(0xffffffffu, mb_wait(sm_addr(&dfull), (uint32_t)n & 1u, A.wait_cycles, abort,
+                                                          &g_mx_timeouts));
+            tc5_fence_after();
+            for (int c0 = 0; c0 < NW; c0 += cp) {
+                // the stores of what was staged before have read it
+                if (pending && warp == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(kPreEpi * 32) : "memory");
+#pragma unroll 1
+                for (int cc = e * (cp / 2); cc < (e + 1) * (cp / 2); cc += 32) {  // columns c0 + cc .. + 31
+                    uint32_t v[2][16];
+                    if (!failed) {
+                        tc5_ld16(lanes + (uint32_t)(c0 + cc), v[0]);
+                        tc5_ld16(lanes + (uint32_t)(c0 + cc + 16), v[1]);
+                        tc5_ld_wait();
+                        tc5_ld_done(v[0]);
+                        tc5_ld_done(v[1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = __float_as_uint(kMxNaN);
+                    }
+                    const uint32_t box = rowp + (uint32_t)(cc / per) * 16384u;
+                    if (A.ydt == kF32) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_v4(box + (((uint32_t)q ^ sw) << 4), v[q >> 2][4 * (q & 3)], v[q >> 2][4 * (q & 3) + 1],
+                                         v[q >> 2][4 * (q & 3) + 2], v[q >> 2][4 * (q & 3) + 3]);
+                    } else {
+                        const uint32_t p0 = (uint32_t)(cc & 63) >> 3;  // 16-byte piece of the row: 0 or 4
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t b[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = 8 * (q & 1) + 2 * i;
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[q >> 1][j]),
+                                                                               __uint_as_float(v[q >> 1][j + 1]));
+                                b[i] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                            st_shared_v4(box + (((p0 + (uint32_t)q) ^ sw) << 4), b[0], b[1], b[2], b[3]);
+                        }
+                    }
+                }
+                if (c0 + cp >= NW) {  // the accumulator has been read
+                    tc5_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(sm_addr(&dfree));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(kPreEpi * 32) : "memory");
+                if (warp == 2 && lane == 0) {
+                    for (int b = 0; b < cp / per; ++b) {
+                        const int64_t x = (int64_t)w * NW + c0 + b * per;
+                        if (x < A.N) tma_store_2d(&A.ymap, (int)x, (int)(m * kRows), out + (uint32_t)b * 16384u);
+                    }
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+                pending = true;
+            }
+        }
+        if (pending && warp == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        tc5_fence_before();
+    }
+
+    // ---------------- drain and exit ----------------
+    const bool aborted = __syncthreads_or(*abort) != 0;
+    if (aborted && warp == 0 && lane == 0)
+        for (int k = issued > ST ? issued - ST : 0; k < issued; ++k)
+            mb_drain(sm_addr(&full[k % ST]), (uint32_t)(k / ST) & 1u, A.wait_cycles);
+    tc5_fence_before();
+    __syncthreads();
+    tc5_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kTmem)
+                     : "memory");
+}
+
+using Pre256 = PreCfg<256, 3>;
+using Pre128 = PreCfg<128, 5>;
 
 int mx_sms() {
     static int sms[64] = {0};
@@ -338,14 +582,14 @@ bool encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, 
 
 template <class C>
 cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
-    // CTAs per unit: the split whose waves of chunks (plus about three chunks' time to start and finish a
-    // CTA) are the shortest
+    // CTAs per unit: the split whose waves of chunks are the shortest, with about three chunks' time to start and
+    // finish a CTA and four more to add a cluster's partial sums
     int S = 1;
     int64_t best = -1;
     for (int s = 1; s <= 8 && s <= A.KC && s <= C::NT / 2; s *= 2) {
         const int64_t slots = (int64_t)sms * C::per_sm(s);
         if (slots == 0 || (s > 1 && units * s > slots)) break;
-        const int64_t cost = (units * s + slots - 1) / slots * ((A.KC + s - 1) / s + 3);
+        const int64_t cost = (units * s + slots - 1) / slots * ((A.KC + s - 1) / s + 3) + (s > 1 ? 4 : 0);
         if (best < 0 || cost < best) {
             best = cost;
             S = s;
@@ -355,7 +599,7 @@ cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
     A.units = (uint32_t)units;
     const void* fn = reinterpret_cast<const void*>(&k_mx4_gemm<C>);
     const int smem = C::smem(S);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2) <= 227 * 1024 ? C::smem(2) : C::smem(1));
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
@@ -373,6 +617,37 @@ cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// outputs: rows of N, boxes of 128 bytes x 128 rows
+bool encode_out(CUtensorMap* map, void* Y, int ydt, int64_t ldy, int64_t M, int64_t N) {
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int es = ydt == kF32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ldy * es)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / es), kRows};
+    const cuuint32_t el[2] = {1, 1};
+    return enc(map, ydt == kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, dims,
+               strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class C>
+cudaError_t launch_prefill(PreArgs& A, const void* w, const void* x, int64_t K, cudaStream_t st, int sms) {
+    A.TW = (int32_t)((A.N + C::NW - 1) / C::NW);
+    const int64_t units = (int64_t)A.TW * ((A.M + kRows - 1) / kRows);
+    if (units > 0x7FFFFFFF || !encode_codes(&A.xmap, x, A.M, K, kRows) || !encode_codes(&A.wmap, w, A.N, K, C::NW))
+        return cudaErrorInvalidValue;
+    A.units = (uint32_t)units;
+    // the units that run at once form a block of about sqrt(148) tiles of W by as many of X: what they read from L2
+    // and, at long K, from HBM is least
+    A.group = 12;
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_mx4_prefill<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    k_mx4_prefill<C><<<(unsigned)std::min<int64_t>(units, sms), kPreThreads, C::kSmem, st>>>(A);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* x, const uint8_t* x_scales, void* Y,
@@ -380,6 +655,26 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
                             cudaStream_t st) {
     const int sms = mx_sms();
     if (sms <= 0) return cudaErrorInitializationError;
+    const int64_t T = (N + kRows - 1) / kRows, es = ydt == kF32 ? 4 : 2;
+    const int64_t pre = ((M + kRows - 1) / kRows) * T;  // tiles of 128 x 128
+    if (M > 128 && pre >= sms / 2 && reinterpret_cast<uintptr_t>(Y) % 16 == 0 && ldy * es % 16 == 0 &&
+        N * es % 16 == 0) {  // tensor stores write whole 16-byte pieces of a row
+        PreArgs A;
+        std::memset(&A, 0, sizeof(A));
+        if (!encode_out(&A.ymap, Y, ydt, ldy, M, N)) return cudaErrorInvalidValue;
+        A.xsf = x_scales;
+        A.wsf = w_scales;
+        A.wait_cycles = wait_cycles;
+        A.N = N;
+        A.M = (int32_t)M;
+        A.K = (int32_t)K;
+        A.KC = (int32_t)((K + kChunkK - 1) / kChunkK);
+        A.KT = (int32_t)((K + 127) / 128);
+        A.ydt = ydt;
+        A.stall = stall ? 1 : 0;
+        if (pre >= 2 * sms) return launch_prefill<Pre256>(A, w, x, K, st, sms);
+        return launch_prefill<Pre128>(A, w, x, K, st, sms);
+    }
     MxArgs A;
     std::memset(&A, 0, sizeof(A));
     A.wsf = w_scales;
@@ -394,9 +689,7 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
     A.KT = (int32_t)((K + 127) / 128);
     A.ydt = ydt;
     A.stall = stall ? 1 : 0;
-    const int64_t T = (N + kRows - 1) / kRows;
-    int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
-    if (M > 128 && T * ((M + 255) / 256) >= sms) nt = 256;
+    const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
     A.MB = (int32_t)((M + nt - 1) / nt);
     const int64_t units = T * A.MB;
     if (units > 0x7FFFFFFF || !encode_codes(&A.wmap, w, N, K, kRows) || !encode_codes(&A.xmap, x, M, K, nt))
@@ -405,8 +698,7 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
         case 16: return launch<Mx16>(A, units, st, sms);
         case 32: return launch<Mx32>(A, units, st, sms);
         case 64: return launch<Mx64>(A, units, st, sms);
-        case 128: return launch<Mx128>(A, units, st, sms);
-        default: return launch<Mx256>(A, units, st, sms);
+        default: return launch<Mx128>(A, units, st, sms);
     }
 }
 

@@ -126,6 +126,18 @@ def test_gemm(M, N, K, dt):
     check_gemm(w, ws, x, xs, dt, extra=3 if N % 2 else 0)
 
 
+@pytest.mark.parametrize("M,N,K,extra", [(200, 6000, 288, 0), (200, 6000, 288, 8), (385, 5001, 1088, 7), (385, 5001, 1088, 8),
+                                         (1000, 4500, 96, 4), (300, 20000, 544, 4), (300, 20000, 544, 5)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gemm_prefill_tiles(M, N, K, extra, dt):
+    """Tiles of 128 and of 256 rows of W, ragged in every direction; row lengths that are multiples of 16 bytes and
+    ones that are not."""
+    rng = np.random.default_rng(M + N + K)
+    w, ws = R.random_mx4(N, K, rng)
+    x, xs = R.random_mx4(M, K, rng)
+    check_gemm(w, ws, x, xs, dt, extra)
+
+
 def test_gemm_persistent_units():
     """More units than the GPU holds at once: every CTA takes several."""
     rng = np.random.default_rng(5)
