@@ -17,8 +17,9 @@
 // costs one DFMA, two and a half integer operations per weight shared by
 // the tokens of the cluster.
 //
-// A cluster of eight CTAs handles TB tokens: its 128 warps take one expert
-// each at a time and leave the logits in the shared memory of the CTA that
+// A cluster of eight CTAs handles TB tokens: its 128 warps take two experts
+// each at a time (a token's words, the heaviest traffic, are read from shared
+// memory once for both) and leave the logits in the shared memory of the CTA that
 // selects for the token.  No workspace, no atomics.
 #include "tb_async.cuh"
 #include "tb_device.cuh"
@@ -42,7 +43,7 @@ namespace {
 constexpr int kRtCluster = 8;
 constexpr int kRtWarps = 16;
 constexpr int kRtThreads = kRtWarps * 32;
-constexpr int kRtUnroll = 4;
+constexpr int kRtUnroll = 4;  // 16-byte loads of the router in flight per lane
 
 __device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
 // high word of w 2^-896 for the bf16 in the upper half of u
@@ -118,10 +119,11 @@ __global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(kRtCluster, 1,
     const int64_t t0 = (int64_t)(blockIdx.x / kRtCluster) * TB;
     const int nt = (int)min((int64_t)TB, A.T - t0);
     cluster_arrive();
-    for (int i = threadIdx.x; i < TB * (A.H / 8); i += kRtThreads) {
-        const int t = i / (A.H / 8), h = (i - t * (A.H / 8)) * 8;
+    const int H8 = A.H / 8;  // eights of x: their first four words in one plane, the others in a second
+    for (int i = threadIdx.x; i < TB * H8; i += kRtThreads) {
+        const int t = i / H8, h = i - t * H8;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (t < nt) v = *reinterpret_cast<const uint4*>(A.x + (t0 + t) * A.ldx + h);
+        if (t < nt) v = *reinterpret_cast<const uint4*>(A.x + (t0 + t) * A.ldx + 8 * h);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         uint32_t d[8];
 #pragma unroll
@@ -129,51 +131,70 @@ __global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(kRtCluster, 1,
             d[2 * j] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] << 16));
             d[2 * j + 1] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] & 0xFFFF0000u));
         }
-        uint4* p = reinterpret_cast<uint4*>(xs + t * A.H + h);
+        uint4* p = reinterpret_cast<uint4*>(xs) + t * 2 * H8 + h;
         p[0] = make_uint4(d[0], d[1], d[2], d[3]);
-        p[1] = make_uint4(d[4], d[5], d[6], d[7]);
+        p[H8] = make_uint4(d[4], d[5], d[6], d[7]);
     }
     __syncthreads();
     cluster_wait();  // every CTA of the cluster has begun
-    for (int e = (int)rank * kRtWarps + warp; e < A.E; e += kRtCluster * kRtWarps) {
-        const uint16_t* w = A.R + (int64_t)e * A.H;
-        double acc[TB];
+    constexpr int EB = TB > 1 ? 2 : 1;  // experts of a warp's pass
+    constexpr int U = kRtUnroll / EB, kStep = kRtCluster * kRtWarps;
+    for (int e0 = (int)rank * kRtWarps + warp; e0 < A.E; e0 += EB * kStep) {
+        const uint4* w[EB];
 #pragma unroll
-        for (int t = 0; t < TB; ++t) acc[t] = 0.0;
-        for (int h0 = lane * 8; h0 < A.H; h0 += 256 * kRtUnroll) {
-            uint4 v[kRtUnroll];
+        for (int b = 0; b < EB; ++b)  // a pass without a second expert takes the first again
+            w[b] = reinterpret_cast<const uint4*>(A.R + (int64_t)(e0 + b * kStep < A.E ? e0 + b * kStep : e0) * A.H);
+        double acc[EB][TB];
 #pragma unroll
-            for (int q = 0; q < kRtUnroll; ++q)
-                v[q] = h0 + 256 * q < A.H ? __ldg(reinterpret_cast<const uint4*>(w + h0 + 256 * q))
-                                          : make_uint4(0u, 0u, 0u, 0u);
+        for (int b = 0; b < EB; ++b)
 #pragma unroll
-            for (int q = 0; q < kRtUnroll; ++q) {
-                const int h = h0 + 256 * q;
-                if (h >= A.H) break;
-                const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-                double wd[8];
+            for (int t = 0; t < TB; ++t) acc[b][t] = 0.0;
+        for (int h0 = lane; h0 < H8; h0 += 32 * U) {
+            uint4 v[U][EB];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    wd[2 * j] = from_hi(scaled_hi(u[j] << 16));
-                    wd[2 * j + 1] = from_hi(scaled_hi(u[j]));
-                }
+            for (int q = 0; q < U; ++q)
 #pragma unroll
-                for (int t = 0; t < TB; ++t) {
-                    const uint4* p = reinterpret_cast<const uint4*>(xs + t * A.H + h);
-                    const uint4 a = p[0], b = p[1];
-                    const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                for (int b = 0; b < EB; ++b)
+                    v[q][b] = h0 + 32 * q < H8 ? __ldg(w[b] + h0 + 32 * q) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[t] = fma(wd[j], from_hi(d[j]), acc[t]);
+            for (int q = 0; q < U; ++q) {
+                const int h = h0 + 32 * q;
+                if (h >= H8) break;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    double wd[EB][4];
+#pragma unroll
+                    for (int b = 0; b < EB; ++b) {
+                        const uint32_t u0 = half ? v[q][b].z : v[q][b].x, u1 = half ? v[q][b].w : v[q][b].y;
+                        wd[b][0] = from_hi(scaled_hi(u0 << 16));
+                        wd[b][1] = from_hi(scaled_hi(u0));
+                        wd[b][2] = from_hi(scaled_hi(u1 << 16));
+                        wd[b][3] = from_hi(scaled_hi(u1));
+                    }
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) {
+                        const uint4 a = reinterpret_cast<const uint4*>(xs)[(2 * t + half) * H8 + h];
+                        const double x[4] = {from_hi(a.x), from_hi(a.y), from_hi(a.z), from_hi(a.w)};
+#pragma unroll
+                        for (int b = 0; b < EB; ++b)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) acc[b][t] = fma(wd[b][j], x[j], acc[b][t]);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
+        for (int b = 0; b < EB; ++b)
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-            // 2^896: 1023 + 896 in the exponent field
-            if (lane == 0) st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), acc[t] * from_hi(1919u << 20));
-        }
+            for (int t = 0; t < TB; ++t) {
+                double s = acc[b][t];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                // 2^896: 1023 + 896 in the exponent field
+                const int e = e0 + b * kStep;
+                if (lane == 0 && e < A.E)
+                    st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), s * from_hi(1919u << 20));
+            }
     }
     __syncwarp();
     cluster_arrive();

@@ -10,10 +10,10 @@
 // instruction rounds half to even.
 //
 // Both kernels are bound by HBM: 2 or 4 bytes per weight on the wide side,
-// 0.53 on the narrow one.  A half-warp holds 128 consecutive k of a row (the
-// scale word of a row is then one 4-byte store), a thread 8 of them (one or
-// two 16-byte loads), a block of 32 four threads (two shuffles for amax);
-// kTasks consecutive 128-runs per half-warp keep that many loads in flight.
+// 0.53 on the narrow one.  A thread holds 16 bytes of a row at a time, so a
+// run of 128 values (whose four scale bytes are one word) is 32 lanes of fp32
+// or 16 of bf16 and every load is contiguous over its lanes; a few
+// consecutive runs per group of lanes keep that many loads in flight.
 #include "tb_async.cuh"
 #include "tb_device.cuh"
 #include "tb_internal.h"
@@ -24,71 +24,52 @@ namespace tb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTasks = 4;  // 128-runs per half-warp
+constexpr int kTasks = 4;  // runs per group of lanes
 
 // scale word of (row, 128-run): 512-byte tiles of 128 rows x 4 blocks
 __device__ __forceinline__ int64_t scale_word(int64_t row, int64_t g, int64_t G) {
     return ((row >> 7) * G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3);
 }
 
-// eight values -> eight codes; w[0] in the lowest nibble
-__device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
-    uint32_t d;
-    asm("{\n .reg .b8 a, b, c, d;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
-        " mov.b32 %0, {a, b, c, d};\n}"
-        : "=r"(d)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-    return d;
+// four values -> two bytes of codes, a in the lowest half-byte
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n .reg .b8 x, y;\n .reg .b16 h;\n cvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 y, %4, %3;\n mov.b16 h, {x, y};\n cvt.u32.u16 %0, h;\n}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
 
 struct QuantArgs {
     const void* W;       // [N][ldw]
-    uint32_t* codes;     // [N][K/8] words
+    uint8_t* codes;      // [N][K/2]
     uint32_t* scales;    // tiles
     int32_t* bad;        // or null
-    int64_t N, K, ldw, G, tasks;
+    int64_t K, ldw, G, tasks;
     int32_t own_bad;     // the only CTA: it writes the count itself
 };
 
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
-    if constexpr (DT == kF32) {
-        const float4 a = __ldcs(static_cast<const float4*>(p)), b = __ldcs(static_cast<const float4*>(p) + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a = __ldcs(static_cast<const uint4*>(p));
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    }
-}
-
-template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
-    const int lane16 = threadIdx.x & 15;
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kTasks;
-    int64_t row = first / A.G, g = first - row * A.G;
-    float v[kTasks][8];
-    int64_t rows[kTasks], gs[kTasks];
-    bool in[kTasks];
+    constexpr int V = DT == kF32 ? 4 : 8;  // values of a thread's 16 bytes
+    constexpr int L = 128 / V;             // lanes of a run
+    const int lane = threadIdx.x & (L - 1);
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L) * kTasks;
+    int64_t row = first / A.G;
+    int32_t g = (int32_t)(first - row * A.G);
+    uint4 v[kTasks];
+    int64_t at[kTasks], word[kTasks];  // place of the thread's codes (bytes), of the run's scales; -1: none
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
-        rows[i] = row;
-        gs[i] = g;
-        const int64_t k = g * 128 + lane16 * 8;
-        in[i] = first + i < A.tasks && k < A.K;
-        if (in[i]) {
-            load8<DT>(static_cast<const char*>(A.W) + (row * A.ldw + k) * (DT == kF32 ? 4 : 2), v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
-        if (++g == A.G) {
+        const int64_t k = (int64_t)g * 128 + lane * V;
+        const bool run = first + i < A.tasks, in = run && k < A.K;
+        v[i] = in ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(A.W) +
+                                                          (row * A.ldw + k) * (DT == kF32 ? 4 : 2)))
+                  : make_uint4(0u, 0u, 0u, 0u);
+        at[i] = in ? (row * A.K + k) / 2 : -1;
+        word[i] = run ? scale_word(row, g, A.G) : -1;
+        if (++g == (int32_t)A.G) {
             g = 0;
             ++row;
         }
@@ -96,31 +77,53 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
     int bad = 0;
 #pragma unroll
     for (int i = 0; i < kTasks; ++i) {
-        uint32_t amax = 0;  // bits of |w|: ordered like the values
+        float f[V];
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t a = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
-            if (a < 0x7F800000u) {
-                amax = max(amax, a);
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == kF32) {
+                f[j] = __uint_as_float(u[j]);
             } else {
-                ++bad;
-                if (a > 0x7F800000u) v[i][j] = 0.f;  // NaN: code 0; an infinity saturates by itself
+                f[2 * j] = __uint_as_float(u[j] << 16);
+                f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
             }
         }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = (int)(amax >> 23);
-        const uint32_t byte = (uint32_t)max(e - 2, 0);
+        uint32_t all = 0;  // the largest |w| as bits (ordered like the values), non-finite ones included
+#pragma unroll
+        for (int j = 0; j < V; ++j) all = max(all, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+        uint32_t amax = all;
+        if (all >= 0x7F800000u) {
+            amax = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const uint32_t a = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+                if (a < 0x7F800000u) {
+                    amax = max(amax, a);
+                } else {
+                    ++bad;
+                    if (a > 0x7F800000u) f[j] = 0.f;  // NaN: code 0; an infinity saturates by itself
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32 / V; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const uint32_t byte = (uint32_t)max((int)(amax >> 23) - 2, 0);
         const float inv = __uint_as_float((254u - byte) << 23);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-        const uint32_t c = encode8(v[i]);
-        // the four blocks' bytes of this 128-run, in the half-warp's first lane
-        uint32_t word = byte << (8 * (lane16 >> 2));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (in[i]) A.codes[(rows[i] * A.K + gs[i] * 128) / 8 + lane16] = c;
-        if (lane16 == 0 && first + i < A.tasks) A.scales[scale_word(rows[i], gs[i], A.G)] = word;
+        for (int j = 0; j < V; ++j) f[j] *= inv;
+        // the four blocks' bytes of this run
+        uint32_t w = byte << (8 * (lane / (32 / V)));
+        w |= __shfl_xor_sync(0xffffffffu, w, 32 / V);
+        w |= __shfl_xor_sync(0xffffffffu, w, 64 / V);
+        if (at[i] >= 0) {
+            const uint32_t lo = encode4(f[0], f[1], f[2], f[3]);
+            if constexpr (DT == kF32) {
+                *reinterpret_cast<uint16_t*>(A.codes + at[i]) = (uint16_t)lo;
+            } else {
+                *reinterpret_cast<uint32_t*>(A.codes + at[i]) = lo | encode4(f[4], f[5], f[6], f[7]) << 16;
+            }
+        }
+        if (lane == 0 && word[i] >= 0) A.scales[word[i]] = w;
     }
     if (A.bad) {
         bad = __reduce_add_sync(0xffffffffu, bad);
@@ -198,8 +201,9 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
     }
 }
 
-bool blocks_of(int64_t tasks, unsigned* blocks) {
-    const int64_t b = (tasks + kThreads / 16 * kTasks - 1) / (kThreads / 16 * kTasks);
+// CTAs for so many runs of `lanes` lanes each
+bool blocks_of(int64_t tasks, int lanes, unsigned* blocks) {
+    const int64_t per = kThreads / lanes * kTasks, b = (tasks + per - 1) / per;
     if (b > 0x7FFFFFFF) return false;
     *blocks = (unsigned)b;
     return true;
@@ -211,16 +215,15 @@ cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t
                                 uint8_t* scales, int32_t* bad, cudaStream_t st) {
     QuantArgs A;
     A.W = W;
-    A.codes = static_cast<uint32_t*>(codes);
+    A.codes = static_cast<uint8_t*>(codes);
     A.scales = reinterpret_cast<uint32_t*>(scales);
     A.bad = bad;
-    A.N = N;
     A.K = K;
     A.ldw = ldw;
     A.G = (K + 127) / 128;
     A.tasks = N * A.G;
     unsigned blocks;
-    if (!blocks_of(A.tasks, &blocks)) return cudaErrorInvalidValue;
+    if (!blocks_of(A.tasks, w_dtype == kF32 ? 32 : 16, &blocks)) return cudaErrorInvalidValue;
     A.own_bad = blocks == 1;
     if (bad && blocks > 1) {
         const cudaError_t e = cudaMemsetAsync(bad, 0, sizeof(int32_t), st);
@@ -242,7 +245,7 @@ cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int6
     A.G = (K + 127) / 128;
     A.tasks = N * A.G;
     unsigned blocks;
-    if (!blocks_of(A.tasks, &blocks)) return cudaErrorInvalidValue;
+    if (!blocks_of(A.tasks, 16, &blocks)) return cudaErrorInvalidValue;
     if (w_dtype == kF32) k_mx4_dequantize<kF32><<<blocks, kThreads, 0, st>>>(A);
     else k_mx4_dequantize<kBF16><<<blocks, kThreads, 0, st>>>(A);
     return cudaGetLastError();

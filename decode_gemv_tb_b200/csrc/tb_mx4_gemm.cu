@@ -582,14 +582,15 @@ bool encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, 
 
 template <class C>
 cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
-    // CTAs per unit: the split whose waves of chunks are the shortest, with about three chunks' time to start and
-    // finish a CTA and four more to add a cluster's partial sums
+    // CTAs per unit.  A chunk takes a CTA about 0.32 us; adding a cluster's partial sums about 0.6 us and 0.04 us per
+    // column of the unit (measured: 4096 x 4096, M = 1: 8.8 / 6.8 / 5.5 us with 1 / 2 / 4 CTAs, M = 61: 9.4 / 10.4 /
+    // 7.9 us), and clusters that do not all fit one CTA per SM lose more than they gain (8 CTAs: 7.1 and 10.3 us).
     int S = 1;
     int64_t best = -1;
-    for (int s = 1; s <= 8 && s <= A.KC && s <= C::NT / 2; s *= 2) {
+    for (int s = 1; s <= 8 && s <= A.KC; s *= 2) {
+        if (s > 1 && units * s > sms) break;
         const int64_t slots = (int64_t)sms * C::per_sm(s);
-        if (slots == 0 || (s > 1 && units * s > slots)) break;
-        const int64_t cost = (units * s + slots - 1) / slots * ((A.KC + s - 1) / s + 3) + (s > 1 ? 4 : 0);
+        const int64_t cost = (units * s + slots - 1) / slots * ((A.KC + s - 1) / s) + (s > 1 ? 2 + C::NT / 8 : 0);
         if (best < 0 || cost < best) {
             best = cost;
             S = s;
