@@ -17,7 +17,7 @@
 // costs one DFMA, two and a half integer operations per weight shared by
 // the tokens of the cluster.
 //
-// A cluster of eight CTAs handles TB tokens: its 128 warps take two experts
+// A cluster of eight CTAs handles TB tokens: its warps take two experts
 // each at a time (a token's words, the heaviest traffic, are read from shared
 // memory once for both) and leave the logits in the shared memory of the CTA that
 // selects for the token.  No workspace, no atomics.
@@ -41,8 +41,6 @@ struct RouteArgs {
 namespace {
 
 constexpr int kRtCluster = 8;
-constexpr int kRtWarps = 16;
-constexpr int kRtThreads = kRtWarps * 32;
 constexpr int kRtUnroll = 4;  // 16-byte loads of the router in flight per lane
 
 __device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
@@ -109,8 +107,13 @@ __device__ void select_experts(const double* l, const RouteArgs& A, int64_t t) {
     }
 }
 
+// warps of a CTA: sixteen finish one token soonest; with several clusters eight leave room for two CTAs per SM (with
+// one, sixteen clusters of eight do not fit the GPU's SM groups at once: 64 tokens x 256 experts took 26 us)
+__host__ __device__ constexpr int rt_warps(int tb) { return tb == 1 ? 16 : 8; }
+
 template <int TB>
-__global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(kRtCluster, 1, 1) k_moe_route(const RouteArgs A) {
+__global__ void __launch_bounds__(rt_warps(TB) * 32) __cluster_dims__(kRtCluster, 1, 1) k_moe_route(const RouteArgs A) {
+    constexpr int kRtWarps = rt_warps(TB), kRtThreads = kRtWarps * 32;
     extern __shared__ __align__(16) uint8_t smem[];
     double* logits = reinterpret_cast<double*>(smem);                 // [E]: of this CTA's token
     uint32_t* xs = reinterpret_cast<uint32_t*>(smem + 8 * ((A.E + 1) & ~1));  // [TB][H] high words of x
@@ -214,7 +217,7 @@ cudaError_t launch(const RouteArgs& A, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
     if (e != cudaSuccess) return e;
-    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * kRtCluster, kRtThreads, smem, st>>>(A);
+    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * kRtCluster, rt_warps(TB) * 32, smem, st>>>(A);
     return cudaGetLastError();
 }
 

@@ -10,10 +10,11 @@
 // instruction rounds half to even.
 //
 // Both kernels are bound by HBM: 2 or 4 bytes per weight on the wide side,
-// 0.53 on the narrow one.  A thread holds 16 bytes of a row at a time, so a
-// run of 128 values (whose four scale bytes are one word) is 32 lanes of fp32
-// or 16 of bf16 and every load is contiguous over its lanes; a few
-// consecutive runs per group of lanes keep that many loads in flight.
+// 0.53 on the narrow one.  A warp holds a piece of one row, each lane 16 bytes
+// of it per load (contiguous over the lanes), kLoads loads in flight; what is
+// addressed after the first load is a constant away.  (With a division and
+// 64-bit addresses per load the quantiser was bound by its instructions, 98 us
+// on 17408 x 5120 fp32.)
 #include "tb_async.cuh"
 #include "tb_device.cuh"
 #include "tb_internal.h"
@@ -24,7 +25,8 @@ namespace tb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTasks = 4;  // runs per group of lanes
+constexpr int kTasks = 4;  // dequantisation: runs of 128 per half-warp
+constexpr int kLoads = 4;  // quantisation: 16-byte loads of a lane
 
 // scale word of (row, 128-run): 512-byte tiles of 128 rows x 4 blocks
 __device__ __forceinline__ int64_t scale_word(int64_t row, int64_t g, int64_t G) {
@@ -42,88 +44,85 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
 }
 
 struct QuantArgs {
-    const void* W;       // [N][ldw]
-    uint8_t* codes;      // [N][K/2]
-    uint32_t* scales;    // tiles
-    int32_t* bad;        // or null
-    int64_t K, ldw, G, tasks;
-    int32_t own_bad;     // the only CTA: it writes the count itself
+    const void* W;      // [N][ldw]
+    uint8_t* codes;     // [N][K/2]
+    uint8_t* scales;    // tiles
+    int32_t* bad;       // or null
+    int64_t K, ldw, G;  // G: 128-runs of a row
+    int64_t warps;      // pieces of all rows
+    uint32_t pieces;    // of a row
+    int32_t own_bad;    // the only CTA: it writes the count itself
 };
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
-    constexpr int V = DT == kF32 ? 4 : 8;  // values of a thread's 16 bytes
-    constexpr int L = 128 / V;             // lanes of a run
-    const int lane = threadIdx.x & (L - 1);
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / L) + threadIdx.x / L) * kTasks;
-    int64_t row = first / A.G;
-    int32_t g = (int32_t)(first - row * A.G);
-    uint4 v[kTasks];
-    int64_t at[kTasks], word[kTasks];  // place of the thread's codes (bytes), of the run's scales; -1: none
-#pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
-        const int64_t k = (int64_t)g * 128 + lane * V;
-        const bool run = first + i < A.tasks, in = run && k < A.K;
-        v[i] = in ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(A.W) +
-                                                          (row * A.ldw + k) * (DT == kF32 ? 4 : 2)))
-                  : make_uint4(0u, 0u, 0u, 0u);
-        at[i] = in ? (row * A.K + k) / 2 : -1;
-        word[i] = run ? scale_word(row, g, A.G) : -1;
-        if (++g == (int32_t)A.G) {
-            g = 0;
-            ++row;
-        }
-    }
+    constexpr int V = DT == kF32 ? 4 : 8;   // values of a lane's 16 bytes
+    constexpr int S = 32 * V;               // values of a warp's load
+    constexpr int B = 32 / V;               // lanes of a block
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     int bad = 0;
+    if (id < A.warps) {
+        const int64_t row = A.warps <= 0x7FFFFFFF ? (uint32_t)id / A.pieces : id / A.pieces;
+        const int64_t k0 = (id - row * A.pieces) * (S * kLoads) + lane * V;
+        const int left = (int)min(A.K - k0, (int64_t)(S * kLoads)), runs = (int)min(A.G * 128 - k0, (int64_t)(S * kLoads));
+        const char* src = static_cast<const char*>(A.W) + (row * A.ldw + k0) * (DT == kF32 ? 4 : 2);
+        uint4 v[kLoads];
 #pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
-        float f[V];
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i = 0; i < kLoads; ++i)
+            v[i] = i * S < left ? __ldcs(reinterpret_cast<const uint4*>(src + i * 512)) : make_uint4(0u, 0u, 0u, 0u);
+        uint8_t* codes = A.codes + (row * A.K + k0) / 2;
+        uint8_t* scale = A.scales + ((row >> 7) * A.G + (k0 >> 7)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+                         ((k0 >> 5) & 3);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == kF32) {
-                f[j] = __uint_as_float(u[j]);
-            } else {
-                f[2 * j] = __uint_as_float(u[j] << 16);
-                f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-            }
-        }
-        uint32_t all = 0;  // the largest |w| as bits (ordered like the values), non-finite ones included
+        for (int i = 0; i < kLoads; ++i) {
+            float f[V];
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-        for (int j = 0; j < V; ++j) all = max(all, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-        uint32_t amax = all;
-        if (all >= 0x7F800000u) {
-            amax = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const uint32_t a = __float_as_uint(f[j]) & 0x7FFFFFFFu;
-                if (a < 0x7F800000u) {
-                    amax = max(amax, a);
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (DT == kF32) {
+                    f[j] = __uint_as_float(u[j]);
                 } else {
-                    ++bad;
-                    if (a > 0x7F800000u) f[j] = 0.f;  // NaN: code 0; an infinity saturates by itself
+                    f[2 * j] = __uint_as_float(u[j] << 16);
+                    f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
                 }
             }
-        }
+            float amax = 0.f, odd = 0.f;  // odd: no number as soon as a value is not finite
 #pragma unroll
-        for (int o = 1; o < 32 / V; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const uint32_t byte = (uint32_t)max((int)(amax >> 23) - 2, 0);
-        const float inv = __uint_as_float((254u - byte) << 23);
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] *= inv;
-        // the four blocks' bytes of this run
-        uint32_t w = byte << (8 * (lane / (32 / V)));
-        w |= __shfl_xor_sync(0xffffffffu, w, 32 / V);
-        w |= __shfl_xor_sync(0xffffffffu, w, 64 / V);
-        if (at[i] >= 0) {
-            const uint32_t lo = encode4(f[0], f[1], f[2], f[3]);
-            if constexpr (DT == kF32) {
-                *reinterpret_cast<uint16_t*>(A.codes + at[i]) = (uint16_t)lo;
-            } else {
-                *reinterpret_cast<uint32_t*>(A.codes + at[i]) = lo | encode4(f[4], f[5], f[6], f[7]) << 16;
+            for (int j = 0; j < V; ++j) {
+                amax = fmaxf(amax, fabsf(f[j]));
+                odd = fmaf(f[j], 0.f, odd);
             }
+            if (odd != 0.f) {
+                amax = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const uint32_t a = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+                    if (a < 0x7F800000u) {
+                        amax = fmaxf(amax, fabsf(f[j]));
+                    } else {
+                        ++bad;
+                        if (a > 0x7F800000u) f[j] = 0.f;  // NaN: code 0; an infinity saturates by itself
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < B; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const uint32_t byte = (uint32_t)max((int)(__float_as_uint(amax) >> 23) - 2, 0);
+            const float inv = __uint_as_float((254u - byte) << 23);
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] *= inv;
+            if (i * S < left) {
+                const uint32_t lo = encode4(f[0], f[1], f[2], f[3]);
+                if constexpr (DT == kF32) {
+                    *reinterpret_cast<uint16_t*>(codes + i * (S / 2)) = (uint16_t)lo;
+                } else {
+                    *reinterpret_cast<uint32_t*>(codes + i * (S / 2)) = lo | encode4(f[4], f[5], f[6], f[7]) << 16;
+                }
+            }
+            // one lane of a block; blocks past K in the row's last run write their 0 too
+            if ((lane & (B - 1)) == 0 && i * S < runs) scale[i * (S / 128) * 512] = (uint8_t)byte;
         }
-        if (lane == 0 && word[i] >= 0) A.scales[word[i]] = w;
     }
     if (A.bad) {
         bad = __reduce_add_sync(0xffffffffu, bad);
@@ -201,14 +200,6 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
     }
 }
 
-// CTAs for so many runs of `lanes` lanes each
-bool blocks_of(int64_t tasks, int lanes, unsigned* blocks) {
-    const int64_t per = kThreads / lanes * kTasks, b = (tasks + per - 1) / per;
-    if (b > 0x7FFFFFFF) return false;
-    *blocks = (unsigned)b;
-    return true;
-}
-
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t N, int64_t K, void* codes,
@@ -216,21 +207,23 @@ cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t
     QuantArgs A;
     A.W = W;
     A.codes = static_cast<uint8_t*>(codes);
-    A.scales = reinterpret_cast<uint32_t*>(scales);
+    A.scales = scales;
     A.bad = bad;
     A.K = K;
     A.ldw = ldw;
     A.G = (K + 127) / 128;
-    A.tasks = N * A.G;
-    unsigned blocks;
-    if (!blocks_of(A.tasks, w_dtype == kF32 ? 32 : 16, &blocks)) return cudaErrorInvalidValue;
+    const int64_t piece = 32 * (w_dtype == kF32 ? 4 : 8) * kLoads;
+    A.pieces = (uint32_t)((K + piece - 1) / piece);
+    A.warps = N * A.pieces;
+    const int64_t blocks = (A.warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     A.own_bad = blocks == 1;
     if (bad && blocks > 1) {
         const cudaError_t e = cudaMemsetAsync(bad, 0, sizeof(int32_t), st);
         if (e != cudaSuccess) return e;
     }
-    if (w_dtype == kF32) k_mx4_quantize<kF32><<<blocks, kThreads, 0, st>>>(A);
-    else k_mx4_quantize<kBF16><<<blocks, kThreads, 0, st>>>(A);
+    if (w_dtype == kF32) k_mx4_quantize<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(A);
+    else k_mx4_quantize<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(A);
     return cudaGetLastError();
 }
 
@@ -244,10 +237,10 @@ cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int6
     A.ldw = ldw;
     A.G = (K + 127) / 128;
     A.tasks = N * A.G;
-    unsigned blocks;
-    if (!blocks_of(A.tasks, 16, &blocks)) return cudaErrorInvalidValue;
-    if (w_dtype == kF32) k_mx4_dequantize<kF32><<<blocks, kThreads, 0, st>>>(A);
-    else k_mx4_dequantize<kBF16><<<blocks, kThreads, 0, st>>>(A);
+    const int64_t per = kThreads / 16 * kTasks, blocks = (A.tasks + per - 1) / per;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (w_dtype == kF32) k_mx4_dequantize<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(A);
+    else k_mx4_dequantize<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(A);
     return cudaGetLastError();
 }
 
