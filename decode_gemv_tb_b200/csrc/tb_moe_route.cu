@@ -17,7 +17,7 @@
 // costs one DFMA, two and a half integer operations per weight shared by
 // the tokens of the cluster.
 //
-// A cluster of eight CTAs handles TB tokens: its warps take two experts
+// A cluster of CTAs handles TB tokens: its warps take two experts
 // each at a time (a token's words, the heaviest traffic, are read from shared
 // memory once for both) and leave the logits in the shared memory of the CTA that
 // selects for the token.  No workspace, no atomics.
@@ -40,7 +40,6 @@ struct RouteArgs {
 
 namespace {
 
-constexpr int kRtCluster = 8;
 constexpr int kRtUnroll = 4;  // 16-byte loads of the router in flight per lane
 
 __device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
@@ -107,13 +106,15 @@ __device__ void select_experts(const double* l, const RouteArgs& A, int64_t t) {
     }
 }
 
-// warps of a CTA: sixteen finish one token soonest; with several clusters eight leave room for two CTAs per SM (with
-// one, sixteen clusters of eight do not fit the GPU's SM groups at once: 64 tokens x 256 experts took 26 us)
-__host__ __device__ constexpr int rt_warps(int tb) { return tb == 1 ? 16 : 8; }
+// CTAs of a cluster: eight finish one token soonest; the clusters of a batch have four, which the SM groups hold on more
+// SMs at once (64 tokens x 256 experts: 26 us with clusters of eight, one or two CTAs per SM)
+__host__ __device__ constexpr int rt_cluster(int tb) { return tb == 1 ? 8 : 4; }
+constexpr int kRtWarps = 16;
+constexpr int kRtThreads = kRtWarps * 32;
 
 template <int TB>
-__global__ void __launch_bounds__(rt_warps(TB) * 32) __cluster_dims__(kRtCluster, 1, 1) k_moe_route(const RouteArgs A) {
-    constexpr int kRtWarps = rt_warps(TB), kRtThreads = kRtWarps * 32;
+__global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(rt_cluster(TB), 1, 1) k_moe_route(const RouteArgs A) {
+    constexpr int kRtCluster = rt_cluster(TB);
     extern __shared__ __align__(16) uint8_t smem[];
     double* logits = reinterpret_cast<double*>(smem);                 // [E]: of this CTA's token
     uint32_t* xs = reinterpret_cast<uint32_t*>(smem + 8 * ((A.E + 1) & ~1));  // [TB][H] high words of x
@@ -123,20 +124,29 @@ __global__ void __launch_bounds__(rt_warps(TB) * 32) __cluster_dims__(kRtCluster
     const int nt = (int)min((int64_t)TB, A.T - t0);
     cluster_arrive();
     const int H8 = A.H / 8;  // eights of x: their first four words in one plane, the others in a second
-    for (int i = threadIdx.x; i < TB * H8; i += kRtThreads) {
-        const int t = i / H8, h = i - t * H8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (t < nt) v = *reinterpret_cast<const uint4*>(A.x + (t0 + t) * A.ldx + 8 * h);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t d[8];
+    for (int i0 = threadIdx.x; i0 < TB * H8; i0 += 4 * kRtThreads) {
+        uint4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            d[2 * j] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] << 16));
-            d[2 * j + 1] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] & 0xFFFF0000u));
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * kRtThreads, t = i / H8, h = i - t * H8;
+            v[q] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < TB * H8 && t < nt) v[q] = *reinterpret_cast<const uint4*>(A.x + (t0 + t) * A.ldx + 8 * h);
         }
-        uint4* p = reinterpret_cast<uint4*>(xs) + t * 2 * H8 + h;
-        p[0] = make_uint4(d[0], d[1], d[2], d[3]);
-        p[H8] = make_uint4(d[4], d[5], d[6], d[7]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * kRtThreads, t = i / H8, h = i - t * H8;
+            if (i >= TB * H8) break;
+            const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+            uint32_t d[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                d[2 * j] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] << 16));
+                d[2 * j + 1] = (uint32_t)__double2hiint((double)__uint_as_float(u[j] & 0xFFFF0000u));
+            }
+            uint4* p = reinterpret_cast<uint4*>(xs) + t * 2 * H8 + h;
+            p[0] = make_uint4(d[0], d[1], d[2], d[3]);
+            p[H8] = make_uint4(d[4], d[5], d[6], d[7]);
+        }
     }
     __syncthreads();
     cluster_wait();  // every CTA of the cluster has begun
@@ -152,13 +162,22 @@ __global__ void __launch_bounds__(rt_warps(TB) * 32) __cluster_dims__(kRtCluster
         for (int b = 0; b < EB; ++b)
 #pragma unroll
             for (int t = 0; t < TB; ++t) acc[b][t] = 0.0;
+        uint4 next[U][EB];
+        auto load = [&](int h0) {
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+#pragma unroll
+                for (int b = 0; b < EB; ++b)
+                    next[q][b] = h0 + 32 * q < H8 ? __ldg(w[b] + h0 + 32 * q) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        load(lane);
         for (int h0 = lane; h0 < H8; h0 += 32 * U) {
             uint4 v[U][EB];
 #pragma unroll
             for (int q = 0; q < U; ++q)
 #pragma unroll
-                for (int b = 0; b < EB; ++b)
-                    v[q][b] = h0 + 32 * q < H8 ? __ldg(w[b] + h0 + 32 * q) : make_uint4(0u, 0u, 0u, 0u);
+                for (int b = 0; b < EB; ++b) v[q][b] = next[q][b];
+            load(h0 + 32 * U);
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 const int h = h0 + 32 * q;
@@ -217,7 +236,7 @@ cudaError_t launch(const RouteArgs& A, cudaStream_t st) {
     const cudaError_t e =
         cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
     if (e != cudaSuccess) return e;
-    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * kRtCluster, rt_warps(TB) * 32, smem, st>>>(A);
+    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * rt_cluster(TB), kRtThreads, smem, st>>>(A);
     return cudaGetLastError();
 }
 
@@ -239,9 +258,9 @@ cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* rou
     A.H = (int32_t)H;
     A.k = k;
     A.renorm = renorm ? 1 : 0;
-    // tokens per cluster: one while sixteen clusters (128 SMs) hold them all, then as many as share a weight's
-    // conversion and its read from L2
-    int tb = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
+    // tokens per cluster: one for a few tokens, two while the clusters of four hold them all at once, then four, which
+    // share a weight's conversion and its read from L2
+    int tb = T <= 16 ? 1 : (T <= 64 ? 2 : 4);
     while (tb > 1 && route_smem(tb, E, (int)H) > 224 * 1024) tb /= 2;
     return tb == 1 ? launch<1>(A, st) : (tb == 2 ? launch<2>(A, st) : launch<4>(A, st));
 }
