@@ -334,7 +334,8 @@ extern "C" {
 int tb_version(void) { return 100; }
 
 unsigned int tb_wait_timeouts(void) {
-    const unsigned int n[] = {take_wait_timeouts(), take_g8_timeouts(), take_ss_timeouts(), take_mx_timeouts()};
+    const unsigned int n[] = {take_wait_timeouts(), take_g8_timeouts(), take_ss_timeouts(), take_mx_timeouts(),
+                              take_moe_timeouts()};
     unsigned int sum = 0;
     for (const unsigned int v : n) {
         if (v == 0xFFFFFFFFu) return v;
@@ -666,27 +667,28 @@ tb_status_t tb_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* router,
 }
 
 size_t tb_moe_workspace_bytes(const tb_moe_t* layer, int64_t T, int k) {
-    return check_moe(layer, T, k) == TB_OK ? 2 * moe_data_bytes(T, k, layer->I) : 0;
+    return check_moe(layer, T, k) == TB_OK ? 2 * moe_data_bytes(T, k, layer->H, layer->I) : 0;
 }
 
 tb_status_t tb_moe(const tb_moe_t* layer, const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights,
-                   int64_t T, int k, void* y, tb_dtype_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
-                   tb_stream_t stream) {
+                   int64_t T, int k, void* y, tb_dtype_t y_dtype, int64_t ldy, unsigned flags, void* workspace,
+                   size_t workspace_bytes, tb_stream_t stream) {
     tb_status_t s = check_moe(layer, T, k);
     if (s != TB_OK) return s;
-    if (!x || !ids || !weights || !workspace) return TB_ERR_ARG;
+    if (!x || !ids || !weights || !workspace || (flags & ~(unsigned)TB_FLAG_TEST_STALL) != 0) return TB_ERR_ARG;
     if ((s = check_out(y, y_dtype)) != TB_OK) return s;
     if (ldx < layer->H || ldy < layer->H) return TB_ERR_SHAPE;
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
         return TB_ERR_ALIGN;
-    const size_t data = moe_data_bytes(T, k, layer->I);
+    const size_t data = moe_data_bytes(T, k, layer->H, layer->I);
     if (workspace_bytes < 2 * data) return TB_ERR_ARG;
     char* back = static_cast<char*>(workspace) + (workspace_bytes & ~size_t(255)) - data;
+    const bool stall = (flags & TB_FLAG_TEST_STALL) != 0;
     return cuda_status(launch_moe({layer->gate, layer->gate_scales, layer->gate_grid},
                                   {layer->up, layer->up_scales, layer->up_grid},
                                   {layer->down, layer->down_scales, layer->down_grid}, layer->E, layer->H, layer->I, x,
-                                  ldx, ids, weights, (int)T, k, y, y_dtype, ldy, back,
-                                  static_cast<cudaStream_t>(stream)));
+                                  ldx, ids, weights, (int)T, k, y, y_dtype, ldy, back, stall ? kTestWaitCycles : kWaitCycles,
+                                  stall, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -43,6 +43,24 @@ __device__ __forceinline__ bool mb_wait(uint32_t bar, uint32_t parity, long long
         }
     }
 }
+// the same for a wait that concerns one warp only
+__device__ __forceinline__ bool mb_wait_alone(uint32_t bar, uint32_t parity, long long limit, unsigned int* timeouts) {
+    long long t0 = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (t0 == 0) t0 = clock64();
+        if (clock64() - t0 > limit) {
+            atomicAdd(timeouts, 1u);
+            return false;
+        }
+    }
+}
 // the same wait without abort checks (draining what is in flight before exit)
 __device__ __forceinline__ void mb_drain(uint32_t bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();

@@ -97,11 +97,13 @@ struct MoeWeights {
     const void* scales;
     int grid;
 };
-// bytes of the gated activations between the two kernels (written before they are read)
-size_t moe_data_bytes(int64_t T, int k, int64_t I);
+constexpr int kMoeSliceRows = 128;  // of the results, at least: room to split K when pairs are few
+// bytes of the gated activations and of the pairs' results (both written before they are read)
+size_t moe_data_bytes(int64_t T, int k, int64_t H, int64_t I);
 cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWeights& down, int E, int64_t H, int64_t I,
                        const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int T, int k, void* y,
-                       int ydt, int64_t ldy, void* data, cudaStream_t st);
+                       int ydt, int64_t ldy, void* data, long long wait_cycles, bool stall, cudaStream_t st);
+unsigned int take_moe_timeouts();
 
 // bounded device waits that gave up since the last call (clears the count;
 // synchronous); 0xFFFFFFFF if the count cannot be read

@@ -3,14 +3,15 @@
 //
 //     h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   y[t] = sum_j w[t,j] Wd[ids[t,j]] h[t,ids[t,j]]
 //
-// Every expert that some token takes is read once per sixteen of its tokens:
+// Every expert that some token takes is read once per eight or sixteen of its
+// tokens:
 // with few tokens the layer is bound by the bytes of the experts it touches
 // and by decoding them.
 //
 // Both kernels group the (token, choice) pairs by expert themselves, in
 // shared memory (a 64-bit token mask per expert, a prefix sum over the
 // experts): at most 1024 pairs, no extra launch, no atomics on floats.  A
-// block is an expert with up to sixteen of its tokens.
+// block is an expert with up to eight or sixteen of its tokens.
 //
 // The products run on mma.sync m16n8k16: 16 weight rows decoded in registers
 // to bf16 (exact, 4-bit codes with their power-of-two scale too), the
@@ -18,7 +19,10 @@
 // share the decode.  A lane of a quad owns 32 consecutive k of every
 // 128-group in both operands, so a row's group is one 8-, 12- or 16-byte read
 // per lane, free of bank conflicts, and no code moves between lanes.  Weights
-// stream through a private cp.async ring per warp, a group per stage.
+// stream through a private ring per warp, filled by tensor copies of 16 or 32
+// rows x 128 (144) bytes.  (With cp.async, 32 rows' scattered 16- and 4-byte
+// pieces per group, both kernels were bound by the L1's request rate: more
+// warps changed nothing, 64 tokens x 4-bit experts took 466 us.)
 //
 // h is rounded to bf16 between the two products, as tb_gate_up_silu's is: the
 // MMA's operand, and half the activations a second part would cost.
@@ -37,12 +41,14 @@
 
 namespace tb {
 
+__device__ unsigned int g_moe_timeouts = 0;
+
 struct MoeMat {
-    const uint8_t* packed;
-    const uint8_t* scales;
-    int64_t rb;    // bytes of a packed row
-    int32_t G;     // 128-groups of a row
-    int32_t kind;  // 0: 2 bits, 1: 3 bits, 2: MX4
+    CUtensorMap codes;      // packed rows: bytes x rows
+    CUtensorMap tiles;      // 4-bit scales: 512 bytes x (row tile, group)
+    const uint16_t* scales;  // bf16 [rows][G]
+    int32_t G;               // 128-groups of a row
+    int32_t kind;            // 0: 2 bits, 1: 3 bits, 2: MX4
 };
 
 struct MoeArgs {
@@ -51,10 +57,12 @@ struct MoeArgs {
     const int32_t* ids;      // [T][k]
     const float* weights;    // [T][k]
     uint16_t* h;             // [slots][I] bf16
+    float* z;                // [H / 32][zrows][32]: weighted results of the slots
     void* y;                 // [T][ldy]
     int64_t ldx, ldy;
-    int32_t T, k, E, H, I, ydt;
-    int32_t S, C;
+    long long wait_cycles;
+    int32_t T, k, E, H, I, ydt, stall;
+    int32_t S, C, zrows;
     int32_t hperm;  // h in the order of the 4-bit decode's pairs
 };
 
@@ -62,27 +70,20 @@ namespace {
 
 constexpr int kMoeWarps = 4;
 constexpr int kMoeThreads = kMoeWarps * 32;
-constexpr int kStages = 4;
-constexpr int kBlockTokens = 16;
+constexpr int kStages = 2;  // of a warp's ring
+constexpr float kMoeNaN = __builtin_nanf("");
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxK;
-constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / kBlockTokens;
+constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / 8;
 
-// packed bytes of a row's group (also its stride in shared memory: with 32, 48 and 64 bytes the reads of eight rows
-// by a quad each touch every bank once)
+// packed bytes of a row's group; groups of a stage; bytes of a row in it.  The 2-bit and 4-bit stages have 128-byte rows
+// in the 128-byte swizzle, the 3-bit ones plain rows of 144 bytes; with a tile's rows taken in bit-reversed order the
+// reads of a group (8, 12 or 16 bytes by each lane of a quad, a row per quad) are free of bank conflicts in all three.
 __host__ __device__ constexpr int group_bytes(int kind) { return kind == 0 ? 32 : (kind == 1 ? 48 : 64); }
+__host__ __device__ constexpr int stage_groups(int kind) { return kind == 0 ? 4 : (kind == 1 ? 3 : 2); }
+__host__ __device__ constexpr int row_stride(int kind) { return kind == 1 ? 144 : 128; }
+// a unit's bf16 scales are copied whole up to this many groups; longer rows read them one by one
+constexpr int kMaxScaleGroups = 64;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 4 bytes, of which the first n (2 or 4) are read
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait_groups() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -96,6 +97,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -153,9 +159,9 @@ __device__ __forceinline__ void pair_up(uint32_t (&x)[16], const uint32_t (&v)[1
 }
 
 template <int NS, bool BIG>
-__device__ __forceinline__ void mx4_product(uint32_t row, int t, uint32_t ba, uint32_t bb,
+__device__ __forceinline__ void mx4_product(uint32_t row, uint32_t ba, uint32_t bb,
                                             const uint32_t (&x)[NS][16], float (&acc)[NS][4]) {
-    const uint4 a = lds128(row + 16 * t), b = lds128(row + 8 * group_bytes(2) + 16 * t);
+    const uint4 a = lds128(row), b = lds128(row + 8 * row_stride(2));
     const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
     // 2^(byte - 1) as a pair; above 2^127 in two factors; 255 is no number
     const uint32_t fa = ((BIG ? min(ba, 128u) : ba) + 126u) * 0x00800080u;
@@ -185,15 +191,15 @@ __device__ __forceinline__ void mx4_product(uint32_t row, int t, uint32_t ba, ui
     }
 }
 
-// One 128-group of 16 rows times NS sets of eight columns: acc += s W x.  `row`: shared address of row lane/4 of the
-// group, `sc`: of its scale word, `odd`: the scale is the word's upper half.
+// One 128-group of 16 rows times NS sets of eight columns: acc += s W x.  `row`: shared address of the lane's codes in
+// the first of its two rows (the second is eight rows on); s0, s1: the rows' scales, or the lane's two scale bytes.
 template <int KIND, int NS>
-__device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool odd, int t, const uint32_t (&x)[NS][16],
+__device__ __forceinline__ void group_product(uint32_t row, uint32_t s0b, uint32_t s1b, const uint32_t (&x)[NS][16],
                                               float (&acc)[NS][4]) {
     if constexpr (KIND == 2) {
-        const uint32_t ba = lds8(sc + t), bb = lds8(sc + 32 + t);
-        if (__builtin_expect(__any_sync(0xffffffffu, max(ba, bb) > 128u), 0)) mx4_product<NS, true>(row, t, ba, bb, x, acc);
-        else mx4_product<NS, false>(row, t, ba, bb, x, acc);
+        const uint32_t ba = s0b, bb = s1b;
+        if (__builtin_expect(__any_sync(0xffffffffu, max(ba, bb) > 128u), 0)) mx4_product<NS, true>(row, ba, bb, x, acc);
+        else mx4_product<NS, false>(row, ba, bb, x, acc);
     } else {
         float d[NS][4];
 #pragma unroll
@@ -201,7 +207,7 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
         if constexpr (KIND == 0) {
-            const uint2 a = lds64(row + 8 * t), b = lds64(row + 8 * group_bytes(0) + 8 * t);
+            const uint2 a = lds64(row), b = lds64(row + 8 * row_stride(0));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t ra[8], rb[8];
@@ -215,8 +221,8 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
             }
         } else {
             uint32_t ra[16], rb[16];
-            const uint32_t ar = row + 12 * t, br = ar + 8 * group_bytes(1);
-            decode3_signed(lds32(ar), lds32(ar + 4), lds32(ar + 8), ra);
+            const uint32_t br = row + 8 * row_stride(1);
+            decode3_signed(lds32(row), lds32(row + 4), lds32(row + 8), ra);
             decode3_signed(lds32(br), lds32(br + 4), lds32(br + 8), rb);
 #pragma unroll
             for (int j = 0; j < 16; j += 2)
@@ -224,9 +230,7 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
                 for (int n = 0; n < NS; ++n)
                     mma_bf16(d[n], ra[j], rb[j], ra[j + 1], rb[j + 1], x[n][j], x[n][j + 1]);
         }
-        const uint32_t w0 = lds32(sc), w1 = lds32(sc + 32);
-        const float s0 = __uint_as_float(odd ? w0 & 0xFFFF0000u : w0 << 16);
-        const float s1 = __uint_as_float(odd ? w1 & 0xFFFF0000u : w1 << 16);
+        const float s0 = __uint_as_float(s0b << 16), s1 = __uint_as_float(s1b << 16);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
@@ -237,58 +241,133 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t sc, bool od
     }
 }
 
-// A warp's place in the packed rows of a matrix: group after group of the 16 rows row0 .., each lane with its own
-// 16-byte pieces.
-template <int KIND>
-struct CodeCursor {
-    const uint8_t* p;
-    uint32_t second;  // from the lane's first piece to its second
-    __device__ __forceinline__ void init(const MoeMat& m, int lane) {
-        constexpr int P = group_bytes(KIND) / 16;
-        const int a = lane, b = lane + 32;
-        second = (uint32_t)((b / P - a / P) * m.rb + (b % P - a % P) * 16);
+// ---- a warp's stream of a matrix -------------------------------------------------------
+// Units of ROWS consecutive rows and a range of their groups, one after the other, through kStages stages of kGroups
+// groups.  The warp refills a stage as soon as it has read it.
+template <int KIND, int ROWS>
+struct Stream {
+    static constexpr int kGroups = stage_groups(KIND);
+    static constexpr int kCodes = ROWS * row_stride(KIND);       // of a stage
+    static constexpr int kTiles = KIND == 2 ? ROWS * 16 * kGroups : 0;  // a 4-bit stage's scale rows
+    static constexpr int kBars = 8 * 2 * kStages;                // per stage; per scale buffer of a unit
+    // bytes of a warp's ring (codes first: swizzled stages begin at multiples of 1 KB)
+    static constexpr int kRing = (kStages * kCodes + 1023) & ~1023;
+    __host__ __device__ static constexpr int side(int G) {
+        return (kStages * kTiles + (KIND != 2 && G <= kMaxScaleGroups ? kStages * ROWS * 2 * G : 0) + 127) & ~127;
     }
-    __device__ __forceinline__ void at(const MoeMat& m, int64_t row0, int g, int lane) {
-        constexpr int P = group_bytes(KIND) / 16;
-        p = m.packed + (row0 + lane / P) * m.rb + (int64_t)g * group_bytes(KIND) + (lane % P) * 16;
+
+    const MoeMat& m;
+    uint32_t codes, sides, bars;
+    long long limit;
+    int lane, row, t;  // row: the lane's first row in a 16-row tile
+    // requests: the unit's first row, its next group and their end, how many stages and units have been begun
+    int64_t prow;
+    int pg, pend, pn, pu;
+    // reading: stage, its parity, the group in it and how many it holds; the unit's row, number and group
+    int stage, gi, left, cu, g;
+    uint32_t parity;
+    int64_t crow;
+    bool dead;
+
+    __device__ __forceinline__ Stream(const MoeMat& m_, uint32_t ring, uint32_t side_, uint32_t bars_, long long limit_)
+        : m(m_), codes(ring), sides(side_), bars(bars_), limit(limit_), pn(0), pu(0), stage(0), left(0), cu(0),
+          parity(0), dead(false) {
+        lane = threadIdx.x & 31;
+        row = (lane >> 2 & 1) << 2 | (lane >> 2 & 2) | (lane >> 4);  // lane / 4 with its three bits reversed
+        t = lane & 3;
     }
-    __device__ __forceinline__ void load(uint32_t dst, int lane) {
-        cp16(dst + lane * 16, p);
-        if (KIND == 2 || (KIND == 1 && lane < 16)) cp16(dst + (lane + 32) * 16, p + second);
-        p += group_bytes(KIND);
+    __device__ __forceinline__ void init_bars() const {
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < 2 * kStages; ++i) mb_init(bars + 8 * i, 1);
     }
-};
-// The same for a row's scales: two bytes per group, fetched with the aligned word they lie in, or a word per 4-bit
-// group.
-struct ScaleCursor {
-    const uint8_t* p;
-    uint32_t step, n;
-    template <int KIND>
-    __device__ __forceinline__ void at(const MoeMat& m, int64_t row, int g) {
+    __device__ __forceinline__ bool wide() const { return KIND != 2 && m.G > kMaxScaleGroups; }
+
+    // begins the requests of a unit
+    __device__ __forceinline__ void open(int64_t row0, int g0, int g1, bool stall) {
+        prow = row0, pg = g0, pend = g1;
+        if (KIND != 2 && !wide() && lane == 0 && !stall) {
+            const uint32_t bar = bars + 8 * (kStages + (pu % kStages)), n = (uint32_t)(ROWS * 2 * m.G);
+            mb_arrive_expect(bar, n);
+            bulk_load(sides + (pu % kStages) * n, m.scales + row0 * m.G, n, bar);
+        }
+        ++pu;
+    }
+    // requests the next stage of the open unit; false when that was its last
+    __device__ __forceinline__ bool request(bool stall) {
+        const int s = pn % kStages;
+        if (lane == 0 && !stall) {
+            const uint32_t bar = bars + 8 * s;
+            mb_arrive_expect(bar, (uint32_t)(kCodes + kTiles));
+            tma_load_2d(codes + s * kCodes, &m.codes, pg * group_bytes(KIND), (int)prow, bar);
+            if constexpr (KIND == 2)
+                tma_load_2d(sides + s * kTiles, &m.tiles, (int)(prow & 31) * 16, (int)((prow >> 7) * m.G + pg), bar);
+        }
+        ++pn;
+        pg += kGroups;
+        return pg < pend;
+    }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t par) {
+        if (!dead) dead = !__all_sync(0xffffffffu, mb_wait_alone(bar, par, limit, &g_moe_timeouts));
+        return !dead;
+    }
+    // begins reading a unit at its group g0
+    __device__ __forceinline__ void begin(int64_t row0, int g0) {
+        crow = row0, g = g0, left = 0;
+        if (KIND != 2 && !wide()) wait(bars + 8 * (kStages + (cu % kStages)), (uint32_t)(cu / kStages) & 1u);
+        ++cu;
+    }
+    // the stage of group g, of which the unit has `more` with the later ones, is there
+    __device__ __forceinline__ void arrive(int more) {
+        if (left > 0) return;
+        wait(bars + 8 * stage, parity);
+        gi = 0;
+        left = min(kGroups, more);
+    }
+    // shared address of the lane's codes of the current group in 16-row tile w
+    __device__ __forceinline__ uint32_t at(int w) const {
+        const uint32_t base = codes + stage * kCodes + (w * 16 + row) * row_stride(KIND);
+        if constexpr (KIND == 0) return base + (((uint32_t)(2 * gi + (t >> 1)) ^ (uint32_t)row) << 4) + (t & 1) * 8;
+        if constexpr (KIND == 1) return base + gi * 48 + t * 12;
+        return base + (((uint32_t)(4 * gi + t) ^ (uint32_t)row) << 4);
+    }
+    // scale of row `row` + r of the unit at the current group: its bf16 bits, or the lane's byte
+    __device__ __forceinline__ uint32_t scale(int r) const {
         if constexpr (KIND == 2) {
-            p = m.scales + (((row >> 7) * m.G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3)) * 4;
-            step = 512, n = 4;
+            return lds8(sides + stage * kTiles + (gi * ROWS + row + r) * 16 + (int)(crow >> 5 & 3) * 4 + t);
         } else {
-            p = m.scales + (row * m.G + g) * 2;
-            step = 2, n = 2;
+            if (wide()) return ld_stream_u16(m.scales + (crow + row + r) * m.G + g);
+            return lds16(sides + ((cu - 1) % kStages) * (ROWS * 2 * m.G) + ((row + r) * m.G + g) * 2);
         }
     }
-    __device__ __forceinline__ void load(uint32_t dst) {
-        const uintptr_t v = reinterpret_cast<uintptr_t>(p);
-        cp4(dst, reinterpret_cast<const void*>(v & ~(uintptr_t)3), (v & 2) ? 4 : n);
-        p += step;
+    // the current group has been read; true when its stage has, which then can be requested anew
+    __device__ __forceinline__ bool next() {
+        ++g, ++gi;
+        if (gi < left) return false;
+        left = 0;
+        if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1u;
+        }
+        __syncwarp();
+        return true;
+    }
+    // what a wait that gave up left in flight ends, or its own wait does, before the exit
+    __device__ __forceinline__ void drain(bool stall) const {
+        if (!dead || lane != 0 || stall) return;
+        for (int i = pn > kStages ? pn - kStages : 0; i < pn; ++i)
+            mb_drain(bars + 8 * (i % kStages), (uint32_t)(i / kStages) & 1u, limit);
+        if (KIND != 2 && !wide())
+            for (int i = pu > kStages ? pu - kStages : 0; i < pu; ++i)
+                mb_drain(bars + 8 * (kStages + i % kStages), (uint32_t)(i / kStages) & 1u, limit);
     }
 };
-// the next stage of a ring
-__device__ __forceinline__ uint32_t next_stage(uint32_t at, uint32_t base, uint32_t stage) {
-    at += stage;
-    return at == base + kStages * stage ? base : at;
-}
 
 // ---- the pairs grouped by expert ---------------------------------------------------
 struct MoeList {
     unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
     uint32_t blk[kMaxBlocks];                 // expert, first slot << 10, tokens << 20
+    uint16_t first[kMoeMaxExperts];           // first slot of each expert
     uint8_t slot_token[kMaxPairs];
     int scan[2][kMoeWarps];
     int blocks, slots;
@@ -297,7 +376,8 @@ __device__ __forceinline__ int blk_expert(uint32_t b) { return (int)(b & 1023u);
 __device__ __forceinline__ int blk_slot(uint32_t b) { return (int)(b >> 10 & 1023u); }
 __device__ __forceinline__ int blk_count(uint32_t b) { return (int)(b >> 20); }
 
-template <int THREADS>
+// blocks of up to BT tokens
+template <int THREADS, int BT>
 __device__ void build_list(MoeList& L, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < A.E; e += THREADS) L.mask[e] = 0ull;
@@ -312,7 +392,7 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
     for (int e = e0; e < e1; ++e) {
         const int c = __popcll(L.mask[e]);
         slots += c;
-        blocks += (c + kBlockTokens - 1) / kBlockTokens;
+        blocks += (c + BT - 1) / BT;
     }
     int s = slots, b = blocks;
 #pragma unroll
@@ -340,8 +420,9 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
     b -= blocks;
     for (int e = e0; e < e1; ++e) {
         unsigned long long m = L.mask[e];
-        for (int left = __popcll(m); left > 0; left -= kBlockTokens) {
-            const int n = min(kBlockTokens, left);
+        L.first[e] = (uint16_t)s;
+        for (int left = __popcll(m); left > 0; left -= BT) {
+            const int n = min(BT, left);
             L.blk[b++] = (uint32_t)e | (uint32_t)s << 10 | (uint32_t)n << 20;
             for (int i = 0; i < n; ++i) {
                 L.slot_token[s++] = (uint8_t)(__ffsll((long long)m) - 1);
@@ -353,50 +434,66 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
 }
 
 // ---- gate and up -----------------------------------------------------------------------
-template <int KG, int KU>
+template <int KG, int KU, int NS>
 struct MoeUp {
-    static constexpr int kGate = 16 * group_bytes(KG), kUp = 16 * group_bytes(KU);
-    static constexpr int kStage = kGate + kUp + 128;  // codes of gate and up, their scale words
-    static constexpr int kRing = kMoeWarps * kStages * kStage;
-
-    const MoeArgs& A;
-    MoeList& L;
-    float* part;    // [2][warps][sets][256]: partial sums of gate and up, two units deep
-    uint32_t base;  // this warp's ring
-    int lane, warp, r, t, S, s, ui, g0, steps, tiles, units, ustep, sets;
-    int pu, ps, flip;
-    uint32_t to, from;  // the stages to be filled and read next
-    CodeCursor<KG> cg;
-    CodeCursor<KU> cu;
-    ScaleCursor sc;
-
-    // the first request of unit pu: cursors to its rows
-    __device__ __forceinline__ void seek() {
-        if (pu >= units) return;
-        const int blk = pu / tiles, tile = pu - blk * tiles;
-        const int64_t row0 = (int64_t)blk_expert(L.blk[blk]) * A.I + tile * 16;
-        cg.at(A.gate, row0, g0, lane);
-        cu.at(A.up, row0, g0, lane);
-        if (lane < 16) sc.at<KG>(A.gate, row0 + lane, g0);
-        else sc.at<KU>(A.up, row0 + lane - 16, g0);
-        ps = 0;
+    using Gate = Stream<KG, 16>;
+    using Up = Stream<KU, 16>;
+    static constexpr int kWarpRing = Gate::kRing + Up::kRing;
+    static constexpr int kBars = Gate::kBars + Up::kBars;
+    __host__ __device__ static int smem(int G, int S) {
+        return kMoeWarps * (kWarpRing + Gate::side(G) + Up::side(G) + kBars) +
+               (S > 1 ? 2 * kMoeWarps * NS * 1024 : 0) + 1024;
     }
-    __device__ __forceinline__ void issue() {
-        if (pu < units) {
-            cg.load(to, lane);
-            cu.load(to + kGate, lane);
-            sc.load(to + kGate + kUp + 4 * lane);
-            if (++ps == steps) {
-                pu += ustep;
-                seek();
-            }
-        }
-        to = next_stage(to, base, kStage);
-        cp_commit_group();
-    }
+};
 
-    template <int NS>
-    __device__ __forceinline__ void unit(uint32_t block, int tile) {
+template <int KG, int KU, int NS>
+__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant__ MoeArgs A) {
+    using M = MoeUp<KG, KU, NS>;
+    extern __shared__ uint8_t raw[];
+    __shared__ MoeList L;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const int G = A.gate.G, S = A.S, per = kMoeWarps / S, s = warp & (S - 1), ui = warp / S;
+    // rings of all warps, then their scales, then partial sums [2][warps][NS][256] (two units deep), then barriers
+    const uint32_t base = (sm_addr(raw) + 1023u) & ~1023u;
+    const uint32_t ring = base + warp * M::kWarpRing;
+    const uint32_t sides = base + kMoeWarps * M::kWarpRing + warp * (M::Gate::side(G) + M::Up::side(G));
+    const uint32_t part_s = base + kMoeWarps * (M::kWarpRing + M::Gate::side(G) + M::Up::side(G));
+    float* part = reinterpret_cast<float*>(raw + (part_s - sm_addr(raw)));
+    const uint32_t bars = part_s + (S > 1 ? 2 * kMoeWarps * NS * 1024 : 0) + warp * M::kBars;
+    typename M::Gate gate(A.gate, ring, sides, bars, A.wait_cycles);
+    typename M::Up up(A.up, ring + M::Gate::kRing, sides + M::Gate::side(G), bars + M::Gate::kBars, A.wait_cycles);
+    gate.init_bars();
+    up.init_bars();
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_wait();
+    build_list<kMoeThreads, 8 * NS>(L, A);
+    pdl_trigger();
+
+    const int g0 = G * s / S, g1 = G * (s + 1) / S;
+    const int tiles = A.I / 16, units = L.blocks * tiles, ustep = (int)gridDim.x * per;
+    const bool stall = A.stall != 0;
+    auto row_of = [&](int u) {
+        const int blk = u / tiles;
+        return (int64_t)blk_expert(L.blk[blk]) * A.I + (u - blk * tiles) * 16;
+    };
+    // each stream's next unit to request
+    int gu = (int)blockIdx.x * per + ui, uu = gu;
+    auto feed = [&](auto& m, int& u, bool& open) {
+        if (u >= units || m.dead) return;
+        if (!open) m.open(row_of(u), g0, g1, stall);
+        open = m.request(stall);
+        if (!open) u += ustep;
+    };
+    bool gopen = false, uopen = false;
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+        feed(gate, gu, gopen);
+        feed(up, uu, uopen);
+    }
+    int flip = 0;
+    for (int u = (int)blockIdx.x * per + ui; u < units; u += ustep) {
+        const int blk = u / tiles, tile = u - blk * tiles;
+        const uint32_t block = L.blk[blk];
         const int count = blk_count(block), slot0 = blk_slot(block);
         const int64_t row0 = (int64_t)blk_expert(block) * A.I + tile * 16;
         const uint16_t* xr[NS];
@@ -404,57 +501,52 @@ struct MoeUp {
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             have[n] = 8 * n + r < count;
-            xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + g0 * 128 + 32 * t;
+            xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + 32 * t;
         }
-        // parity of the scale's place in its word, for the first group
-        const int pg = (int)((row0 + r) * A.gate.G + g0) & 1;
         float ag[NS][4], au[NS][4];
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = 0.f;
         uint32_t v[NS][16];
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int n = 0; n < NS; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = 0.f;
 #pragma unroll
             for (int q = 0; q < 16; ++q) v[n][q] = 0u;
-        auto load_x = [&](int st) {
+        }
+        gate.begin(row0, g0);
+        up.begin(row0, g0);
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 if (have[n]) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint4 u = ld_act_u4(xr[n] + st * 128 + 8 * q);
-                        v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                        const uint4 w = ld_act_u4(xr[n] + g * 128 + 8 * q);
+                        v[n][4 * q] = w.x, v[n][4 * q + 1] = w.y, v[n][4 * q + 2] = w.z, v[n][4 * q + 3] = w.w;
                     }
                 }
-        };
-        load_x(0);
-        for (int st = 0; st < steps; ++st) {
-            // this group's activations in the order of the decoders' pairs; then the next group's are requested
-            uint32_t p[NS][16], w[NS][16];
+            // the activations in the order of the 4-bit decoder's pairs, where one is to read them
+            uint32_t p[NS][16];
+            if constexpr (KG == 2 || KU == 2) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                if constexpr (KG == 2 || KU == 2) pair_up(p[n], v[n]);
-                if constexpr (KG != 2 || KU != 2) {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
-                }
+                for (int n = 0; n < NS; ++n) pair_up(p[n], v[n]);
             }
-            if (NS == 1 && st + 1 < steps) load_x(st + 1);
-            cp_wait_groups<kStages - 2>();
-            __syncwarp();
-            const bool odd = ((pg + st) & 1) != 0;
-            group_product<KG, NS>(from + r * group_bytes(KG), from + kGate + kUp + 4 * r, odd, t, KG == 2 ? p : w, ag);
-            group_product<KU, NS>(from + kGate + r * group_bytes(KU), from + kGate + kUp + 64 + 4 * r, odd, t,
-                                  KU == 2 ? p : w, au);
-            if (NS > 1 && st + 1 < steps) load_x(st + 1);
-            from = next_stage(from, base, kStage);
-            __syncwarp();
-            issue();
+            gate.arrive(g1 - g);
+            group_product<KG, NS>(gate.at(0), gate.scale(0), gate.scale(8), KG == 2 ? p : v, ag);
+            if (gate.next()) feed(gate, gu, gopen);
+            up.arrive(g1 - g);
+            group_product<KU, NS>(up.at(0), up.scale(0), up.scale(8), KU == 2 ? p : v, au);
+            if (up.next()) feed(up, uu, uopen);
+        }
+        const bool dead = gate.dead || up.dead;
+        if (dead) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = kMoeNaN;
         }
         if (S > 1) {
-            float* mine = part + ((flip * kMoeWarps + warp) * sets) * 256 + lane;
+            float* mine = part + ((flip * kMoeWarps + warp) * NS) * 256 + lane;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -462,7 +554,9 @@ struct MoeUp {
                     mine[n * 256 + i * 32] = ag[n][i];
                     mine[n * 256 + 128 + i * 32] = au[n][i];
                 }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + ui), "r"(S * 32) : "memory");
+            // (constant barrier numbers: with a variable one a CTA holds all sixteen, and four CTAs fill the SM)
+            if (ui == 0) asm volatile("bar.sync 1, %0;" ::"r"(S * 32) : "memory");
+            else asm volatile("bar.sync 2, %0;" ::"r"(S * 32) : "memory");
             // warp s of the unit finishes registers s, s + S, ... of every set
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -471,7 +565,7 @@ struct MoeUp {
                     if ((i & (S - 1)) != s) continue;
                     float sg = 0.f, su = 0.f;
                     for (int w = 0; w < S; ++w) {
-                        const float* q = part + ((flip * kMoeWarps + ui * S + w) * sets + n) * 256 + i * 32 + lane;
+                        const float* q = part + ((flip * kMoeWarps + ui * S + w) * NS + n) * 256 + i * 32 + lane;
                         sg += q[0];
                         su += q[128];
                     }
@@ -486,156 +580,113 @@ struct MoeUp {
             for (int i = 0; i < 4; ++i) {
                 const int col = 8 * n + 2 * t + (i & 1);
                 if ((i & (S - 1)) != s || col >= count) continue;
-                const float g = ag[n][i], h = g / (1.f + expf(-g)) * au[n][i];
-                int c = tile * 16 + r + 8 * (i >> 1);
+                const float gv = ag[n][i], h = gv / (1.f + expf(-gv)) * au[n][i];
+                // h in the order in which the down kernel's lanes read a 128-group: 16-byte pieces (q, t)
+                int c = (tile & 7) * 16 + gate.row + 8 * (i >> 1);
                 if (A.hperm) c = (c & ~7) | (c & 3) << 1 | (c >> 2 & 1);
-                A.h[(int64_t)(slot0 + col) * A.I + c] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+                c = ((c >> 3 & 3) << 2 | c >> 5) << 3 | (c & 7);
+                A.h[(int64_t)(slot0 + col) * A.I + (tile >> 3) * 128 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
             }
     }
-};
-
-template <int KG, int KU>
-__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant__ MoeArgs A) {
-    using Up = MoeUp<KG, KU>;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeList L;
-    pdl_wait();
-    build_list<kMoeThreads>(L, A);
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = A.S, per = kMoeWarps / S;
-    Up u{A, L, reinterpret_cast<float*>(ring + Up::kRing), sm_addr(ring) + (uint32_t)(warp * kStages * Up::kStage)};
-    u.lane = lane, u.warp = warp, u.r = lane >> 2, u.t = lane & 3;
-    u.S = S, u.s = warp & (S - 1), u.ui = warp / S;
-    u.g0 = A.gate.G * u.s / S;
-    u.steps = A.gate.G * (u.s + 1) / S - u.g0;
-    u.tiles = A.I / 16;
-    u.units = L.blocks * u.tiles;
-    u.ustep = (int)gridDim.x * per;
-    u.sets = A.T > 8 ? 2 : 1;
-    u.pu = (int)blockIdx.x * per + u.ui;
-    u.ps = u.flip = 0;
-    u.to = u.from = u.base;
-    u.cg.init(A.gate, lane);
-    u.cu.init(A.up, lane);
-    u.seek();
-    for (int i = 0; i < kStages - 1; ++i) u.issue();
-    for (int v = (int)blockIdx.x * per + u.ui; v < u.units; v += u.ustep) {
-        const int blk = v / u.tiles;
-        const uint32_t block = L.blk[blk];
-        if (blk_count(block) > 8) u.template unit<2>(block, v - blk * u.tiles);
-        else u.template unit<1>(block, v - blk * u.tiles);
-    }
-    cp_wait_groups<0>();
+    gate.drain(stall);
+    up.drain(stall);
 }
 
 // ---- down and the weighted sum ------------------------------------------------------------
-constexpr int kDownRows = 32;    // of a CTA: each warp holds all of them, two tiles that share h's fragments
-constexpr int kDownStages = 3;
+constexpr int kDownRows = 32;  // of a CTA: each warp holds all of them, two tiles that share h's fragments
+
+// slices of a block's groups: enough tasks for the warps that share a tile, as far as z holds them
+__device__ __forceinline__ int down_slices(int G, int warps, int blocks, int slots, int zrows) {
+    if (blocks == 0) return 1;
+    return max(1, min(min(G, (3 * warps + blocks - 1) / blocks), zrows / slots));
+}
 
 template <int KIND>
 struct MoeDown {
-    static constexpr int kCodes = 16 * group_bytes(KIND);
-    static constexpr int kStage = 2 * kCodes + 128;
-    static constexpr int kRing = kMoeWarps * kDownStages * kStage;
+    using W = Stream<KIND, kDownRows>;
+    __host__ __device__ static int smem(int G) { return kMoeWarps * (W::kRing + W::side(G) + W::kBars) + 1024; }
+};
 
-    const MoeArgs& A;
-    MoeList& L;
-    const float* slot_w;
-    float* sum;     // this warp's [T][kDownRows]
-    uint32_t base;  // this warp's ring
-    int lane, r, t, G, tasks, KS, step;
-    int64_t wrow;
-    int pq, ps, pend;   // the next request: task, group, end of the task's groups
-    uint32_t to, from;  // the stages to be filled and read next
-    CodeCursor<KIND> codes;
-    int64_t tile2;  // from a piece of the first tile to that of the second
-    ScaleCursor sc;
-
-    __device__ __forceinline__ void range(int q, int& b, int& g0, int& g1) const {
-        b = q / KS;
-        const int k = q - b * KS;
-        g0 = G * k / KS;
-        g1 = G * (k + 1) / KS;
-    }
-    __device__ __forceinline__ void seek() {
-        if (pq >= tasks) return;
-        int b;
-        range(pq, b, ps, pend);
-        const int64_t row0 = (int64_t)blk_expert(L.blk[b]) * A.H + wrow;
-        codes.at(A.down, row0, ps, lane);
-        sc.at<KIND>(A.down, row0 + lane, ps);
-    }
-    __device__ __forceinline__ void issue() {
-        if (pq < tasks) {
-            CodeCursor<KIND> second = codes;
-            second.p += tile2;
-            second.load(to + kCodes, lane);
-            codes.load(to, lane);
-            sc.load(to + 2 * kCodes + 4 * lane);
-            if (++ps == pend) {
-                pq += step;
-                seek();
-            }
+template <int KIND, int NS>
+__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
+    using M = MoeDown<KIND>;
+    extern __shared__ uint8_t raw[];
+    __shared__ MoeList L;
+    __shared__ float slot_w[kMaxPairs];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, C = A.C, G = A.down.G;
+    const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
+    const uint32_t base = (sm_addr(raw) + 1023u) & ~1023u;
+    typename M::W w(A.down, base + warp * M::W::kRing, base + kMoeWarps * M::W::kRing + warp * M::W::side(G),
+                    base + kMoeWarps * (M::W::kRing + M::W::side(G)) + warp * M::W::kBars, A.wait_cycles);
+    w.init_bars();
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the kernel before waited for its inputs: ids and weights are final, only h is not
+    build_list<kMoeThreads, 8 * NS>(L, A);
+    float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
+    // blocks fewer than the warps that share them: their groups are split too
+    const int step = C * kMoeWarps, KS = down_slices(G, step, L.blocks, L.slots, A.zrows), tasks = L.blocks * KS;
+    const bool stall = A.stall != 0;
+    int pq = rank * kMoeWarps + warp;  // the next task to request
+    bool open = false;
+    auto feed = [&]() {
+        if (pq >= tasks || w.dead) return;
+        if (!open) {
+            const int b = pq / KS, k = pq - b * KS;
+            w.open((int64_t)blk_expert(L.blk[b]) * A.H + (int64_t)tile * kDownRows, G * k / KS, G * (k + 1) / KS, stall);
         }
-        to += kStage;
-        if (to == base + kDownStages * kStage) to = base;
-        cp_commit_group();
+        open = w.request(stall);
+        if (!open) pq += step;
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) feed();
+    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
+        const uint32_t blk = L.blk[b];
+        for (int i = 0; i < blk_count(blk); ++i) {
+            const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
+            float v = 0.f;  // a token may name an expert more than once
+            for (int j = 0; j < A.k; ++j)
+                if (A.ids[tok * A.k + j] == blk_expert(blk)) v += A.weights[tok * A.k + j];
+            slot_w[slot] = v;
+        }
     }
-
-    template <int NS>
-    __device__ __forceinline__ void block(uint32_t b, int g0, int g1) {
-        const int count = blk_count(b), slot0 = blk_slot(b);
-        const int64_t row0 = (int64_t)blk_expert(b) * A.H + wrow;
-        const int pg = (int)((row0 + r) * A.down.G) & 1;  // 16 rows on it is the same
+    __syncthreads();
+    pdl_wait();
+    for (int q = rank * kMoeWarps + warp; q < tasks; q += step) {
+        const int b = q / KS, k = q - b * KS, g0 = G * k / KS, g1 = G * (k + 1) / KS;
+        const uint32_t block = L.blk[b];
+        const int count = blk_count(block), slot0 = blk_slot(block);
         const uint16_t* hp[NS];
         bool have[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             have[n] = 8 * n + r < count;
-            hp[n] = A.h + (int64_t)(slot0 + (have[n] ? 8 * n + r : 0)) * A.I + 32 * t;
+            hp[n] = A.h + (int64_t)(slot0 + (have[n] ? 8 * n + r : 0)) * A.I + 8 * t;
         }
         float acc[2][NS][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
         uint32_t v[NS][16];
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int n = 0; n < NS; ++n) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) v[n][q] = 0u;
-        auto load_h = [&](int g) {
+            for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[n][j] = 0u;
+        }
+        w.begin((int64_t)blk_expert(block) * A.H + (int64_t)tile * kDownRows, g0);
+#pragma unroll 1
+        for (int g = g0; g < g1; ++g) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 if (have[n]) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 u = ldg_plain(hp[n] + g * 128 + 8 * q);
-                        v[n][4 * q] = u.x, v[n][4 * q + 1] = u.y, v[n][4 * q + 2] = u.z, v[n][4 * q + 3] = u.w;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 u = ldg_plain(hp[n] + g * 128 + 32 * j);
+                        v[n][4 * j] = u.x, v[n][4 * j + 1] = u.y, v[n][4 * j + 2] = u.z, v[n][4 * j + 3] = u.w;
                     }
                 }
-        };
-        load_h(g0);
-        for (int g = g0; g < g1; ++g) {
-            uint32_t w[NS][16];
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-#pragma unroll
-                for (int q = 0; q < 16; ++q) w[n][q] = v[n][q];
-            if (NS == 1 && g + 1 < g1) load_h(g + 1);
-            cp_wait_groups<kDownStages - 2>();
-            __syncwarp();
-            const bool odd = ((pg + g) & 1) != 0;
-            group_product<KIND, NS>(from + r * group_bytes(KIND), from + 2 * kCodes + 4 * r, odd, t, w, acc[0]);
-            group_product<KIND, NS>(from + kCodes + r * group_bytes(KIND), from + 2 * kCodes + 64 + 4 * r, odd, t, w,
-                                    acc[1]);
-            if (NS > 1 && g + 1 < g1) load_h(g + 1);
-            from += kStage;
-            if (from == base + kDownStages * kStage) from = base;
-            __syncwarp();
-            issue();
+            w.arrive(g1 - g);
+            group_product<KIND, NS>(w.at(0), w.scale(0), w.scale(8), v, acc[0]);
+            group_product<KIND, NS>(w.at(1), w.scale(16), w.scale(24), v, acc[1]);
+            if (w.next()) feed();
         }
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -643,122 +694,70 @@ struct MoeDown {
             for (int j = 0; j < 2; ++j) {
                 const int tok = 8 * n + 2 * t + j;
                 if (tok >= count) continue;
-                const float w = slot_w[slot0 + tok];
-                float* p = sum + L.slot_token[slot0 + tok] * kDownRows + r;
+                const int slot = slot0 + tok;
+                float* p = z + ((int64_t)slot * KS + k) * kDownRows + w.row;
+                const float f = w.dead ? kMoeNaN : slot_w[slot];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    p[16 * m] = fmaf(w, acc[m][n][j], p[16 * m]);
-                    p[16 * m + 8] = fmaf(w, acc[m][n][2 + j], p[16 * m + 8]);
+                    p[16 * m] = f * acc[m][n][j];
+                    p[16 * m + 8] = f * acc[m][n][2 + j];
                 }
             }
-        __syncwarp();
     }
-};
-
-template <int KIND>
-__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
-    using Down = MoeDown<KIND>;
-    extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ MoeList L;
-    __shared__ float slot_w[kMaxPairs];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = A.C;
-    const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
-    float* sum = reinterpret_cast<float*>(ring + Down::kRing);  // [warps][T][kDownRows]
-    const int sums = A.T * kDownRows;
-    // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list<kMoeThreads>(L, A);
-    Down d{A, L, slot_w, sum + warp * sums, sm_addr(ring) + (uint32_t)(warp * kDownStages * Down::kStage)};
-    d.lane = lane, d.r = lane >> 2, d.t = lane & 3;
-    d.G = A.down.G;
-    d.step = C * kMoeWarps;
-    // blocks fewer than the warps that share them: their groups are split too
-    d.KS = max(1, min(d.G, d.step / max(1, L.blocks)));
-    d.tasks = L.blocks * d.KS;
-    d.wrow = (int64_t)tile * kDownRows;
-    d.tile2 = 16 * A.down.rb;
-    const int q0 = rank * kMoeWarps + warp;
-    d.pq = q0;
-    d.to = d.from = d.base;
-    d.codes.init(A.down, lane);
-    d.seek();
-    for (int i = 0; i < kDownStages - 1; ++i) d.issue();
-    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
-        const uint32_t blk = L.blk[b];
-        for (int i = 0; i < blk_count(blk); ++i) {
-            const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
-            float w = 0.f;  // a token may name an expert more than once
-            for (int j = 0; j < A.k; ++j)
-                if (A.ids[tok * A.k + j] == blk_expert(blk)) w += A.weights[tok * A.k + j];
-            slot_w[slot] = w;
-        }
-    }
-    for (int i = threadIdx.x; i < kMoeWarps * sums; i += kMoeThreads) sum[i] = 0.f;
-    __syncthreads();
-    pdl_wait();
-    for (int q = q0; q < d.tasks; q += d.step) {
-        int b, g0, g1;
-        d.range(q, b, g0, g1);
-        const uint32_t blk = L.blk[b];
-        if (blk_count(blk) > 8) d.template block<2>(blk, g0, g1);
-        else d.template block<1>(blk, g0, g1);
-    }
-    cp_wait_groups<0>();
-    if (C > 1) {
+    w.drain(stall);
+    __syncwarp();
+    if (C > 1) {  // the cluster's z is complete
         cluster_arrive();
         cluster_wait();
     } else {
         __syncthreads();
     }
-    // the warps' sums, rank by rank; rank q finishes tokens q, q + C, ...
-    const uint32_t sum_s = sm_addr(sum);
-    for (int i = threadIdx.x; i < sums; i += kMoeThreads) {
-        const int tok = i / kDownRows, row = i - tok * kDownRows;
-        if (tok % C != rank) continue;
+    // a token's slots in the order of its choices, a slot's slices in order; rank q finishes tokens q, q + C, ...
+    for (int i = threadIdx.x; i < (A.T - rank + C - 1) / C * kDownRows; i += kMoeThreads) {
+        const int tok = rank + i / kDownRows * C, row = i % kDownRows;
         float v = 0.f;
-        for (int q = 0; q < C; ++q)
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
-                const int j = w * sums + i;
-                float pq;
-                if (C > 1)
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(pq)
-                                 : "r"(map_rank(sum_s + 4 * j, (uint32_t)q))
-                                 : "memory");
-                else
-                    pq = sum[j];
-                v += pq;
-            }
+        for (int j = 0; j < A.k; ++j) {
+            const int e = A.ids[tok * A.k + j];
+            if (e < 0 || e >= A.E) continue;
+            bool seen = false;
+            for (int q = 0; q < j; ++q) seen |= A.ids[tok * A.k + q] == e;
+            if (seen) continue;  // its slot holds all its weights
+            const int slot = L.first[e] + __popcll(L.mask[e] & ((1ull << tok) - 1));
+            const float* p = z + (int64_t)slot * KS * kDownRows + row;
+            for (int q = 0; q < KS; ++q) v += __ldcg(p + q * kDownRows);
+        }
         const int64_t at = (int64_t)tok * A.ldy + (int64_t)tile * kDownRows + row;
         if (A.ydt == kF32) static_cast<float*>(A.y)[at] = v;
         else static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(v);
     }
-    if (C > 1) {  // no CTA leaves while another reads its sums
-        cluster_arrive();
-        cluster_wait();
-    }
 }
 
-struct KernelOf {
+struct UpKernel {
     const void* fn;
-    int ring;
+    int (*smem)(int G, int S);
 };
-template <int KG, int KU>
-KernelOf up_of() {
-    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU>), MoeUp<KG, KU>::kRing};
+template <int KG, int KU, int NS>
+UpKernel up_of() {
+    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), &MoeUp<KG, KU, NS>::smem};
 }
-KernelOf up_kernel(int kg, int ku) {
-    static const KernelOf table[3][3] = {{up_of<0, 0>(), up_of<0, 1>(), up_of<0, 2>()},
-                                         {up_of<1, 0>(), up_of<1, 1>(), up_of<1, 2>()},
-                                         {up_of<2, 0>(), up_of<2, 1>(), up_of<2, 2>()}};
+template <int NS>
+UpKernel up_kernel(int kg, int ku) {
+    static const UpKernel table[3][3] = {{up_of<0, 0, NS>(), up_of<0, 1, NS>(), up_of<0, 2, NS>()},
+                                         {up_of<1, 0, NS>(), up_of<1, 1, NS>(), up_of<1, 2, NS>()},
+                                         {up_of<2, 0, NS>(), up_of<2, 1, NS>(), up_of<2, 2, NS>()}};
     return table[kg][ku];
 }
-template <int KIND>
-KernelOf down_of() {
-    return {reinterpret_cast<const void*>(&k_moe_down<KIND>), MoeDown<KIND>::kRing};
+struct DownKernel {
+    const void* fn;
+    int (*smem)(int G);
+};
+template <int KIND, int NS>
+DownKernel down_of() {
+    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), &MoeDown<KIND>::smem};
 }
-KernelOf down_kernel(int kind) {
-    static const KernelOf table[3] = {down_of<0>(), down_of<1>(), down_of<2>()};
+template <int NS>
+DownKernel down_kernel(int kind) {
+    static const DownKernel table[3] = {down_of<0, NS>(), down_of<1, NS>(), down_of<2, NS>()};
     return table[kind];
 }
 
@@ -774,34 +773,75 @@ int moe_sms() {
     return sms[dev];
 }
 
-MoeMat make_mat(const MoeWeights& w, int64_t K) {
-    MoeMat m;
-    m.packed = static_cast<const uint8_t*>(w.packed);
-    m.scales = static_cast<const uint8_t*>(w.scales);
-    m.kind = w.grid == kMx4 ? 2 : (w.grid == kInt3 ? 1 : 0);
-    m.G = (int32_t)(K / kGroup);
-    m.rb = (int64_t)m.G * group_bytes(m.kind);
-    return m;
+// `rows`: of a unit
+bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K, int rows) {
+    TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    m->scales = static_cast<const uint16_t*>(w.scales);
+    m->kind = w.grid == kMx4 ? 2 : (w.grid == kInt3 ? 1 : 0);
+    m->G = (int32_t)(K / kGroup);
+    const cuuint32_t one[2] = {1, 1};
+    {
+        const cuuint64_t rb = (cuuint64_t)m->G * group_bytes(m->kind);
+        const cuuint64_t dims[2] = {rb, (cuuint64_t)N}, strides[1] = {rb};
+        const cuuint32_t box[2] = {(cuuint32_t)row_stride(m->kind), (cuuint32_t)rows};
+        if (enc(&m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w.packed), dims, strides, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, m->kind == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    if (m->kind == 2) {
+        const cuuint64_t dims[2] = {512, (cuuint64_t)((N + 127) / 128 * m->G)}, strides[1] = {512};
+        const cuuint32_t box[2] = {(cuuint32_t)(16 * rows), (cuuint32_t)stage_groups(2)};
+        if (rows * 16 > 256) {  // a box holds at most 256 elements of a dimension: as 32-bit words
+            const cuuint64_t d4[2] = {128, dims[1]};
+            const cuuint32_t b4[2] = {(cuuint32_t)(4 * rows), box[1]};
+            return enc(&m->tiles, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(w.scales), d4, strides, b4, one,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+        }
+        return enc(&m->tiles, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w.scales), dims, strides, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    return true;
+}
+
+// One split of the SM's memory for both kernels: with one of its own each, an SM is emptied and set up anew between them.
+cudaError_t shape_kernel(const void* fn) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
 }  // namespace
 
-size_t moe_data_bytes(int64_t T, int k, int64_t I) { return (size_t)((T * k * I * 2 + 255) / 256 * 256); }
+namespace {
+size_t h_bytes(int64_t T, int k, int64_t I) { return (size_t)((T * k * I * 2 + 255) / 256 * 256); }
+// rows of z: a slot's per slice of its groups
+int64_t z_rows(int64_t T, int k) { return std::max<int64_t>(T * k, kMoeSliceRows); }
+}  // namespace
+
+size_t moe_data_bytes(int64_t T, int k, int64_t H, int64_t I) { return h_bytes(T, k, I) + (size_t)(z_rows(T, k) * H * 4); }
 
 cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWeights& down, int E, int64_t H, int64_t I,
                        const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int T, int k, void* y,
-                       int ydt, int64_t ldy, void* data, cudaStream_t st) {
+                       int ydt, int64_t ldy, void* data, long long wait_cycles, bool stall, cudaStream_t st) {
     const int sms = moe_sms();
     if (sms <= 0) return cudaErrorInitializationError;
     MoeArgs A;
     std::memset(&A, 0, sizeof(A));
-    A.gate = make_mat(gate, H);
-    A.up = make_mat(up, H);
-    A.down = make_mat(down, I);
+    if (!make_mat(&A.gate, gate, E * I, H, 16) || !make_mat(&A.up, up, E * I, H, 16) ||
+        !make_mat(&A.down, down, E * H, I, kDownRows))
+        return cudaErrorInvalidValue;
+    A.wait_cycles = wait_cycles;
+    A.stall = stall ? 1 : 0;
     A.x = x;
     A.ids = ids;
     A.weights = weights;
     A.h = static_cast<uint16_t*>(data);
+    A.z = reinterpret_cast<float*>(static_cast<char*>(data) + h_bytes(T, k, I));
+    A.zrows = (int32_t)z_rows(T, k);
     A.y = y;
     A.ldx = ldx;
     A.ldy = ldy;
@@ -812,16 +852,19 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.I = (int32_t)I;
     A.ydt = ydt;
     // units that the pairs can make at most; warps split K while they would leave the GPU's warps idle
-    const int64_t units = (int64_t)std::min(T * k, E + T * k / kBlockTokens) * (I / 16);
+    const int64_t units = (int64_t)std::min(T * k, E + T * k / 8) * (I / 16);
     A.S = 1;
     while (A.S < kMoeWarps && units * A.S < (int64_t)sms * 16 && A.gate.G >= 2 * A.S) A.S *= 2;
     A.hperm = A.down.kind == 2 ? 1 : 0;
-    const KernelOf ku = up_kernel(A.gate.kind, A.up.kind), kd = down_kernel(A.down.kind);
-    const int up_smem = ku.ring + (A.S > 1 ? 2 * kMoeWarps * (T > 8 ? 2 : 1) * 1024 : 0);
-    const int down_smem = kd.ring + T * kMoeWarps * kDownRows * 4;
-    cudaError_t e = cudaFuncSetAttribute(ku.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    // Sets of eight columns that share a decode: one while an expert's tokens seldom exceed eight, else two (a second
+    // set costs about a tenth of a product, a second decode a whole one)
+    const int NS = T * k > 5 * E ? 2 : 1;
+    const UpKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
+    const DownKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
+    const int up_smem = ku.smem(A.gate.G, A.S), down_smem = kd.smem(A.down.G);
+    cudaError_t e = shape_kernel(ku.fn);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kd.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    e = shape_kernel(kd.fn);
     if (e != cudaSuccess) return e;
     int per_sm = 0, down_per_sm = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ku.fn, kMoeThreads, (size_t)up_smem);
@@ -831,7 +874,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     if (per_sm < 1 || down_per_sm < 1) return cudaErrorInvalidConfiguration;
     // CTAs per cluster of the down kernel: the count whose waves, each as long as a warp's share of the blocks that
     // the tokens are expected to fill (in sixteenths of a block), end first
-    const double filled = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T)) + T * k / (double)(2 * kBlockTokens);
+    const double filled = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T)) + T * k / (16.0 * NS);
     double best = 0;
     for (int c = 1; c <= 8; ++c) {
         const int64_t waves = (H / kDownRows * c + (int64_t)sms * down_per_sm - 1) / ((int64_t)sms * down_per_sm);
@@ -857,6 +900,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     e = cudaLaunchKernelExC(&cfg, ku.fn, args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
+    cfg.blockDim = dim3(kMoeThreads);
     cfg.dynamicSmemBytes = (size_t)down_smem;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -865,6 +909,13 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     return cudaLaunchKernelExC(&cfg, kd.fn, args);
+}
+
+unsigned int take_moe_timeouts() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_moe_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (cudaMemcpyToSymbol(g_moe_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    return v;
 }
 
 }  // namespace tb

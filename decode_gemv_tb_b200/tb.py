@@ -53,7 +53,7 @@ SIGNATURES = {
     "tb_mx4_dequantize": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
     "tb_moe_route": (_I32, [_P, _I64, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _P]),
     "tb_moe_workspace_bytes": (_SZ, [_P, _I64, _I32]),
-    "tb_moe": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _I64, _P, _SZ, _P]),
+    "tb_moe": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _P, _I32, _I64, ctypes.c_uint, _P, _SZ, _P]),
     "tb_mx4_gemm": (_I32, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, ctypes.c_uint, _P]),
 }
 
@@ -444,7 +444,7 @@ def moe_workspace_bytes(layer: MoELayer, T: int, k: int) -> int:
 
 
 def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None,
-           out_dtype=torch.float32, ws: torch.Tensor | None = None, stream: int | None = None) -> torch.Tensor:
+           out_dtype=torch.float32, ws: torch.Tensor | None = None, flags: int = 0, stream: int | None = None) -> torch.Tensor:
     """y [T][H] = the routed experts' MLP of x [T][H] (bf16, rows may be strided), summed with the weights."""
     T, k = ids.shape
     H = layer.desc.H
@@ -458,6 +458,6 @@ def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.T
     ldy = _rows(y, "y", T, H)
     if ws is None:
         ws = workspace(moe_workspace_bytes(layer, T, k), x.device)
-    _check(load().tb_moe(layer.ptr, x.data_ptr(), ldx, ip, wp, T, k, y.data_ptr(), _ydtype(y.dtype), ldy,
+    _check(load().tb_moe(layer.ptr, x.data_ptr(), ldx, ip, wp, T, k, y.data_ptr(), _ydtype(y.dtype), ldy, flags,
                          _dev(ws, "workspace"), ws.numel(), _stream(x) if stream is None else stream), "tb_moe")
     return y

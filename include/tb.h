@@ -447,8 +447,8 @@ typedef struct {
     int64_t H, I;                                         /* positive multiples of 128, at most 2^20 */
 } tb_moe_t;
 
-/* Workspace bytes of tb_moe: 2 * ceil256(2 T k I) (data only); 0 for bad
- * arguments. */
+/* Workspace bytes of tb_moe (data only): 2 * (ceil256(2 T k I) + 4 H max(T k,
+ * 128)), the pairs' gated activations and their results; 0 for bad arguments. */
 TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
 
 /* The routed experts of T tokens in two launches:
@@ -462,6 +462,7 @@ TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
  *              without experts gets y = 0.
  *   weights    [T][k] fp32.
  *   y          [T][ldy] fp32 or bf16, ldy >= H, written for columns < H.
+ *   flags      0 (test hook: TB_FLAG_TEST_STALL).
  *   workspace  tb_moe_workspace_bytes(layer, T, k) bytes (rules above).
  * Codes (times their scale, for MX4) are decoded exactly, sums are fp32;
  * bitwise deterministic.  With u = 2^-24 and A(v)
@@ -471,8 +472,8 @@ TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
  *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/8 + k + 24) u A_down(|h| + |dh|))
  * (plus 2^-8 |y| for bf16 outputs). */
 TB_API tb_status_t tb_moe(const tb_moe_t *layer, const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
-                          int64_t T, int k, void *y, tb_dtype_t y_dtype, int64_t ldy, void *workspace,
-                          size_t workspace_bytes, tb_stream_t stream);
+                          int64_t T, int k, void *y, tb_dtype_t y_dtype, int64_t ldy, unsigned flags,
+                          void *workspace, size_t workspace_bytes, tb_stream_t stream);
 
 /* Size of the fixed device scratch behind tb_gemv_noalloc (4 MiB). */
 #define TB_NOALLOC_SCRATCH_BYTES (4u << 20)

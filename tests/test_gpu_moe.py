@@ -240,6 +240,53 @@ def test_moe_batch_rows_are_independent():
     assert torch.equal(y[keep, :256], y2[keep]) and torch.isnan(y2[3]).all()
 
 
+def test_moe_long_rows():
+    """Rows of more 128-groups than their scales are copied whole for."""
+    g = torch.Generator().manual_seed(16)
+    for grids, H, I in (((0, 2, 1), 128 * 67, 128), ((2, 4, 2), 256, 128 * 65), ((1, 0, 4), 128 * 65, 128 * 3)):
+        mats, layer = make_layer(2, H, I, grids, H + I)
+        x = torch.randn((3, H), generator=g).to(torch.bfloat16)
+        check_moe(mats, layer, x, draw_ids(3, 2, 2, g), torch.rand((3, 2), generator=g))
+
+
+def test_moe_waits_that_give_up_are_reported():
+    """The copies are never issued: every wait gives up after about 10 ms, the outputs of tokens with experts are NaN,
+    the status says so, and the next call is correct."""
+    g = torch.Generator().manual_seed(17)
+    for grids, T in (((0, 2, 4), 1), ((4, 1, 2), 20)):
+        mats, layer = make_layer(4, 256, 256, grids, 18)
+        x = torch.randn((T, 256), generator=g).to(torch.bfloat16)
+        ids, w = draw_ids(T, 2, 4, g), torch.rand((T, 2), generator=g) + 0.1
+        y = tb.tb_moe(layer, x.to(DEV), ids.to(DEV), w.to(DEV), flags=tb.FLAG_TEST_STALL)
+        assert tb.sync_status() == 6 and torch.isnan(y).all()
+        check_moe(mats, layer, x, ids, w)
+        assert tb.sync_status() == 0
+
+
+def test_moe_large_scales():
+    """4-bit scales across their range: below 2^1 (one factor), above it (two), 255 (no number, in its row only)."""
+    rng = np.random.default_rng(19)
+    H = I = 128
+    wg, g = R.random_matrix(2 * I, H, R.INT2, rng)
+    wu, u = R.random_matrix(2 * I, H, R.INT2, rng)
+    c, b = R.random_mx4(2 * H, I, rng)
+    b[:, 0], b[5, 1], b[6, 2], b[7, 3] = 127, 129, 200, 240
+    b[130, 1], b[131, 1], b[132, 1] = 128, 1, 0
+    p, s = R.to_gpu(c, b)
+    layer = tb.moe_layer(g, u, (p, s, R.MX4), 2, H, I)
+    gen = torch.Generator().manual_seed(19)
+    x = torch.randn((2, H), generator=gen).to(torch.bfloat16)
+    ids, w = torch.tensor([[0, 1], [1, -1]], dtype=torch.int32), torch.rand((2, 2), generator=gen)
+    check_moe((wg, wu, torch.from_numpy(R.values(c, b)).to(DEV)), layer, x, ids, w)
+    b[9, 2] = 255
+    p, s = R.to_gpu(c, b)
+    layer = tb.moe_layer(g, u, (p, s, R.MX4), 2, H, I)
+    y = tb.tb_moe(layer, x.to(DEV), ids.to(DEV), w.to(DEV))
+    want = torch.zeros(2, H, dtype=torch.bool)
+    want[0, 9] = True
+    assert torch.equal(torch.isnan(y).cpu(), want)
+
+
 def test_routed_layer_run():
     """The operators as a decoder uses them: weights quantised and packed by the library (scalar grid for gate and up,
     4-bit floats for down), tokens routed, experts applied -- in one stream, captured and replayed."""

@@ -29,24 +29,24 @@ def layer(**kw):
 
 
 def test_workspace(lib):
-    for T, k, I in ((1, 1, 128), (1, 8, 768), (64, 16, 1536), (7, 3, 640)):
-        want = 2 * (-(-2 * T * k * I // 256) * 256)
-        assert lib.tb_moe_workspace_bytes(ctypes.addressof(l := layer(I=I, E=16)), T, k) == want, l
+    for T, k, H, I in ((1, 1, 128, 128), (1, 8, 2048, 768), (64, 16, 4096, 1536), (7, 3, 384, 640)):
+        want = 2 * (-(-2 * T * k * I // 256) * 256 + 4 * H * max(T * k, 128))
+        assert lib.tb_moe_workspace_bytes(ctypes.addressof(l := layer(H=H, I=I, E=16)), T, k) == want, l
     assert lib.tb_moe_workspace_bytes(0, 1, 1) == 0
     assert lib.tb_moe_workspace_bytes(ctypes.addressof(l := layer()), 65, 1) == 0
 
 
 def test_moe_refusals(lib):
-    def f(l=None, x=A, ldx=256, ids=A, w=A, T=4, k=2, y=A, dt=0, ldy=256, ws=A, nws=W, **kw):
+    def f(l=None, x=A, ldx=256, ids=A, w=A, T=4, k=2, y=A, dt=0, ldy=256, flags=0, ws=A, nws=W, **kw):
         d = layer(**kw)
-        return lib.tb_moe(ctypes.addressof(d) if l is None else l, x, ldx, ids, w, T, k, y, dt, ldy, ws, nws, 0)
+        return lib.tb_moe(ctypes.addressof(d) if l is None else l, x, ldx, ids, w, T, k, y, dt, ldy, flags, ws, nws, 0)
     assert f(l=0) == ARG and f(x=0) == ARG and f(ids=0) == ARG and f(w=0) == ARG and f(y=0) == ARG and f(ws=0) == ARG
     for n in ("gate", "up", "down", "gate_scales", "up_scales", "down_scales"):
         assert f(**{n: 0}) == ARG and f(**{n: A + 8}) == ALIGN
     for n in ("gate_grid", "up_grid", "down_grid"):
         assert f(**{n: 3}) == UNSUPPORTED and f(**{n: 5}) == ARG and f(**{n: -1}) == ARG
-    assert f(k=0) == ARG and f(k=17) == ARG and f(E=0) == ARG and f(E=513) == ARG and f(dt=2) == ARG
-    assert f(nws=2 * 2048 - 1) == ARG
+    assert f(k=0) == ARG and f(k=17) == ARG and f(E=0) == ARG and f(E=513) == ARG and f(dt=2) == ARG and f(flags=1) == ARG
+    assert f(nws=2 * (2048 + 4 * 256 * 128) - 1) == ARG
     assert f(T=0) == SHAPE and f(T=65) == SHAPE and f(H=200) == SHAPE and f(I=64) == SHAPE and f(I=0) == SHAPE
     assert f(H=(1 << 20) + 128, ldx=1 << 21, ldy=1 << 21) == SHAPE and f(ldx=248) == SHAPE and f(ldy=255) == SHAPE
     assert f(x=A + 8) == ALIGN and f(ldx=260) == ALIGN and f(ids=A + 2) == ALIGN and f(w=A + 1) == ALIGN
