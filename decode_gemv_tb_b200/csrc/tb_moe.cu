@@ -19,8 +19,8 @@
 // share the decode.  A lane of a quad owns 32 consecutive k of every
 // 128-group in both operands, so a row's group is one 8-, 12- or 16-byte read
 // per lane, free of bank conflicts, and no code moves between lanes.  Weights
-// stream through a private ring per warp, filled by tensor copies of 16 or 32
-// rows x 128 (144) bytes.  (With cp.async, 32 rows' scattered 16- and 4-byte
+// stream through a private ring per warp, filled by tensor copies of 16 rows
+// x 128 (144) bytes.  (With cp.async, 32 rows' scattered 16- and 4-byte
 // pieces per group, both kernels were bound by the L1's request rate: more
 // warps changed nothing, 64 tokens x 4-bit experts took 466 us.)
 //
@@ -28,7 +28,7 @@
 // MMA's operand, and half the activations a second part would cost.
 //
 // k_moe_up: a unit is (block, 16 rows of gate and of up); S warps of a CTA
-// split K when units are few.  k_moe_down: a cluster of C CTAs holds 64 rows
+// split K where that evens out the warps' shares.  k_moe_down: a cluster of C CTAs holds 64 rows
 // of H, its CTAs split the blocks; each warp adds its rows' results per
 // token in shared memory, the ranks are added in order (deterministic).
 #include "tb_async.cuh"
@@ -62,7 +62,7 @@ struct MoeArgs {
     int64_t ldx, ldy;
     long long wait_cycles;
     int32_t T, k, E, H, I, ydt, stall;
-    int32_t S, C, zrows;
+    int32_t C, zrows;
     int32_t hperm;  // h in the order of the 4-bit decode's pairs
 };
 
@@ -83,43 +83,12 @@ __host__ __device__ constexpr int stage_groups(int kind) { return kind == 0 ? 4 
 __host__ __device__ constexpr int row_stride(int kind) { return kind == 1 ? 144 : 128; }
 // a unit's bf16 scales are copied whole up to this many groups; longer rows read them one by one
 constexpr int kMaxScaleGroups = 64;
+// the row of a 16-row tile that a lane holds first (the second is eight on): lane / 4, its three bits reversed
+__device__ __forceinline__ int tile_row(int lane) { return (lane >> 2 & 1) << 2 | (lane >> 2 & 2) | lane >> 4; }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 ldg_plain(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -159,9 +128,8 @@ __device__ __forceinline__ void pair_up(uint32_t (&x)[16], const uint32_t (&v)[1
 }
 
 template <int NS, bool BIG>
-__device__ __forceinline__ void mx4_product(uint32_t row, uint32_t ba, uint32_t bb,
+__device__ __forceinline__ void mx4_product(const uint4& a, const uint4& b, uint32_t ba, uint32_t bb,
                                             const uint32_t (&x)[NS][16], float (&acc)[NS][4]) {
-    const uint4 a = lds128(row), b = lds128(row + 8 * row_stride(2));
     const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
     // 2^(byte - 1) as a pair; above 2^127 in two factors; 255 is no number
     const uint32_t fa = ((BIG ? min(ba, 128u) : ba) + 126u) * 0x00800080u;
@@ -191,15 +159,18 @@ __device__ __forceinline__ void mx4_product(uint32_t row, uint32_t ba, uint32_t 
     }
 }
 
-// One 128-group of 16 rows times NS sets of eight columns: acc += s W x.  `row`: shared address of the lane's codes in
-// the first of its two rows (the second is eight rows on); s0, s1: the rows' scales, or the lane's two scale bytes.
+// One 128-group of 16 rows times NS sets of eight columns: acc += s W x.  `row`: the lane's codes in the first of its
+// two rows (the second is eight rows on); s0, s1: the rows' scales as bf16 bits, or the lane's two scale bytes.
 template <int KIND, int NS>
-__device__ __forceinline__ void group_product(uint32_t row, uint32_t s0b, uint32_t s1b, const uint32_t (&x)[NS][16],
+__device__ __forceinline__ void group_product(const uint8_t* row, uint32_t s0, uint32_t s1, const uint32_t (&x)[NS][16],
                                               float (&acc)[NS][4]) {
+    const uint8_t* row8 = row + 8 * row_stride(KIND);
     if constexpr (KIND == 2) {
-        const uint32_t ba = s0b, bb = s1b;
-        if (__builtin_expect(__any_sync(0xffffffffu, max(ba, bb) > 128u), 0)) mx4_product<NS, true>(row, ba, bb, x, acc);
-        else mx4_product<NS, false>(row, ba, bb, x, acc);
+        const uint4 a = *reinterpret_cast<const uint4*>(row), b = *reinterpret_cast<const uint4*>(row8);
+        if (__builtin_expect(__any_sync(0xffffffffu, max(s0, s1) > 128u), 0))
+            mx4_product<NS, true>(a, b, s0, s1, x, acc);
+        else
+            mx4_product<NS, false>(a, b, s0, s1, x, acc);
     } else {
         float d[NS][4];
 #pragma unroll
@@ -207,7 +178,7 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t s0b, uint32
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[n][i] = 0.f;
         if constexpr (KIND == 0) {
-            const uint2 a = lds64(row), b = lds64(row + 8 * row_stride(0));
+            const uint2 a = *reinterpret_cast<const uint2*>(row), b = *reinterpret_cast<const uint2*>(row8);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t ra[8], rb[8];
@@ -221,145 +192,158 @@ __device__ __forceinline__ void group_product(uint32_t row, uint32_t s0b, uint32
             }
         } else {
             uint32_t ra[16], rb[16];
-            const uint32_t br = row + 8 * row_stride(1);
-            decode3_signed(lds32(row), lds32(row + 4), lds32(row + 8), ra);
-            decode3_signed(lds32(br), lds32(br + 4), lds32(br + 8), rb);
+            const uint32_t* a = reinterpret_cast<const uint32_t*>(row);
+            const uint32_t* b = reinterpret_cast<const uint32_t*>(row8);
+            decode3_signed(a[0], a[1], a[2], ra);
+            decode3_signed(b[0], b[1], b[2], rb);
 #pragma unroll
             for (int j = 0; j < 16; j += 2)
 #pragma unroll
                 for (int n = 0; n < NS; ++n)
                     mma_bf16(d[n], ra[j], rb[j], ra[j + 1], rb[j + 1], x[n][j], x[n][j + 1]);
         }
-        const float s0 = __uint_as_float(s0b << 16), s1 = __uint_as_float(s1b << 16);
+        const float f0 = __uint_as_float(s0 << 16), f1 = __uint_as_float(s1 << 16);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            acc[n][0] = fmaf(s0, d[n][0], acc[n][0]);
-            acc[n][1] = fmaf(s0, d[n][1], acc[n][1]);
-            acc[n][2] = fmaf(s1, d[n][2], acc[n][2]);
-            acc[n][3] = fmaf(s1, d[n][3], acc[n][3]);
+            acc[n][0] = fmaf(f0, d[n][0], acc[n][0]);
+            acc[n][1] = fmaf(f0, d[n][1], acc[n][1]);
+            acc[n][2] = fmaf(f1, d[n][2], acc[n][2]);
+            acc[n][3] = fmaf(f1, d[n][3], acc[n][3]);
         }
     }
 }
 
-// ---- a warp's stream of a matrix -------------------------------------------------------
-// Units of ROWS consecutive rows and a range of their groups, one after the other, through kStages stages of kGroups
-// groups.  The warp refills a stage as soon as it has read it.
-template <int KIND, int ROWS>
+// ---- a warp's stream of weights -----------------------------------------------------------
+// Units (TILES tiles of 16 rows, of one matrix or of two of the same format, and a range of groups), one after the
+// other, through kStages stages of kGroups groups.  The warp requests a stage anew as soon as it has read it.
+template <int KIND, int TILES>
 struct Stream {
     static constexpr int kGroups = stage_groups(KIND);
-    static constexpr int kCodes = ROWS * row_stride(KIND);       // of a stage
-    static constexpr int kTiles = KIND == 2 ? ROWS * 16 * kGroups : 0;  // a 4-bit stage's scale rows
-    static constexpr int kBars = 8 * 2 * kStages;                // per stage; per scale buffer of a unit
-    // bytes of a warp's ring (codes first: swizzled stages begin at multiples of 1 KB)
-    static constexpr int kRing = (kStages * kCodes + 1023) & ~1023;
+    static constexpr int kCodes = 16 * row_stride(KIND);                  // of a tile in a stage
+    static constexpr int kScales = KIND == 2 ? 256 * kGroups : 0;         // 4-bit: its scale rows
+    static constexpr int kStageCodes = (TILES * kCodes + 1023) & ~1023;   // (swizzled tiles begin at multiples of 1 KB)
+    static constexpr int kBars = 8 * 2 * kStages;                         // a stage's, a scale buffer's
+    static constexpr int kRing = kStages * kStageCodes;
+    // scales beside the ring: per stage, or per unit (two in turn) the bf16 scales of its rows
     __host__ __device__ static constexpr int side(int G) {
-        return (kStages * kTiles + (KIND != 2 && G <= kMaxScaleGroups ? kStages * ROWS * 2 * G : 0) + 127) & ~127;
+        return (kStages * TILES * (KIND == 2 ? kScales : (G <= kMaxScaleGroups ? 32 * G : 0)) + 127) & ~127;
     }
 
-    const MoeMat& m;
-    uint32_t codes, sides, bars;
+    const MoeMat& m0;
+    const MoeMat& m1;
+    uint8_t *ring, *scl;
+    uint32_t bars;
     long long limit;
-    int lane, row, t;  // row: the lane's first row in a 16-row tile
-    // requests: the unit's first row, its next group and their end, how many stages and units have been begun
-    int64_t prow;
-    int pg, pend, pn, pu;
-    // reading: stage, its parity, the group in it and how many it holds; the unit's row, number and group
-    int stage, gi, left, cu, g;
-    uint32_t parity;
-    int64_t crow;
-    bool dead;
+    int off1;  // rows from tile 0 to tile 1: 0 (two matrices), or 16 from a row0 that is a multiple of 32
+    bool stall, dead;
+    uint32_t pn, pu, cn, cu;  // stages and units requested, read
+    int64_t prow;             // the open unit's first row, its next group and their end
+    int pg, pend;
 
-    __device__ __forceinline__ Stream(const MoeMat& m_, uint32_t ring, uint32_t side_, uint32_t bars_, long long limit_)
-        : m(m_), codes(ring), sides(side_), bars(bars_), limit(limit_), pn(0), pu(0), stage(0), left(0), cu(0),
-          parity(0), dead(false) {
-        lane = threadIdx.x & 31;
-        row = (lane >> 2 & 1) << 2 | (lane >> 2 & 2) | (lane >> 4);  // lane / 4 with its three bits reversed
-        t = lane & 3;
-    }
-    __device__ __forceinline__ void init_bars() const {
-        if (lane == 0)
+    __device__ __forceinline__ Stream(const MoeMat& a, const MoeMat& b, int off, uint8_t* ring_, uint8_t* scl_,
+                                      uint32_t bars_, const MoeArgs& A)
+        : m0(a), m1(b), ring(ring_), scl(scl_), bars(bars_), limit(A.wait_cycles), off1(off), stall(A.stall != 0),
+          dead(false), pn(0), pu(0), cn(0), cu(0), prow(0), pg(0), pend(0) {
+        if (bars != 0 && (threadIdx.x & 31) == 0)  // (0: a stream that is never used)
 #pragma unroll
             for (int i = 0; i < 2 * kStages; ++i) mb_init(bars + 8 * i, 1);
     }
-    __device__ __forceinline__ bool wide() const { return KIND != 2 && m.G > kMaxScaleGroups; }
+    __device__ __forceinline__ bool wide() const { return KIND != 2 && m0.G > kMaxScaleGroups; }
+    __device__ __forceinline__ bool open() const { return pg < pend; }
 
     // begins the requests of a unit
-    __device__ __forceinline__ void open(int64_t row0, int g0, int g1, bool stall) {
+    __device__ __forceinline__ void start(int64_t row0, int g0, int g1) {
         prow = row0, pg = g0, pend = g1;
-        if (KIND != 2 && !wide() && lane == 0 && !stall) {
-            const uint32_t bar = bars + 8 * (kStages + (pu % kStages)), n = (uint32_t)(ROWS * 2 * m.G);
-            mb_arrive_expect(bar, n);
-            bulk_load(sides + (pu % kStages) * n, m.scales + row0 * m.G, n, bar);
+        if (KIND != 2 && !wide() && (threadIdx.x & 31) == 0 && !stall) {
+            const uint32_t bar = bars + 8 * (kStages + pu % kStages), n = 32u * (uint32_t)m0.G;
+            const uint32_t dst = sm_addr(scl) + (pu % kStages) * TILES * n;
+            mb_arrive_expect(bar, TILES * n);
+            bulk_load(dst, m0.scales + row0 * m0.G, n, bar);
+            if (TILES == 2) bulk_load(dst + n, m1.scales + (row0 + off1) * m0.G, n, bar);
         }
         ++pu;
     }
-    // requests the next stage of the open unit; false when that was its last
-    __device__ __forceinline__ bool request(bool stall) {
-        const int s = pn % kStages;
-        if (lane == 0 && !stall) {
-            const uint32_t bar = bars + 8 * s;
-            mb_arrive_expect(bar, (uint32_t)(kCodes + kTiles));
-            tma_load_2d(codes + s * kCodes, &m.codes, pg * group_bytes(KIND), (int)prow, bar);
-            if constexpr (KIND == 2)
-                tma_load_2d(sides + s * kTiles, &m.tiles, (int)(prow & 31) * 16, (int)((prow >> 7) * m.G + pg), bar);
+    // requests the next stage of the open unit
+    __device__ __forceinline__ void request() {
+        if ((threadIdx.x & 31) == 0 && !stall) {
+            const uint32_t s = pn % kStages, bar = bars + 8 * s, dst = sm_addr(ring) + s * kStageCodes;
+            mb_arrive_expect(bar, TILES * (kCodes + kScales));
+            tma_load_2d(dst, &m0.codes, pg * group_bytes(KIND), (int)prow, bar);
+            if (TILES == 2) tma_load_2d(dst + kCodes, &m1.codes, pg * group_bytes(KIND), (int)prow + off1, bar);
+            if constexpr (KIND == 2) {
+                const uint32_t sd = sm_addr(scl) + s * TILES * kScales;
+                tma_load_2d(sd, &m0.tiles, (int)(prow & 31) * 16, (int)((prow >> 7) * m0.G + pg), bar);
+                if (TILES == 2) {
+                    const int64_t r1 = prow + off1;
+                    tma_load_2d(sd + kScales, &m1.tiles, (int)(r1 & 31) * 16, (int)((r1 >> 7) * m0.G + pg), bar);
+                }
+            }
         }
         ++pn;
         pg += kGroups;
-        return pg < pend;
     }
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t par) {
-        if (!dead) dead = !__all_sync(0xffffffffu, mb_wait_alone(bar, par, limit, &g_moe_timeouts));
-        return !dead;
+    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+        if (!dead) dead = !__all_sync(0xffffffffu, mb_wait_alone(bar, parity, limit, &g_moe_timeouts));
     }
-    // begins reading a unit at its group g0
-    __device__ __forceinline__ void begin(int64_t row0, int g0) {
-        crow = row0, g = g0, left = 0;
-        if (KIND != 2 && !wide()) wait(bars + 8 * (kStages + (cu % kStages)), (uint32_t)(cu / kStages) & 1u);
-        ++cu;
-    }
-    // the stage of group g, of which the unit has `more` with the later ones, is there
-    __device__ __forceinline__ void arrive(int more) {
-        if (left > 0) return;
-        wait(bars + 8 * stage, parity);
-        gi = 0;
-        left = min(kGroups, more);
-    }
-    // shared address of the lane's codes of the current group in 16-row tile w
-    __device__ __forceinline__ uint32_t at(int w) const {
-        const uint32_t base = codes + stage * kCodes + (w * 16 + row) * row_stride(KIND);
-        if constexpr (KIND == 0) return base + (((uint32_t)(2 * gi + (t >> 1)) ^ (uint32_t)row) << 4) + (t & 1) * 8;
-        if constexpr (KIND == 1) return base + gi * 48 + t * 12;
-        return base + (((uint32_t)(4 * gi + t) ^ (uint32_t)row) << 4);
-    }
-    // scale of row `row` + r of the unit at the current group: its bf16 bits, or the lane's byte
-    __device__ __forceinline__ uint32_t scale(int r) const {
-        if constexpr (KIND == 2) {
-            return lds8(sides + stage * kTiles + (gi * ROWS + row + r) * 16 + (int)(crow >> 5 & 3) * 4 + t);
-        } else {
-            if (wide()) return ld_stream_u16(m.scales + (crow + row + r) * m.G + g);
-            return lds16(sides + ((cu - 1) % kStages) * (ROWS * 2 * m.G) + ((row + r) * m.G + g) * 2);
-        }
-    }
-    // the current group has been read; true when its stage has, which then can be requested anew
-    __device__ __forceinline__ bool next() {
-        ++g, ++gi;
-        if (gi < left) return false;
-        left = 0;
-        if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1u;
-        }
-        __syncwarp();
-        return true;
-    }
-    // what a wait that gave up left in flight ends, or its own wait does, before the exit
-    __device__ __forceinline__ void drain(bool stall) const {
-        if (!dead || lane != 0 || stall) return;
-        for (int i = pn > kStages ? pn - kStages : 0; i < pn; ++i)
-            mb_drain(bars + 8 * (i % kStages), (uint32_t)(i / kStages) & 1u, limit);
+    // what is in flight ends, or its own wait does, before the exit
+    __device__ __forceinline__ void drain() const {
+        if (!dead || (threadIdx.x & 31) != 0 || stall) return;
+        for (uint32_t i = pn > kStages ? pn - kStages : 0; i < pn; ++i)
+            mb_drain(bars + 8 * (i % kStages), i / kStages & 1u, limit);
         if (KIND != 2 && !wide())
-            for (int i = pu > kStages ? pu - kStages : 0; i < pu; ++i)
-                mb_drain(bars + 8 * (kStages + i % kStages), (uint32_t)(i / kStages) & 1u, limit);
+            for (uint32_t i = pu > kStages ? pu - kStages : 0; i < pu; ++i)
+                mb_drain(bars + 8 * (kStages + i % kStages), i / kStages & 1u, limit);
+    }
+
+    // acc += the unit's rows times the columns that load_x(g, x) gives, groups g0 .. g1 - 1; feed() requests the next
+    // stage of this stream
+    template <int NS, class LoadX, class Feed>
+    __device__ __forceinline__ void multiply(int64_t row0, int g0, int g1, LoadX load_x, Feed feed,
+                                             float (&acc)[TILES][NS][4]) {
+        const int lane = threadIdx.x & 31, t = lane & 3, row = tile_row(lane), G = m0.G;
+        // the lane's codes of a stage's first group, and what the swizzle makes of the others'
+        const uint32_t first = KIND == 1 ? row * 144 + t * 12
+                                         : row * 128 + (KIND == 0 ? (((t >> 1) ^ row) << 4) + (t & 1) * 8 : (t ^ row) << 4);
+        const uint8_t* su = nullptr;  // the unit's scales
+        if constexpr (KIND == 2) {
+            su = scl + row * 16 + (int)(row0 >> 5 & 3) * 4 + t;
+        } else if (!wide()) {
+            wait(bars + 8 * (kStages + cu % kStages), cu / kStages & 1u);
+            su = scl + (cu % kStages) * TILES * 32 * G + row * 2 * G;
+        }
+        ++cu;
+#pragma unroll 1
+        for (int g = g0; g < g1; g += kGroups) {
+            const uint32_t s = cn % kStages;
+            const uint8_t* codes = ring + s * kStageCodes;
+            wait(bars + 8 * s, cn / kStages & 1u);
+            ++cn;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                if (i > 0 && g + i >= g1) break;
+                uint32_t x[NS][16];
+                load_x(g + i, x);
+#pragma unroll
+                for (int w = 0; w < TILES; ++w) {
+                    uint32_t s0, s1;
+                    if constexpr (KIND == 2) {
+                        const uint8_t* p = su + (s * TILES + w) * kScales + i * 256;
+                        s0 = p[0], s1 = p[128];
+                    } else if (wide()) {
+                        const uint16_t* p = (w ? m1 : m0).scales + (row0 + w * off1 + row) * G + g + i;
+                        s0 = __ldg(p), s1 = __ldg(p + 8 * G);
+                    } else {
+                        const uint8_t* p = su + w * 32 * G + 2 * (g + i);
+                        s0 = *reinterpret_cast<const uint16_t*>(p);
+                        s1 = *reinterpret_cast<const uint16_t*>(p + 16 * G);
+                    }
+                    const uint32_t at = KIND == 1 ? first + i * 48 : first ^ (uint32_t)(i * group_bytes(KIND));
+                    group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, x, acc[w]);
+                }
+            }
+            __syncwarp();
+            if (!dead) feed();
+        }
     }
 };
 
@@ -434,16 +418,17 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
 }
 
 // ---- gate and up -----------------------------------------------------------------------
+// Of one format, gate's and up's tiles share the stages and the activations' fragments; else each has a stream.
 template <int KG, int KU, int NS>
 struct MoeUp {
-    using Gate = Stream<KG, 16>;
-    using Up = Stream<KU, 16>;
-    static constexpr int kWarpRing = Gate::kRing + Up::kRing;
-    static constexpr int kBars = Gate::kBars + Up::kBars;
-    __host__ __device__ static int smem(int G, int S) {
-        return kMoeWarps * (kWarpRing + Gate::side(G) + Up::side(G) + kBars) +
-               (S > 1 ? 2 * kMoeWarps * NS * 1024 : 0) + 1024;
-    }
+    static constexpr bool kBoth = KG == KU;
+    using Gate = Stream<KG, kBoth ? 2 : 1>;
+    using Up = Stream<KU, 1>;
+    static constexpr int kWarpRing = Gate::kRing + (kBoth ? 0 : Up::kRing);
+    static constexpr int kBars = Gate::kBars + (kBoth ? 0 : Up::kBars);
+    static constexpr int kPart = 2 * kMoeWarps * NS * 1024;  // partial sums of split units, two units deep
+    __host__ __device__ static constexpr int side(int G) { return Gate::side(G) + (kBoth ? 0 : Up::side(G)); }
+    __host__ __device__ static int smem(int G) { return kMoeWarps * (kWarpRing + side(G) + kBars) + kPart + 1024; }
 };
 
 template <int KG, int KU, int NS>
@@ -451,47 +436,66 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
     using M = MoeUp<KG, KU, NS>;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
-    const int G = A.gate.G, S = A.S, per = kMoeWarps / S, s = warp & (S - 1), ui = warp / S;
-    // rings of all warps, then their scales, then partial sums [2][warps][NS][256] (two units deep), then barriers
-    const uint32_t base = (sm_addr(raw) + 1023u) & ~1023u;
-    const uint32_t ring = base + warp * M::kWarpRing;
-    const uint32_t sides = base + kMoeWarps * M::kWarpRing + warp * (M::Gate::side(G) + M::Up::side(G));
-    const uint32_t part_s = base + kMoeWarps * (M::kWarpRing + M::Gate::side(G) + M::Up::side(G));
-    float* part = reinterpret_cast<float*>(raw + (part_s - sm_addr(raw)));
-    const uint32_t bars = part_s + (S > 1 ? 2 * kMoeWarps * NS * 1024 : 0) + warp * M::kBars;
-    typename M::Gate gate(A.gate, ring, sides, bars, A.wait_cycles);
-    typename M::Up up(A.up, ring + M::Gate::kRing, sides + M::Gate::side(G), bars + M::Gate::kBars, A.wait_cycles);
-    gate.init_bars();
-    up.init_bars();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, G = A.gate.G;
+    // rings of all warps, partial sums, the warps' scales, barriers
+    uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
+    uint8_t* const ring = base + warp * M::kWarpRing;
+    float* const part = reinterpret_cast<float*>(base + kMoeWarps * M::kWarpRing);
+    uint8_t* const side = base + kMoeWarps * M::kWarpRing + M::kPart + warp * M::side(G);
+    const uint32_t bars = sm_addr(base + kMoeWarps * (M::kWarpRing + M::side(G)) + M::kPart) + warp * M::kBars;
+    typename M::Gate gate(A.gate, M::kBoth ? A.up : A.gate, 0, ring, side, bars, A);
+    typename M::Up up(A.up, A.up, 0, ring + M::Gate::kRing, side + M::Gate::side(G),
+                      M::kBoth ? 0u : bars + M::Gate::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
     build_list<kMoeThreads, 8 * NS>(L, A);
     pdl_trigger();
 
-    const int g0 = G * s / S, g1 = G * (s + 1) / S;
-    const int tiles = A.I / 16, units = L.blocks * tiles, ustep = (int)gridDim.x * per;
-    const bool stall = A.stall != 0;
+    // warps that share a unit, each a part of K: the number whose rounds over all units end first (in groups; a unit
+    // costs about one more to begin and end, two more where its parts are added)
+    const int tiles = A.I / 16, units = L.blocks * tiles;
+    int lg = 0, least = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        if (1 << i > G) break;
+        const int slots = (int)gridDim.x * kMoeWarps >> i, rounds = (units + slots - 1) / slots;
+        const int cost = rounds * ((G + (1 << i) - 1 >> i) + (i ? 3 : 1));
+        if (cost < least) {
+            least = cost;
+            lg = i;
+        }
+    }
+    const int S = 1 << lg, per = kMoeWarps >> lg, s = warp & (S - 1), ui = warp >> lg;
+    const int g0 = G * s >> lg, g1 = G * (s + 1) >> lg;
+    const int ustep = (int)gridDim.x * per, u0 = (int)blockIdx.x * per + ui;
     auto row_of = [&](int u) {
         const int blk = u / tiles;
         return (int64_t)blk_expert(L.blk[blk]) * A.I + (u - blk * tiles) * 16;
     };
-    // each stream's next unit to request
-    int gu = (int)blockIdx.x * per + ui, uu = gu;
-    auto feed = [&](auto& m, int& u, bool& open) {
-        if (u >= units || m.dead) return;
-        if (!open) m.open(row_of(u), g0, g1, stall);
-        open = m.request(stall);
-        if (!open) u += ustep;
+    int gu = u0, uu = u0;  // the units that the streams have begun to request, plus a step
+    auto feed_gate = [&]() {
+        if (!gate.open()) {
+            if (gu >= units) return;
+            gate.start(row_of(gu), g0, g1);
+            gu += ustep;
+        }
+        gate.request();
     };
-    bool gopen = false, uopen = false;
+    auto feed_up = [&]() {
+        if (!up.open()) {
+            if (uu >= units) return;
+            up.start(row_of(uu), g0, g1);
+            uu += ustep;
+        }
+        up.request();
+    };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-        feed(gate, gu, gopen);
-        feed(up, uu, uopen);
+        feed_gate();
+        if (!M::kBoth) feed_up();
     }
     int flip = 0;
-    for (int u = (int)blockIdx.x * per + ui; u < units; u += ustep) {
+    for (int u = u0; u < units; u += ustep) {
         const int blk = u / tiles, tile = u - blk * tiles;
         const uint32_t block = L.blk[blk];
         const int count = blk_count(block), slot0 = blk_slot(block);
@@ -503,47 +507,50 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
             have[n] = 8 * n + r < count;
             xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + 32 * t;
         }
-        float ag[NS][4], au[NS][4];
-        uint32_t v[NS][16];
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = 0.f;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) v[n][q] = 0u;
-        }
-        gate.begin(row0, g0);
-        up.begin(row0, g0);
-#pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
+        auto load_plain = [&](int g, uint32_t (&x)[NS][16]) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                if (have[n]) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 w = ld_act_u4(xr[n] + g * 128 + 8 * q);
-                        v[n][4 * q] = w.x, v[n][4 * q + 1] = w.y, v[n][4 * q + 2] = w.z, v[n][4 * q + 3] = w.w;
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (have[n]) w = __ldg(reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q));
+                    x[n][4 * q] = w.x, x[n][4 * q + 1] = w.y, x[n][4 * q + 2] = w.z, x[n][4 * q + 3] = w.w;
                 }
-            // the activations in the order of the 4-bit decoder's pairs, where one is to read them
-            uint32_t p[NS][16];
-            if constexpr (KG == 2 || KU == 2) {
+        };
+        auto load_paired = [&](int g, uint32_t (&x)[NS][16]) {
+            uint32_t v[NS][16];
+            load_plain(g, v);
 #pragma unroll
-                for (int n = 0; n < NS; ++n) pair_up(p[n], v[n]);
-            }
-            gate.arrive(g1 - g);
-            group_product<KG, NS>(gate.at(0), gate.scale(0), gate.scale(8), KG == 2 ? p : v, ag);
-            if (gate.next()) feed(gate, gu, gopen);
-            up.arrive(g1 - g);
-            group_product<KU, NS>(up.at(0), up.scale(0), up.scale(8), KU == 2 ? p : v, au);
-            if (up.next()) feed(up, uu, uopen);
-        }
-        const bool dead = gate.dead || up.dead;
-        if (dead) {
+            for (int n = 0; n < NS; ++n) pair_up(x[n], v[n]);
+        };
+        float acc[2][NS][4];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+        if constexpr (M::kBoth) {
+            if constexpr (KG == 2) gate.template multiply<NS>(row0, g0, g1, load_paired, feed_gate, acc);
+            else gate.template multiply<NS>(row0, g0, g1, load_plain, feed_gate, acc);
+        } else {
+            float one[1][NS][4], two[1][NS][4];
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ag[n][i] = au[n][i] = kMoeNaN;
+                for (int i = 0; i < 4; ++i) one[0][n][i] = two[0][n][i] = 0.f;
+            if constexpr (KG == 2) gate.template multiply<NS>(row0, g0, g1, load_paired, feed_gate, one);
+            else gate.template multiply<NS>(row0, g0, g1, load_plain, feed_gate, one);
+            if constexpr (KU == 2) up.template multiply<NS>(row0, g0, g1, load_paired, feed_up, two);
+            else up.template multiply<NS>(row0, g0, g1, load_plain, feed_up, two);
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][n][i] = one[0][n][i], acc[1][n][i] = two[0][n][i];
+        }
+        if (gate.dead || up.dead) {
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = kMoeNaN;
         }
         if (S > 1) {
             float* mine = part + ((flip * kMoeWarps + warp) * NS) * 256 + lane;
@@ -551,8 +558,8 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mine[n * 256 + i * 32] = ag[n][i];
-                    mine[n * 256 + 128 + i * 32] = au[n][i];
+                    mine[n * 256 + i * 32] = acc[0][n][i];
+                    mine[n * 256 + 128 + i * 32] = acc[1][n][i];
                 }
             // (constant barrier numbers: with a variable one a CTA holds all sixteen, and four CTAs fill the SM)
             if (ui == 0) asm volatile("bar.sync 1, %0;" ::"r"(S * 32) : "memory");
@@ -569,8 +576,8 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
                         sg += q[0];
                         su += q[128];
                     }
-                    ag[n][i] = sg;
-                    au[n][i] = su;
+                    acc[0][n][i] = sg;
+                    acc[1][n][i] = su;
                 }
             flip ^= 1;
         }
@@ -580,62 +587,67 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
             for (int i = 0; i < 4; ++i) {
                 const int col = 8 * n + 2 * t + (i & 1);
                 if ((i & (S - 1)) != s || col >= count) continue;
-                const float gv = ag[n][i], h = gv / (1.f + expf(-gv)) * au[n][i];
+                const float gv = acc[0][n][i], h = gv / (1.f + expf(-gv)) * acc[1][n][i];
                 // h in the order in which the down kernel's lanes read a 128-group: 16-byte pieces (q, t)
-                int c = (tile & 7) * 16 + gate.row + 8 * (i >> 1);
+                int c = (tile & 7) * 16 + tile_row(lane) + 8 * (i >> 1);
                 if (A.hperm) c = (c & ~7) | (c & 3) << 1 | (c >> 2 & 1);
                 c = ((c >> 3 & 3) << 2 | c >> 5) << 3 | (c & 7);
                 A.h[(int64_t)(slot0 + col) * A.I + (tile >> 3) * 128 + c] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
             }
     }
-    gate.drain(stall);
-    up.drain(stall);
+    gate.drain();
+    if (!M::kBoth) up.drain();
 }
 
 // ---- down and the weighted sum ------------------------------------------------------------
 constexpr int kDownRows = 32;  // of a CTA: each warp holds all of them, two tiles that share h's fragments
 
-// slices of a block's groups: enough tasks for the warps that share a tile, as far as z holds them
+// Slices of a block's groups, as far as z holds them: the number whose rounds over the tile's warps end first (in groups;
+// a task costs about two more to begin and end).
 __device__ __forceinline__ int down_slices(int G, int warps, int blocks, int slots, int zrows) {
-    if (blocks == 0) return 1;
-    return max(1, min(min(G, (3 * warps + blocks - 1) / blocks), zrows / slots));
+    int best = 1, least = 0x7FFFFFFF;
+    for (int k = 1; k <= G && k <= 8 && k * slots <= zrows; ++k) {
+        const int cost = (blocks * k + warps - 1) / warps * ((G + k - 1) / k + 2);
+        if (cost < least) {
+            least = cost;
+            best = k;
+        }
+    }
+    return best;
 }
 
 template <int KIND>
 struct MoeDown {
-    using W = Stream<KIND, kDownRows>;
+    using W = Stream<KIND, 2>;
     __host__ __device__ static int smem(int G) { return kMoeWarps * (W::kRing + W::side(G) + W::kBars) + 1024; }
 };
 
 template <int KIND, int NS>
 __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
-    using M = MoeDown<KIND>;
+    using W = typename MoeDown<KIND>::W;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
     __shared__ float slot_w[kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, C = A.C, G = A.down.G;
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
-    const uint32_t base = (sm_addr(raw) + 1023u) & ~1023u;
-    typename M::W w(A.down, base + warp * M::W::kRing, base + kMoeWarps * M::W::kRing + warp * M::W::side(G),
-                    base + kMoeWarps * (M::W::kRing + M::W::side(G)) + warp * M::W::kBars, A.wait_cycles);
-    w.init_bars();
+    uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
+    W w(A.down, A.down, 16, base + warp * W::kRing, base + kMoeWarps * W::kRing + warp * W::side(G),
+        sm_addr(base + kMoeWarps * (W::kRing + W::side(G))) + warp * W::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     // the kernel before waited for its inputs: ids and weights are final, only h is not
     build_list<kMoeThreads, 8 * NS>(L, A);
     float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
-    // blocks fewer than the warps that share them: their groups are split too
     const int step = C * kMoeWarps, KS = down_slices(G, step, L.blocks, L.slots, A.zrows), tasks = L.blocks * KS;
-    const bool stall = A.stall != 0;
-    int pq = rank * kMoeWarps + warp;  // the next task to request
-    bool open = false;
+    const int q0 = rank * kMoeWarps + warp;
+    int pq = q0;  // the next task to request
     auto feed = [&]() {
-        if (pq >= tasks || w.dead) return;
-        if (!open) {
+        if (!w.open()) {
+            if (pq >= tasks) return;
             const int b = pq / KS, k = pq - b * KS;
-            w.open((int64_t)blk_expert(L.blk[b]) * A.H + (int64_t)tile * kDownRows, G * k / KS, G * (k + 1) / KS, stall);
+            w.start((int64_t)blk_expert(L.blk[b]) * A.H + (int64_t)tile * kDownRows, G * k / KS, G * (k + 1) / KS);
+            pq += step;
         }
-        open = w.request(stall);
-        if (!open) pq += step;
+        w.request();
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) feed();
@@ -651,7 +663,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_consta
     }
     __syncthreads();
     pdl_wait();
-    for (int q = rank * kMoeWarps + warp; q < tasks; q += step) {
+    for (int q = q0; q < tasks; q += step) {
         const int b = q / KS, k = q - b * KS, g0 = G * k / KS, g1 = G * (k + 1) / KS;
         const uint32_t block = L.blk[b];
         const int count = blk_count(block), slot0 = blk_slot(block);
@@ -662,32 +674,22 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_consta
             have[n] = 8 * n + r < count;
             hp[n] = A.h + (int64_t)(slot0 + (have[n] ? 8 * n + r : 0)) * A.I + 8 * t;
         }
-        float acc[2][NS][4];
-        uint32_t v[NS][16];
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[n][j] = 0u;
-        }
-        w.begin((int64_t)blk_expert(block) * A.H + (int64_t)tile * kDownRows, g0);
-#pragma unroll 1
-        for (int g = g0; g < g1; ++g) {
+        auto load_h = [&](int g, uint32_t (&x)[NS][16]) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
-                if (have[n]) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 u = ldg_plain(hp[n] + g * 128 + 32 * j);
-                        v[n][4 * j] = u.x, v[n][4 * j + 1] = u.y, v[n][4 * j + 2] = u.z, v[n][4 * j + 3] = u.w;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    if (have[n]) u = *reinterpret_cast<const uint4*>(hp[n] + g * 128 + 32 * j);
+                    x[n][4 * j] = u.x, x[n][4 * j + 1] = u.y, x[n][4 * j + 2] = u.z, x[n][4 * j + 3] = u.w;
                 }
-            w.arrive(g1 - g);
-            group_product<KIND, NS>(w.at(0), w.scale(0), w.scale(8), v, acc[0]);
-            group_product<KIND, NS>(w.at(1), w.scale(16), w.scale(24), v, acc[1]);
-            if (w.next()) feed();
-        }
+        };
+        float acc[2][NS][4];
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+        w.template multiply<NS>((int64_t)blk_expert(block) * A.H + (int64_t)tile * kDownRows, g0, g1, load_h, feed, acc);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -695,7 +697,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_consta
                 const int tok = 8 * n + 2 * t + j;
                 if (tok >= count) continue;
                 const int slot = slot0 + tok;
-                float* p = z + ((int64_t)slot * KS + k) * kDownRows + w.row;
+                float* p = z + ((int64_t)slot * KS + k) * kDownRows + tile_row(lane);
                 const float f = w.dead ? kMoeNaN : slot_w[slot];
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_consta
                 }
             }
     }
-    w.drain(stall);
+    w.drain();
     __syncwarp();
     if (C > 1) {  // the cluster's z is complete
         cluster_arrive();
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_consta
 
 struct UpKernel {
     const void* fn;
-    int (*smem)(int G, int S);
+    int (*smem)(int G);
 };
 template <int KG, int KU, int NS>
 UpKernel up_of() {
@@ -773,8 +775,7 @@ int moe_sms() {
     return sms[dev];
 }
 
-// `rows`: of a unit
-bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K, int rows) {
+bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K) {
     TensorMapEncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
     m->scales = static_cast<const uint16_t*>(w.scales);
@@ -784,7 +785,7 @@ bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K, int rows) {
     {
         const cuuint64_t rb = (cuuint64_t)m->G * group_bytes(m->kind);
         const cuuint64_t dims[2] = {rb, (cuuint64_t)N}, strides[1] = {rb};
-        const cuuint32_t box[2] = {(cuuint32_t)row_stride(m->kind), (cuuint32_t)rows};
+        const cuuint32_t box[2] = {(cuuint32_t)row_stride(m->kind), 16};
         if (enc(&m->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w.packed), dims, strides, box, one,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, m->kind == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -792,14 +793,7 @@ bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K, int rows) {
     }
     if (m->kind == 2) {
         const cuuint64_t dims[2] = {512, (cuuint64_t)((N + 127) / 128 * m->G)}, strides[1] = {512};
-        const cuuint32_t box[2] = {(cuuint32_t)(16 * rows), (cuuint32_t)stage_groups(2)};
-        if (rows * 16 > 256) {  // a box holds at most 256 elements of a dimension: as 32-bit words
-            const cuuint64_t d4[2] = {128, dims[1]};
-            const cuuint32_t b4[2] = {(cuuint32_t)(4 * rows), box[1]};
-            return enc(&m->tiles, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(w.scales), d4, strides, b4, one,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-        }
+        const cuuint32_t box[2] = {256, (cuuint32_t)stage_groups(2)};
         return enc(&m->tiles, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(w.scales), dims, strides, box, one,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -831,8 +825,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     if (sms <= 0) return cudaErrorInitializationError;
     MoeArgs A;
     std::memset(&A, 0, sizeof(A));
-    if (!make_mat(&A.gate, gate, E * I, H, 16) || !make_mat(&A.up, up, E * I, H, 16) ||
-        !make_mat(&A.down, down, E * H, I, kDownRows))
+    if (!make_mat(&A.gate, gate, E * I, H) || !make_mat(&A.up, up, E * I, H) || !make_mat(&A.down, down, E * H, I))
         return cudaErrorInvalidValue;
     A.wait_cycles = wait_cycles;
     A.stall = stall ? 1 : 0;
@@ -851,17 +844,13 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.H = (int32_t)H;
     A.I = (int32_t)I;
     A.ydt = ydt;
-    // units that the pairs can make at most; warps split K while they would leave the GPU's warps idle
-    const int64_t units = (int64_t)std::min(T * k, E + T * k / 8) * (I / 16);
-    A.S = 1;
-    while (A.S < kMoeWarps && units * A.S < (int64_t)sms * 16 && A.gate.G >= 2 * A.S) A.S *= 2;
     A.hperm = A.down.kind == 2 ? 1 : 0;
     // Sets of eight columns that share a decode: one while an expert's tokens seldom exceed eight, else two (a second
     // set costs about a tenth of a product, a second decode a whole one)
     const int NS = T * k > 5 * E ? 2 : 1;
     const UpKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
     const DownKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
-    const int up_smem = ku.smem(A.gate.G, A.S), down_smem = kd.smem(A.down.G);
+    const int up_smem = ku.smem(A.gate.G), down_smem = kd.smem(A.down.G);
     cudaError_t e = shape_kernel(ku.fn);
     if (e != cudaSuccess) return e;
     e = shape_kernel(kd.fn);
@@ -884,7 +873,8 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
             A.C = c;
         }
     }
-    const int64_t ctas = std::min<int64_t>((units * A.S + kMoeWarps - 1) / kMoeWarps, (int64_t)sms * per_sm);
+    // no more CTAs than the units that the pairs can make at most
+    const int64_t ctas = std::min<int64_t>((int64_t)std::min(T * k, E + T * k / 8) * (I / 16), (int64_t)sms * per_sm);
 
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
