@@ -68,7 +68,7 @@ struct MoeArgs {
 
 namespace {
 
-constexpr int kMoeWarps = 4;
+constexpr int kMoeWarps = 8;
 constexpr int kMoeThreads = kMoeWarps * 32;
 constexpr int kStages = 2;  // of a warp's ring
 constexpr float kMoeNaN = __builtin_nanf("");
@@ -316,13 +316,21 @@ struct Stream {
         for (int g = g0; g < g1; g += kGroups) {
             const uint32_t s = cn % kStages;
             const uint8_t* codes = ring + s * kStageCodes;
+            uint32_t ahead[NS][16];  // (of one set) the activations of the next group
+            if (NS == 1) load_x(g, ahead);
             wait(bars + 8 * s, cn / kStages & 1u);
             ++cn;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 if (i > 0 && g + i >= g1) break;
                 uint32_t x[NS][16];
-                load_x(g + i, x);
+                if (NS == 1) {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) x[0][q] = ahead[0][q];
+                    if (i + 1 < kGroups && g + i + 1 < g1) load_x(g + i + 1, ahead);
+                } else {
+                    load_x(g + i, x);
+                }
 #pragma unroll
                 for (int w = 0; w < TILES; ++w) {
                     uint32_t s0, s1;
@@ -426,13 +434,21 @@ struct MoeUp {
     using Up = Stream<KU, 1>;
     static constexpr int kWarpRing = Gate::kRing + (kBoth ? 0 : Up::kRing);
     static constexpr int kBars = Gate::kBars + (kBoth ? 0 : Up::kBars);
-    static constexpr int kPart = 2 * kMoeWarps * NS * 1024;  // partial sums of split units, two units deep
+    static constexpr int kPart = kMoeWarps * NS * 1024;  // partial sums of split units
     __host__ __device__ static constexpr int side(int G) { return Gate::side(G) + (kBoth ? 0 : Up::side(G)); }
     __host__ __device__ static int smem(int G) { return kMoeWarps * (kWarpRing + side(G) + kBars) + kPart + 1024; }
 };
 
+// the S warps of unit `ui` of a CTA (constant barrier numbers: with a variable one a CTA holds all sixteen of its SM's)
+__device__ __forceinline__ void unit_sync(int ui, int S) {
+    if (ui == 0) asm volatile("bar.sync 1, %0;" ::"r"(S * 32) : "memory");
+    else if (ui == 1) asm volatile("bar.sync 2, %0;" ::"r"(S * 32) : "memory");
+    else if (ui == 2) asm volatile("bar.sync 3, %0;" ::"r"(S * 32) : "memory");
+    else asm volatile("bar.sync 4, %0;" ::"r"(S * 32) : "memory");
+}
+
 template <int KG, int KU, int NS>
-__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant__ MoeArgs A) {
     using M = MoeUp<KG, KU, NS>;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
     const int tiles = A.I / 16, units = L.blocks * tiles;
     int lg = 0, least = 0x7FFFFFFF;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
         if (1 << i > G) break;
         const int slots = (int)gridDim.x * kMoeWarps >> i, rounds = (units + slots - 1) / slots;
         const int cost = rounds * ((G + (1 << i) - 1 >> i) + (i ? 3 : 1));
@@ -494,7 +510,6 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
         feed_gate();
         if (!M::kBoth) feed_up();
     }
-    int flip = 0;
     for (int u = u0; u < units; u += ustep) {
         const int blk = u / tiles, tile = u - blk * tiles;
         const uint32_t block = L.blk[blk];
@@ -553,7 +568,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
                 for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = kMoeNaN;
         }
         if (S > 1) {
-            float* mine = part + ((flip * kMoeWarps + warp) * NS) * 256 + lane;
+            float* mine = part + (warp * NS) * 256 + lane;
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -561,9 +576,7 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
                     mine[n * 256 + i * 32] = acc[0][n][i];
                     mine[n * 256 + 128 + i * 32] = acc[1][n][i];
                 }
-            // (constant barrier numbers: with a variable one a CTA holds all sixteen, and four CTAs fill the SM)
-            if (ui == 0) asm volatile("bar.sync 1, %0;" ::"r"(S * 32) : "memory");
-            else asm volatile("bar.sync 2, %0;" ::"r"(S * 32) : "memory");
+            unit_sync(ui, S);
             // warp s of the unit finishes registers s, s + S, ... of every set
 #pragma unroll
             for (int n = 0; n < NS; ++n)
@@ -572,14 +585,14 @@ __global__ void __launch_bounds__(kMoeThreads, 4) k_moe_up(const __grid_constant
                     if ((i & (S - 1)) != s) continue;
                     float sg = 0.f, su = 0.f;
                     for (int w = 0; w < S; ++w) {
-                        const float* q = part + ((flip * kMoeWarps + ui * S + w) * NS + n) * 256 + i * 32 + lane;
+                        const float* q = part + ((ui * S + w) * NS + n) * 256 + i * 32 + lane;
                         sg += q[0];
                         su += q[128];
                     }
                     acc[0][n][i] = sg;
                     acc[1][n][i] = su;
                 }
-            flip ^= 1;
+            unit_sync(ui, S);
         }
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -623,7 +636,7 @@ struct MoeDown {
 };
 
 template <int KIND, int NS>
-__global__ void __launch_bounds__(kMoeThreads, 4) k_moe_down(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_constant__ MoeArgs A) {
     using W = typename MoeDown<KIND>::W;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
