@@ -312,25 +312,27 @@ struct Stream {
             su = scl + (cu % kStages) * TILES * 32 * G + row * 2 * G;
         }
         ++cu;
+        constexpr int kBuf = NS == 1 ? 2 : 1;
+        uint32_t x[kBuf][NS][16];  // columns without a token stay 0: load_x leaves them alone
+#pragma unroll
+        for (int i = 0; i < kBuf; ++i)
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+                for (int q = 0; q < 16; ++q) x[i][n][q] = 0u;
 #pragma unroll 1
         for (int g = g0; g < g1; g += kGroups) {
             const uint32_t s = cn % kStages;
             const uint8_t* codes = ring + s * kStageCodes;
-            uint32_t ahead[NS][16];  // (of one set) the activations of the next group
-            if (NS == 1) load_x(g, ahead);
+            load_x(g, x[0]);
             wait(bars + 8 * s, cn / kStages & 1u);
             ++cn;
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 if (i > 0 && g + i >= g1) break;
-                uint32_t x[NS][16];
-                if (NS == 1) {
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) x[0][q] = ahead[0][q];
-                    if (i + 1 < kGroups && g + i + 1 < g1) load_x(g + i + 1, ahead);
-                } else {
-                    load_x(g + i, x);
-                }
+                // with one set the next group's activations are requested ahead of this one's products
+                if (NS == 1 && i + 1 < kGroups && g + i + 1 < g1) load_x(g + i + 1, x[(i + 1) % kBuf]);
+                if (NS > 1 && i > 0) load_x(g + i, x[0]);
 #pragma unroll
                 for (int w = 0; w < TILES; ++w) {
                     uint32_t s0, s1;
@@ -346,7 +348,7 @@ struct Stream {
                         s1 = *reinterpret_cast<const uint16_t*>(p + 16 * G);
                     }
                     const uint32_t at = KIND == 1 ? first + i * 48 : first ^ (uint32_t)(i * group_bytes(KIND));
-                    group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, x, acc[w]);
+                    group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, x[i % kBuf], acc[w]);
                 }
             }
             __syncwarp();
@@ -484,24 +486,34 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
     const int S = 1 << lg, per = kMoeWarps >> lg, s = warp & (S - 1), ui = warp >> lg;
     const int g0 = G * s >> lg, g1 = G * (s + 1) >> lg;
     const int ustep = (int)gridDim.x * per, u0 = (int)blockIdx.x * per + ui;
-    auto row_of = [&](int u) {
-        const int blk = u / tiles;
-        return (int64_t)blk_expert(L.blk[blk]) * A.I + (u - blk * tiles) * 16;
+    struct Unit {
+        int blk, tile;
     };
-    int gu = u0, uu = u0;  // the units that the streams have begun to request, plus a step
+    const int sblk = ustep / tiles, stile = ustep - sblk * tiles;
+    const Unit first{u0 / tiles, u0 % tiles};
+    auto advance = [&](Unit& v) {
+        v.blk += sblk;
+        v.tile += stile;
+        if (v.tile >= tiles) {
+            v.tile -= tiles;
+            ++v.blk;
+        }
+    };
+    auto row_of = [&](const Unit& v) { return (int64_t)blk_expert(L.blk[v.blk]) * A.I + v.tile * 16; };
+    Unit gu = first, uu = first;  // the next units that the streams request
     auto feed_gate = [&]() {
         if (!gate.open()) {
-            if (gu >= units) return;
+            if (gu.blk >= L.blocks) return;
             gate.start(row_of(gu), g0, g1);
-            gu += ustep;
+            advance(gu);
         }
         gate.request();
     };
     auto feed_up = [&]() {
         if (!up.open()) {
-            if (uu >= units) return;
+            if (uu.blk >= L.blocks) return;
             up.start(row_of(uu), g0, g1);
-            uu += ustep;
+            advance(uu);
         }
         up.request();
     };
@@ -510,11 +522,11 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
         feed_gate();
         if (!M::kBoth) feed_up();
     }
-    for (int u = u0; u < units; u += ustep) {
-        const int blk = u / tiles, tile = u - blk * tiles;
-        const uint32_t block = L.blk[blk];
+    for (Unit u = first; u.blk < L.blocks; advance(u)) {
+        const int tile = u.tile;
+        const uint32_t block = L.blk[u.blk];
         const int count = blk_count(block), slot0 = blk_slot(block);
-        const int64_t row0 = (int64_t)blk_expert(block) * A.I + tile * 16;
+        const int64_t row0 = row_of(u);
         const uint16_t* xr[NS];
         bool have[NS];
 #pragma unroll
@@ -522,22 +534,26 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
             have[n] = 8 * n + r < count;
             xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + 32 * t;
         }
-        auto load_plain = [&](int g, uint32_t (&x)[NS][16]) {
+        auto load = [&](int g, uint32_t (&x)[NS][16], bool paired) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
+                if (have[n]) {
+                    uint32_t v[16];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (have[n]) w = __ldg(reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q));
-                    x[n][4 * q] = w.x, x[n][4 * q + 1] = w.y, x[n][4 * q + 2] = w.z, x[n][4 * q + 3] = w.w;
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q));
+                        v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
+                    }
+                    if (paired) {
+                        pair_up(x[n], v);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) x[n][q] = v[q];
+                    }
                 }
         };
-        auto load_paired = [&](int g, uint32_t (&x)[NS][16]) {
-            uint32_t v[NS][16];
-            load_plain(g, v);
-#pragma unroll
-            for (int n = 0; n < NS; ++n) pair_up(x[n], v[n]);
-        };
+        auto load_plain = [&](int g, uint32_t (&x)[NS][16]) { load(g, x, false); };
+        auto load_paired = [&](int g, uint32_t (&x)[NS][16]) { load(g, x, true); };
         float acc[2][NS][4];
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -600,7 +616,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
             for (int i = 0; i < 4; ++i) {
                 const int col = 8 * n + 2 * t + (i & 1);
                 if ((i & (S - 1)) != s || col >= count) continue;
-                const float gv = acc[0][n][i], h = gv / (1.f + expf(-gv)) * acc[1][n][i];
+                // (the fast functions' few 2^-23 are far below the rounding of h)
+                const float gv = acc[0][n][i], h = __fdividef(gv, 1.f + __expf(-gv)) * acc[1][n][i];
                 // h in the order in which the down kernel's lanes read a 128-group: 16-byte pieces (q, t)
                 int c = (tile & 7) * 16 + tile_row(lane) + 8 * (i >> 1);
                 if (A.hperm) c = (c & ~7) | (c & 3) << 1 | (c >> 2 & 1);
@@ -690,11 +707,12 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
         auto load_h = [&](int g, uint32_t (&x)[NS][16]) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
+                if (have[n]) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                    if (have[n]) u = *reinterpret_cast<const uint4*>(hp[n] + g * 128 + 32 * j);
-                    x[n][4 * j] = u.x, x[n][4 * j + 1] = u.y, x[n][4 * j + 2] = u.z, x[n][4 * j + 3] = u.w;
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(hp[n] + g * 128 + 32 * j);
+                        x[n][4 * j] = u.x, x[n][4 * j + 1] = u.y, x[n][4 * j + 2] = u.z, x[n][4 * j + 3] = u.w;
+                    }
                 }
         };
         float acc[2][NS][4];
