@@ -63,6 +63,7 @@ struct MoeArgs {
     long long wait_cycles;
     int32_t T, k, E, H, I, ydt, stall;
     int32_t C, zrows;
+    uint32_t per_k;  // ceil(2^16 / k)
     int32_t hperm;  // h in the order of the 4-bit decode's pairs
 };
 
@@ -359,9 +360,9 @@ struct Stream {
 
 // ---- the pairs grouped by expert ---------------------------------------------------
 struct MoeList {
-    unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
-    uint32_t blk[kMaxBlocks];                 // expert, first slot << 10, tokens << 20
-    uint16_t first[kMoeMaxExperts];           // first slot of each expert
+    uint32_t mask[2][kMoeMaxExperts];  // tokens of each expert: the first 32, the others
+    uint32_t blk[kMaxBlocks];          // expert, first slot << 10, tokens << 20
+    uint16_t first[kMoeMaxExperts];    // first slot of each expert
     uint8_t slot_token[kMaxPairs];
     int scan[2][kMoeWarps];
     int blocks, slots;
@@ -369,56 +370,62 @@ struct MoeList {
 __device__ __forceinline__ int blk_expert(uint32_t b) { return (int)(b & 1023u); }
 __device__ __forceinline__ int blk_slot(uint32_t b) { return (int)(b >> 10 & 1023u); }
 __device__ __forceinline__ int blk_count(uint32_t b) { return (int)(b >> 20); }
+// the token of pair p < 1024: p / k by a multiplication (exact, k <= 16)
+__device__ __forceinline__ int pair_token(int p, const MoeArgs& A) { return (int)((uint32_t)p * A.per_k >> 16); }
 
 // blocks of up to BT tokens
-template <int THREADS, int BT>
+template <int BT>
 __device__ void build_list(MoeList& L, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < A.E; e += THREADS) L.mask[e] = 0ull;
+    for (int e = tid; e < A.E; e += kMoeThreads) L.mask[0][e] = L.mask[1][e] = 0u;
     __syncthreads();
-    for (int p = tid; p < A.T * A.k; p += THREADS) {
-        const int e = A.ids[p];
-        if (e >= 0 && e < A.E) atomicOr(&L.mask[e], 1ull << (p / A.k));  // a set: the order does not matter
+    for (int p = tid; p < A.T * A.k; p += kMoeThreads) {
+        const int e = A.ids[p], t = pair_token(p, A);
+        if (e >= 0 && e < A.E) atomicOr(&L.mask[t >> 5][e], 1u << (t & 31));  // a set: the order does not matter
     }
     __syncthreads();
-    const int per = (A.E + THREADS - 1) / THREADS, e0 = tid * per, e1 = min(A.E, e0 + per);
+    constexpr int kPer = kMoeMaxExperts / kMoeThreads;  // experts of a thread
     int slots = 0, blocks = 0;
-    for (int e = e0; e < e1; ++e) {
-        const int c = __popcll(L.mask[e]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        const int c = e < A.E ? __popc(L.mask[0][e]) + __popc(L.mask[1][e]) : 0;
         slots += c;
         blocks += (c + BT - 1) / BT;
     }
-    int s = slots, b = blocks;
+    // slots and blocks (below 2^16 each) summed over the threads before this one
+    const uint32_t mine = (uint32_t)slots << 16 | (uint32_t)blocks;
+    uint32_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int vs = __shfl_up_sync(0xffffffffu, s, o), vb = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= o) {
-            s += vs;
-            b += vb;
-        }
+        const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
     }
-    if (lane == 31) {
-        L.scan[0][warp] = s;
-        L.scan[1][warp] = b;
-    }
+    if (lane == 31) L.scan[0][warp] = (int)sum;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        s += L.scan[0][w];
-        b += L.scan[1][w];
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMoeWarps; ++w) {
+        const uint32_t v = (uint32_t)L.scan[0][w];
+        if (w < warp) before += v;
+        all += v;
     }
-    if (tid == THREADS - 1) {
-        L.slots = s;
-        L.blocks = b;
+    if (tid == 0) {
+        L.slots = (int)(all >> 16);
+        L.blocks = (int)(all & 0xFFFFu);
     }
-    s -= slots;
-    b -= blocks;
-    for (int e = e0; e < e1; ++e) {
-        unsigned long long m = L.mask[e];
+    sum += before - mine;
+    int s = (int)(sum >> 16), b = (int)(sum & 0xFFFFu);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = tid * kPer + i;
+        if (e >= A.E) break;
         L.first[e] = (uint16_t)s;
+        unsigned long long m = (unsigned long long)L.mask[1][e] << 32 | L.mask[0][e];
         for (int left = __popcll(m); left > 0; left -= BT) {
             const int n = min(BT, left);
             L.blk[b++] = (uint32_t)e | (uint32_t)s << 10 | (uint32_t)n << 20;
-            for (int i = 0; i < n; ++i) {
+            for (int q = 0; q < n; ++q) {
                 L.slot_token[s++] = (uint8_t)(__ffsll((long long)m) - 1);
                 m &= m - 1;
             }
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
                       M::kBoth ? 0u : bars + M::Gate::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
-    build_list<kMoeThreads, 8 * NS>(L, A);
+    build_list<8 * NS>(L, A);
     pdl_trigger();
 
     // warps that share a unit, each a part of K: the number whose rounds over all units end first (in groups; a unit
@@ -658,14 +665,16 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
     __shared__ float slot_w[kMaxPairs];
+    __shared__ int16_t pair_slot[kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, C = A.C, G = A.down.G;
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
     uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
     W w(A.down, A.down, 16, base + warp * W::kRing, base + kMoeWarps * W::kRing + warp * W::side(G),
         sm_addr(base + kMoeWarps * (W::kRing + W::side(G))) + warp * W::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    pdl_trigger();
     // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list<kMoeThreads, 8 * NS>(L, A);
+    build_list<8 * NS>(L, A);
     float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
     const int step = C * kMoeWarps, KS = down_slices(G, step, L.blocks, L.slots, A.zrows), tasks = L.blocks * KS;
     const int q0 = rank * kMoeWarps + warp;
@@ -681,15 +690,22 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) feed();
-    for (int b = threadIdx.x; b < L.blocks; b += kMoeThreads) {
-        const uint32_t blk = L.blk[b];
-        for (int i = 0; i < blk_count(blk); ++i) {
-            const int slot = blk_slot(blk) + i, tok = L.slot_token[slot];
-            float v = 0.f;  // a token may name an expert more than once
-            for (int j = 0; j < A.k; ++j)
-                if (A.ids[tok * A.k + j] == blk_expert(blk)) v += A.weights[tok * A.k + j];
-            slot_w[slot] = v;
+    // a pair's slot, or -1: none, or its token names the expert before; the slot's weight: that of all such pairs
+    for (int p = threadIdx.x; p < A.T * A.k; p += kMoeThreads) {
+        const int e = A.ids[p], tok = pair_token(p, A);
+        int slot = -1;
+        if (e >= 0 && e < A.E) {
+            const uint32_t below = (1u << (tok & 31)) - 1u;
+            slot = L.first[e] + (tok < 32 ? __popc(L.mask[0][e] & below) : __popc(L.mask[0][e]) + __popc(L.mask[1][e] & below));
+            float v = A.weights[p];
+            for (int q = tok * A.k; q < (tok + 1) * A.k; ++q)
+                if (q != p && A.ids[q] == e) {
+                    if (q < p) slot = -1;
+                    v += A.weights[q];
+                }
+            if (slot >= 0) slot_w[slot] = v;
         }
+        pair_slot[p] = (int16_t)slot;
     }
     __syncthreads();
     pdl_wait();
@@ -745,23 +761,35 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
     } else {
         __syncthreads();
     }
-    // a token's slots in the order of its choices, a slot's slices in order; rank q finishes tokens q, q + C, ...
-    for (int i = threadIdx.x; i < (A.T - rank + C - 1) / C * kDownRows; i += kMoeThreads) {
+    // Rank q finishes tokens q, q + C, ...: eight lanes an output, each adding every eighth of the token's (choice,
+    // slice) results, then one another's.
+    const int part = threadIdx.x & 7, items = A.k * KS, outs = (A.T - rank + C - 1) / C * kDownRows;
+    for (int i = threadIdx.x >> 3; i < (outs + 3 & ~3); i += kMoeThreads / 8) {  // (a warp's four outputs together)
         const int tok = rank + i / kDownRows * C, row = i % kDownRows;
         float v = 0.f;
-        for (int j = 0; j < A.k; ++j) {
-            const int e = A.ids[tok * A.k + j];
-            if (e < 0 || e >= A.E) continue;
-            bool seen = false;
-            for (int q = 0; q < j; ++q) seen |= A.ids[tok * A.k + q] == e;
-            if (seen) continue;  // its slot holds all its weights
-            const int slot = L.first[e] + __popcll(L.mask[e] & ((1ull << tok) - 1));
-            const float* p = z + (int64_t)slot * KS * kDownRows + row;
-            for (int q = 0; q < KS; ++q) v += __ldcg(p + q * kDownRows);
+        if (i < outs) {
+            int j = part / KS, q = part - j * KS;
+            const int dj = 8 / KS, dq = 8 - dj * KS;
+#pragma unroll 4
+            for (int n = part; n < items; n += 8) {
+                const int slot = pair_slot[tok * A.k + j];
+                if (slot >= 0) v += __ldcg(z + ((int64_t)slot * KS + q) * kDownRows + row);
+                j += dj;
+                q += dq;
+                if (q >= KS) {
+                    q -= KS;
+                    ++j;
+                }
+            }
         }
-        const int64_t at = (int64_t)tok * A.ldy + (int64_t)tile * kDownRows + row;
-        if (A.ydt == kF32) static_cast<float*>(A.y)[at] = v;
-        else static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(v);
+        v += __shfl_xor_sync(0xffffffffu, v, 1);
+        v += __shfl_xor_sync(0xffffffffu, v, 2);
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        if (part == 0 && i < outs) {
+            const int64_t at = (int64_t)tok * A.ldy + (int64_t)tile * kDownRows + row;
+            if (A.ydt == kF32) static_cast<float*>(A.y)[at] = v;
+            else static_cast<__nv_bfloat16*>(A.y)[at] = __float2bfloat16_rn(v);
+        }
     }
 }
 
@@ -871,6 +899,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.ldy = ldy;
     A.T = T;
     A.k = k;
+    A.per_k = (65536u + (uint32_t)k - 1) / (uint32_t)k;
     A.E = E;
     A.H = (int32_t)H;
     A.I = (int32_t)I;
@@ -916,15 +945,16 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     cfg.blockDim = dim3(kMoeThreads);
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.dynamicSmemBytes = (size_t)up_smem;
-    cfg.numAttrs = 0;
+    // (the up kernel begins before the work in front of it has ended and waits for it before its first read)
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
     void* args[] = {&A};
     e = cudaLaunchKernelExC(&cfg, ku.fn, args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
     cfg.blockDim = dim3(kMoeThreads);
     cfg.dynamicSmemBytes = (size_t)down_smem;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)A.C;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
