@@ -793,46 +793,52 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
     }
 }
 
-struct UpKernel {
-    const void* fn;
-    int (*smem)(int G);
-};
-template <int KG, int KU, int NS>
-UpKernel up_of() {
-    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), &MoeUp<KG, KU, NS>::smem};
-}
-template <int NS>
-UpKernel up_kernel(int kg, int ku) {
-    static const UpKernel table[3][3] = {{up_of<0, 0, NS>(), up_of<0, 1, NS>(), up_of<0, 2, NS>()},
-                                         {up_of<1, 0, NS>(), up_of<1, 1, NS>(), up_of<1, 2, NS>()},
-                                         {up_of<2, 0, NS>(), up_of<2, 1, NS>(), up_of<2, 2, NS>()}};
-    return table[kg][ku];
-}
-struct DownKernel {
-    const void* fn;
-    int (*smem)(int G);
-};
-template <int KIND, int NS>
-DownKernel down_of() {
-    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), &MoeDown<KIND>::smem};
-}
-template <int NS>
-DownKernel down_kernel(int kind) {
-    static const DownKernel table[3] = {down_of<0, NS>(), down_of<1, NS>(), down_of<2, NS>()};
-    return table[kind];
+// One split of the SM's memory for both kernels: with one of its own each, an SM is emptied and set up anew between them.
+cudaError_t shape_kernel(const void* fn) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
-int moe_sms() {
-    static int sms[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (sms[dev] == 0) {
-        int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return 0;
-        sms[dev] = v;
-    }
-    return sms[dev];
+// A kernel, its shared memory for rows of G groups and its setup on the current device.
+struct MoeKernel {
+    const void* fn;
+    int (*smem)(int G);
+    cudaError_t (*setup)();
+};
+template <int KG, int KU, int NS>
+cudaError_t up_setup() {
+    return once_per_device<MoeUp<KG, KU, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>)); });
 }
+template <int KG, int KU, int NS>
+MoeKernel up_of() {
+    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), &MoeUp<KG, KU, NS>::smem, &up_setup<KG, KU, NS>};
+}
+template <int NS>
+MoeKernel up_kernel(int kg, int ku) {
+    static const MoeKernel table[3][3] = {{up_of<0, 0, NS>(), up_of<0, 1, NS>(), up_of<0, 2, NS>()},
+                                          {up_of<1, 0, NS>(), up_of<1, 1, NS>(), up_of<1, 2, NS>()},
+                                          {up_of<2, 0, NS>(), up_of<2, 1, NS>(), up_of<2, 2, NS>()}};
+    return table[kg][ku];
+}
+template <int KIND, int NS>
+struct DownOf;  // names a kernel
+template <int KIND, int NS>
+cudaError_t down_setup() {
+    return once_per_device<DownOf<KIND, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_down<KIND, NS>)); });
+}
+template <int KIND, int NS>
+MoeKernel down_of() {
+    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), &MoeDown<KIND>::smem, &down_setup<KIND, NS>};
+}
+template <int NS>
+MoeKernel down_kernel(int kind) {
+    static const MoeKernel table[3] = {down_of<0, NS>(), down_of<1, NS>(), down_of<2, NS>()};
+    return table[kind];
+}
+// CTAs of so much shared memory on an SM: two by the kernels' registers, fewer by the SM's 228 KB (each CTA takes 1 KB
+// more, and up to 15 KB of static shared memory)
+int ctas_per_sm(int smem) { return std::max(1, std::min(2, (228 * 1024) / (smem + 16 * 1024))); }
 
 bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K) {
     TensorMapEncodeFn enc = tensor_map_encoder();
@@ -860,13 +866,6 @@ bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K) {
     return true;
 }
 
-// One split of the SM's memory for both kernels: with one of its own each, an SM is emptied and set up anew between them.
-cudaError_t shape_kernel(const void* fn) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-}
-
 }  // namespace
 
 namespace {
@@ -880,7 +879,7 @@ size_t moe_data_bytes(int64_t T, int k, int64_t H, int64_t I) { return h_bytes(T
 cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWeights& down, int E, int64_t H, int64_t I,
                        const uint16_t* x, int64_t ldx, const int32_t* ids, const float* weights, int T, int k, void* y,
                        int ydt, int64_t ldy, void* data, long long wait_cycles, bool stall, cudaStream_t st) {
-    const int sms = moe_sms();
+    const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInitializationError;
     MoeArgs A;
     std::memset(&A, 0, sizeof(A));
@@ -908,19 +907,15 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     // Sets of eight columns that share a decode: one while an expert's tokens seldom exceed eight, else two (a second
     // set costs about a tenth of a product, a second decode a whole one)
     const int NS = T * k > 5 * E ? 2 : 1;
-    const UpKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
-    const DownKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
+    const MoeKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
+    const MoeKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
     const int up_smem = ku.smem(A.gate.G), down_smem = kd.smem(A.down.G);
-    cudaError_t e = shape_kernel(ku.fn);
+    if (up_smem > 160 * 1024 || down_smem > 160 * 1024) return cudaErrorInvalidConfiguration;
+    cudaError_t e = ku.setup();
     if (e != cudaSuccess) return e;
-    e = shape_kernel(kd.fn);
+    e = kd.setup();
     if (e != cudaSuccess) return e;
-    int per_sm = 0, down_per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ku.fn, kMoeThreads, (size_t)up_smem);
-    if (e != cudaSuccess) return e;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&down_per_sm, kd.fn, kMoeThreads, (size_t)down_smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1 || down_per_sm < 1) return cudaErrorInvalidConfiguration;
+    const int per_sm = ctas_per_sm(up_smem), down_per_sm = ctas_per_sm(down_smem);
     // CTAs per cluster of the down kernel: the count whose waves, each as long as a warp's share of the blocks that
     // the tokens are expected to fill (in sixteenths of a block), end first
     const double filled = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T)) + T * k / (16.0 * NS);

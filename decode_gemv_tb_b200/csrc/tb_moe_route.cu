@@ -26,6 +26,7 @@
 #include "tb_internal.h"
 
 #include <cstring>
+#include <type_traits>
 
 namespace tb {
 
@@ -233,8 +234,9 @@ size_t route_smem(int TB, int E, int H) { return (size_t)8 * ((E + 1) & ~1) + (s
 template <int TB>
 cudaError_t launch(const RouteArgs& A, cudaStream_t st) {
     const size_t smem = route_smem(TB, A.E, A.H);
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    const cudaError_t e = once_per_device<std::integral_constant<int, TB>>([] {
+        return cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    });
     if (e != cudaSuccess) return e;
     k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * rt_cluster(TB), kRtThreads, smem, st>>>(A);
     return cudaGetLastError();

@@ -556,18 +556,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) k_mx4_prefill(const __grid_con
 using Pre256 = PreCfg<256, 3>;
 using Pre128 = PreCfg<128, 5>;
 
-int mx_sms() {
-    static int sms[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (sms[dev] == 0) {
-        int v = 0;
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) return 0;
-        sms[dev] = v;
-    }
-    return sms[dev];
-}
-
 bool encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, int box_rows) {
     TensorMapEncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
@@ -600,7 +588,9 @@ cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
     A.units = (uint32_t)units;
     const void* fn = reinterpret_cast<const void*>(&k_mx4_gemm<C>);
     const int smem = C::smem(S);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2));
+    const cudaError_t e = once_per_device<C>([&] {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2));
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
@@ -642,8 +632,9 @@ cudaError_t launch_prefill(PreArgs& A, const void* w, const void* x, int64_t K, 
     // the units that run at once form a block of about sqrt(148) tiles of W by as many of X: what they read from L2
     // and, at long K, from HBM is least
     A.group = 12;
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_mx4_prefill<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const cudaError_t e = once_per_device<C>([&] {
+        return cudaFuncSetAttribute(k_mx4_prefill<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
     if (e != cudaSuccess) return e;
     k_mx4_prefill<C><<<(unsigned)std::min<int64_t>(units, sms), kPreThreads, C::kSmem, st>>>(A);
     return cudaGetLastError();
@@ -654,7 +645,7 @@ cudaError_t launch_prefill(PreArgs& A, const void* w, const void* x, int64_t K, 
 cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* x, const uint8_t* x_scales, void* Y,
                             int ydt, int64_t ldy, int64_t M, int64_t N, int64_t K, long long wait_cycles, bool stall,
                             cudaStream_t st) {
-    const int sms = mx_sms();
+    const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInitializationError;
     const int64_t T = (N + kRows - 1) / kRows, es = ydt == kF32 ? 4 : 2;
     const int64_t pre = ((M + kRows - 1) / kRows) * T;  // tiles of 128 x 128

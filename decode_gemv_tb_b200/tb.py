@@ -283,31 +283,41 @@ def tb_gate_up_silu(gate, up, h: torch.Tensor, ws: torch.Tensor | None = None, f
 
 # ---- microscaled 4-bit floats -------------------------------------------------
 
-def _same_device(first: torch.Tensor, *rest) -> None:
-    """The library launches on the current device: every tensor has to live there."""
-    if not first.is_cuda:
+def _same_device(first: torch.Tensor, *rest) -> int:
+    """The library launches on the current device: every tensor has to live there.  Returns its index."""
+    dev = first.get_device()  # -1: not a CUDA tensor
+    if dev < 0:
         raise TBError("tensors must be CUDA tensors")
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise TBError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if dev != torch._C._cuda_getDevice():
+        raise TBError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     for t in rest:
-        if t is not None and t.device != dev:
-            raise TBError(f"tensors on different devices: {dev} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise TBError(f"tensors on different devices: cuda:{dev} and {t.device}")
+    return dev
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream of a device, as torch's own generated code asks for it (the Stream object of
+    torch.cuda.current_stream takes longer to make than a small kernel runs)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     """Row stride of a [rows][cols] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise TBError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise TBError(f"{name}'s rows must be contiguous")
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _bytes(t: torch.Tensor, name: str, need: int) -> int:
     if t.dtype != torch.uint8 or t.numel() < need:
         raise TBError(f"{name} must hold at least {need} bytes as uint8")
-    return _dev(t, name)
+    if not t.is_contiguous():
+        raise TBError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def mx4_code_bytes(N: int, K: int) -> int:
@@ -330,7 +340,7 @@ def tb_mx4_quantize(W: torch.Tensor, codes: torch.Tensor | None = None, scales: 
     N, K = W.shape
     ldw = _rows(W, "W", N, K)
     nc, ns = _mx4_sizes(N, K)
-    _same_device(W, codes, scales, bad_count)
+    dev = _same_device(W, codes, scales, bad_count)
     if codes is None:
         codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
     if scales is None:
@@ -339,7 +349,7 @@ def tb_mx4_quantize(W: torch.Tensor, codes: torch.Tensor | None = None, scales: 
         raise TBError("bad_count must be int32")
     bc = 0 if bad_count is None else _dev(bad_count, "bad_count")
     _check(load().tb_mx4_quantize(W.data_ptr(), _wdtype(W), ldw, N, K, _bytes(codes, "codes", nc),
-                                  _bytes(scales, "scales", ns), bc, _stream(W) if stream is None else stream),
+                                  _bytes(scales, "scales", ns), bc, _raw_stream(dev) if stream is None else stream),
            "tb_mx4_quantize")
     return codes, scales
 
@@ -348,12 +358,12 @@ def tb_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int,
                       out_dtype=torch.bfloat16, stream: int | None = None) -> torch.Tensor:
     """The values that MX4 codes stand for, [N][K] fp32 or bf16."""
     nc, ns = _mx4_sizes(N, K)
-    _same_device(codes, scales, W)
+    dev = _same_device(codes, scales, W)
     if W is None:
         W = torch.empty((N, K), dtype=out_dtype, device=codes.device)
     ldw = _rows(W, "W", N, K)
     _check(load().tb_mx4_dequantize(_bytes(codes, "codes", nc), _bytes(scales, "scales", ns), N, K, W.data_ptr(),
-                                    _ydtype(W.dtype), ldw, _stream(codes) if stream is None else stream),
+                                    _ydtype(W.dtype), ldw, _raw_stream(dev) if stream is None else stream),
            "tb_mx4_dequantize")
     return W
 
@@ -364,13 +374,13 @@ def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Te
     """Y [M][N] = X W^T of two MX4 tensors (N rows of W, M rows of X, K columns)."""
     wc, wsb = _mx4_sizes(N, K)
     xc, xsb = _mx4_sizes(M, K)
-    _same_device(w_codes, w_scales, x_codes, x_scales, Y)
+    dev = _same_device(w_codes, w_scales, x_codes, x_scales, Y)
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
     ldy = _rows(Y, "Y", M, N)
     _check(load().tb_mx4_gemm(_bytes(w_codes, "w_codes", wc), _bytes(w_scales, "w_scales", wsb),
                               _bytes(x_codes, "x_codes", xc), _bytes(x_scales, "x_scales", xsb), Y.data_ptr(),
-                              _ydtype(Y.dtype), ldy, M, N, K, flags, _stream(Y) if stream is None else stream),
+                              _ydtype(Y.dtype), ldy, M, N, K, flags, _raw_stream(dev) if stream is None else stream),
            "tb_mx4_gemm")
     return Y
 
@@ -388,9 +398,9 @@ def _bf16_rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
 
 def _pairs(ids: torch.Tensor, weights: torch.Tensor, T: int, k: int):
     for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
-        if t.dtype != dt or t.shape != (T, k):
-            raise TBError(f"{name} must be [{T}][{k}] {dt}, got {tuple(t.shape)} {t.dtype}")
-    return _dev(ids, "ids"), _dev(weights, "weights")
+        if t.dtype != dt or t.shape != (T, k) or not t.is_contiguous():
+            raise TBError(f"{name} must be contiguous [{T}][{k}] {dt}, got {tuple(t.shape)} {t.dtype}")
+    return ids.data_ptr(), weights.data_ptr()
 
 
 def tb_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bool = True,
@@ -402,14 +412,14 @@ def tb_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: boo
     E = router.shape[0]
     if _bf16_rows(router, "router", E, H) != H:
         raise TBError("router must be contiguous")
-    _same_device(x, router, ids, weights)
+    dev = _same_device(x, router, ids, weights)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
     ip, wp = _pairs(ids, weights, T, k)
     _check(load().tb_moe_route(x.data_ptr(), ldx, router.data_ptr(), T, E, H, k, 1 if renormalize else 0, ip, wp,
-                               _stream(x) if stream is None else stream), "tb_moe_route")
+                               _raw_stream(dev) if stream is None else stream), "tb_moe_route")
     return ids, weights
 
 
@@ -417,7 +427,7 @@ class MoELayer:
     """A tb_moe_t and the tensors it points to."""
 
     def __init__(self, desc: MoE, tensors, device):
-        self.desc, self.tensors, self.device = desc, tensors, device
+        self.desc, self.tensors, self.device, self.H = desc, tensors, device, desc.H
         self.ptr = ctypes.addressof(desc)
 
 
@@ -436,7 +446,7 @@ def moe_layer(gate, up, down, E: int, H: int, I: int) -> MoELayer:
                 raise TBError(f"{name} scales must hold {N} x {K // 128} values")
             mats.append((_bytes(packed, name, packed_bytes(grid, N, K)), _bits(scales, f"{name} scales")))
     desc = MoE(*(m[0] for m in mats), *(m[1] for m in mats), gate[2], up[2], down[2], E, H, I)
-    return MoELayer(desc, (gate, up, down), gate[0].device)
+    return MoELayer(desc, (gate, up, down), gate[0].get_device())
 
 
 def moe_workspace_bytes(layer: MoELayer, T: int, k: int) -> int:
@@ -447,17 +457,17 @@ def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.T
            out_dtype=torch.float32, ws: torch.Tensor | None = None, flags: int = 0, stream: int | None = None) -> torch.Tensor:
     """y [T][H] = the routed experts' MLP of x [T][H] (bf16, rows may be strided), summed with the weights."""
     T, k = ids.shape
-    H = layer.desc.H
+    H = layer.H
     ldx = _bf16_rows(x, "x", T, H)
     ip, wp = _pairs(ids, weights, T, k)
-    if x.device != layer.device:
-        raise TBError(f"x on {x.device}, the layer on {layer.device}")
-    _same_device(x, ids, weights, y, ws)
+    dev = _same_device(x, ids, weights, y, ws)
+    if dev != layer.device:
+        raise TBError(f"x on cuda:{dev}, the layer on cuda:{layer.device}")
     if y is None:
         y = torch.empty((T, H), dtype=out_dtype, device=x.device)
     ldy = _rows(y, "y", T, H)
     if ws is None:
         ws = workspace(moe_workspace_bytes(layer, T, k), x.device)
     _check(load().tb_moe(layer.ptr, x.data_ptr(), ldx, ip, wp, T, k, y.data_ptr(), _ydtype(y.dtype), ldy, flags,
-                         _dev(ws, "workspace"), ws.numel(), _stream(x) if stream is None else stream), "tb_moe")
+                         _dev(ws, "workspace"), ws.numel(), _raw_stream(dev) if stream is None else stream), "tb_moe")
     return y
