@@ -20,18 +20,14 @@
 #include "tb_internal.h"
 
 #include <algorithm>
+#include <cstring>
 
 namespace tb {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTasks = 4;  // dequantisation: runs of 128 per half-warp
-constexpr int kLoads = 4;  // quantisation: 16-byte loads of a lane
-
-// scale word of (row, 128-run): 512-byte tiles of 128 rows x 4 blocks
-__device__ __forceinline__ int64_t scale_word(int64_t row, int64_t g, int64_t G) {
-    return ((row >> 7) * G + g) * 128 + (row & 31) * 4 + ((row >> 5) & 3);
-}
+constexpr int kLoads = 4;   // quantisation: 16-byte loads of a lane
+constexpr int kStores = 8;  // dequantisation: 16-byte stores of a lane
 
 // four values -> two bytes of codes, a in the lowest half-byte
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
@@ -53,6 +49,12 @@ struct QuantArgs {
     uint32_t pieces;    // of a row
     int32_t own_bad;    // the only CTA: it writes the count itself
 };
+
+// The count that the quantiser adds to, set to 0 while that kernel already runs.
+__global__ void k_mx4_zero(int32_t* bad) {
+    pdl_trigger();
+    *bad = 0;
+}
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
@@ -135,48 +137,52 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
                 for (int w = 0; w < kThreads / 32; ++w) t += part[w];
                 *A.bad = t;
             }
-        } else if ((threadIdx.x & 31) == 0 && bad) {
-            atomicAdd(A.bad, bad);  // an integer count: the order does not matter
+        } else {
+            pdl_wait();  // the count is 0
+            if ((threadIdx.x & 31) == 0 && bad) atomicAdd(A.bad, bad);  // of integers: the order does not matter
         }
     }
 }
 
 struct DequantArgs {
-    const uint32_t* codes;
-    const uint32_t* scales;
+    const uint8_t* codes;
+    const uint8_t* scales;
     void* W;
-    int64_t K, ldw, G, tasks;
+    int64_t K, ldw, G, warps;
+    uint32_t pieces;
 };
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A) {
-    const int lane16 = threadIdx.x & 15;
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4)) * kTasks;
-    int64_t row = first / A.G, g = first - row * A.G;
-    uint32_t c[kTasks], s[kTasks];
-    int64_t at[kTasks];
+    constexpr int V = DT == kF32 ? 4 : 8;  // values of a lane's 16 bytes
+    constexpr int S = 32 * V;              // values of a warp's store
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (id >= A.warps) return;
+    const int64_t row = A.warps <= 0x7FFFFFFF ? (uint32_t)id / A.pieces : id / A.pieces;
+    const int64_t k0 = (id - row * A.pieces) * (S * kStores) + lane * V;
+    const int left = (int)min(A.K - k0, (int64_t)(S * kStores));
+    const uint8_t* codes = A.codes + (row * A.K + k0) / 2;
+    const uint8_t* scale = A.scales + ((row >> 7) * A.G + (k0 >> 7)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+                           ((k0 >> 5) & 3);
+    char* out = static_cast<char*>(A.W) + (row * A.ldw + k0) * (DT == kF32 ? 4 : 2);
+    uint32_t c[kStores], e[kStores];
 #pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
-        const int64_t k = g * 128 + lane16 * 8;
-        const bool in = first + i < A.tasks && k < A.K;
-        at[i] = in ? row * A.ldw + k : -1;
-        c[i] = in ? __ldcs(A.codes + (row * A.K + k) / 8) : 0u;
-        s[i] = in ? __ldg(A.scales + scale_word(row, g, A.G)) : 0u;
-        if (++g == A.G) {
-            g = 0;
-            ++row;
-        }
+    for (int i = 0; i < kStores; ++i) {
+        const bool in = i * S < left;
+        if constexpr (DT == kF32) c[i] = in ? __ldcs(reinterpret_cast<const uint16_t*>(codes + i * (S / 2))) : 0u;
+        else c[i] = in ? __ldcs(reinterpret_cast<const uint32_t*>(codes + i * (S / 2))) : 0u;
+        e[i] = in ? __ldg(scale + i * (S / 128) * 512) : 0u;
     }
 #pragma unroll
-    for (int i = 0; i < kTasks; ++i) {
-        if (at[i] < 0) continue;
-        const uint32_t byte = (s[i] >> (8 * (lane16 >> 2))) & 255u;
+    for (int i = 0; i < kStores; ++i) {
+        if (i * S >= left) break;
         // 2^(byte - 127): below the normal range at 0, no number at 255
-        const float x = byte == 0 ? __uint_as_float(0x00400000u)
-                                  : (byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23));
-        float v[8];
+        const float x = e[i] == 0 ? __uint_as_float(0x00400000u)
+                                  : (e[i] == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(e[i] << 23));
+        float v[V];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < V / 2; ++j) {
             uint32_t h;
             asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}"
                 : "=r"(h)
@@ -185,9 +191,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
             v[2 * j + 1] = __half2float(__ushort_as_half((unsigned short)(h >> 16))) * x;
         }
         if constexpr (DT == kF32) {
-            float4* p = reinterpret_cast<float4*>(static_cast<float*>(A.W) + at[i]);
-            __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+            __stcs(reinterpret_cast<float4*>(out + i * 512), make_float4(v[0], v[1], v[2], v[3]));
         } else {
             uint32_t u[4];
 #pragma unroll
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
                 const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
                 u[j] = *reinterpret_cast<const uint32_t*>(&b);
             }
-            __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.W) + at[i]), make_uint4(u[0], u[1], u[2], u[3]));
+            __stcs(reinterpret_cast<uint4*>(out + i * 512), make_uint4(u[0], u[1], u[2], u[3]));
         }
     }
 }
@@ -218,26 +222,39 @@ cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t
     const int64_t blocks = (A.warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     A.own_bad = blocks == 1;
-    if (bad && blocks > 1) {
-        const cudaError_t e = cudaMemsetAsync(bad, 0, sizeof(int32_t), st);
-        if (e != cudaSuccess) return e;
-    }
-    if (w_dtype == kF32) k_mx4_quantize<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(A);
-    else k_mx4_quantize<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(A);
-    return cudaGetLastError();
+    const bool zero = bad && blocks > 1;
+    if (zero) k_mx4_zero<<<1, 1, 0, st>>>(bad);
+    // with a count to be set to 0 the quantiser begins beside that kernel (which began after all work in front of it)
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = zero ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    void* args[] = {&A};
+    return cudaLaunchKernelExC(&cfg,
+                               w_dtype == kF32 ? reinterpret_cast<const void*>(&k_mx4_quantize<kF32>)
+                                               : reinterpret_cast<const void*>(&k_mx4_quantize<kBF16>),
+                               args);
 }
 
 cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t N, int64_t K, void* W,
                                   int w_dtype, int64_t ldw, cudaStream_t st) {
     DequantArgs A;
-    A.codes = static_cast<const uint32_t*>(codes);
-    A.scales = reinterpret_cast<const uint32_t*>(scales);
+    A.codes = static_cast<const uint8_t*>(codes);
+    A.scales = scales;
     A.W = W;
     A.K = K;
     A.ldw = ldw;
     A.G = (K + 127) / 128;
-    A.tasks = N * A.G;
-    const int64_t per = kThreads / 16 * kTasks, blocks = (A.tasks + per - 1) / per;
+    const int64_t piece = 32 * (w_dtype == kF32 ? 4 : 8) * kStores;
+    A.pieces = (uint32_t)((K + piece - 1) / piece);
+    A.warps = N * A.pieces;
+    const int64_t blocks = (A.warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if (w_dtype == kF32) k_mx4_dequantize<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(A);
     else k_mx4_dequantize<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(A);
