@@ -245,9 +245,18 @@ struct Stream {
                                       uint32_t bars_, const MoeArgs& A)
         : m0(a), m1(b), ring(ring_), scl(scl_), bars(bars_), limit(A.wait_cycles), off1(off), stall(A.stall != 0),
           dead(false), pn(0), pu(0), cn(0), cu(0), prow(0), pg(0), pend(0) {
-        if (bars != 0 && (threadIdx.x & 31) == 0)  // (0: a stream that is never used)
+        if (bars != 0 && (threadIdx.x & 31) == 0) {  // (0: a stream that is never used)
 #pragma unroll
             for (int i = 0; i < 2 * kStages; ++i) mb_init(bars + 8 * i, 1);
+            if (threadIdx.x == 0) {
+                prefetch_map(&a.codes);
+                if (TILES == 2) prefetch_map(&b.codes);
+                if (KIND == 2) {
+                    prefetch_map(&a.tiles);
+                    if (TILES == 2) prefetch_map(&b.tiles);
+                }
+            }
+        }
     }
     __device__ __forceinline__ bool wide() const { return KIND != 2 && m0.G > kMaxScaleGroups; }
     __device__ __forceinline__ bool open() const { return pg < pend; }
@@ -297,8 +306,8 @@ struct Stream {
     }
 
     // acc += the unit's rows times the columns that load_x(g, x) gives, groups g0 .. g1 - 1; feed() requests the next
-    // stage of this stream
-    template <int NS, class LoadX, class Feed>
+    // stage of this stream.  PAIR: the columns are in natural order and the 4-bit decoder wants its pairs.
+    template <int NS, bool PAIR, class LoadX, class Feed>
     __device__ __forceinline__ void multiply(int64_t row0, int g0, int g1, LoadX load_x, Feed feed,
                                              float (&acc)[TILES][NS][4]) {
         const int lane = threadIdx.x & 31, t = lane & 3, row = tile_row(lane), G = m0.G;
@@ -334,6 +343,11 @@ struct Stream {
                 // with one set the next group's activations are requested ahead of this one's products
                 if (NS == 1 && i + 1 < kGroups && g + i + 1 < g1) load_x(g + i + 1, x[(i + 1) % kBuf]);
                 if (NS > 1 && i > 0) load_x(g + i, x[0]);
+                uint32_t xp[NS][16];
+                if constexpr (PAIR) {
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) pair_up(xp[n], x[i % kBuf][n]);
+                }
 #pragma unroll
                 for (int w = 0; w < TILES; ++w) {
                     uint32_t s0, s1;
@@ -349,7 +363,8 @@ struct Stream {
                         s1 = *reinterpret_cast<const uint16_t*>(p + 16 * G);
                     }
                     const uint32_t at = KIND == 1 ? first + i * 48 : first ^ (uint32_t)(i * group_bytes(KIND));
-                    group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, x[i % kBuf], acc[w]);
+                    if constexpr (PAIR) group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, xp, acc[w]);
+                    else group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, x[i % kBuf], acc[w]);
                 }
             }
             __syncwarp();
@@ -476,15 +491,15 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
     build_list<8 * NS>(L, A);
     pdl_trigger();
 
-    // warps that share a unit, each a part of K: the number whose rounds over all units end first (in groups; a unit
-    // costs about one more to begin and end, two more where its parts are added)
+    // warps that share a unit, each a part of K: the number whose rounds over all units end first (in half groups; a unit
+    // costs about one to begin and end, two where its parts are added)
     const int tiles = A.I / 16, units = L.blocks * tiles;
     int lg = 0, least = 0x7FFFFFFF;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (1 << i > G) break;
         const int slots = (int)gridDim.x * kMoeWarps >> i, rounds = (units + slots - 1) / slots;
-        const int cost = rounds * ((G + (1 << i) - 1 >> i) + (i ? 3 : 1));
+        const int cost = rounds * (2 * (G + (1 << i) - 1 >> i) + (i ? 2 : 1));
         if (cost < least) {
             least = cost;
             lg = i;
@@ -541,44 +556,32 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
             have[n] = 8 * n + r < count;
             xr[n] = A.x + (int64_t)(have[n] ? L.slot_token[slot0 + 8 * n + r] : 0) * A.ldx + 32 * t;
         }
-        auto load = [&](int g, uint32_t (&x)[NS][16], bool paired) {
+        auto load = [&](int g, uint32_t (&x)[NS][16]) {
 #pragma unroll
             for (int n = 0; n < NS; ++n)
                 if (have[n]) {
-                    uint32_t v[16];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const uint4 w = __ldg(reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q));
-                        v[4 * q] = w.x, v[4 * q + 1] = w.y, v[4 * q + 2] = w.z, v[4 * q + 3] = w.w;
-                    }
-                    if (paired) {
-                        pair_up(x[n], v);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) x[n][q] = v[q];
+                        x[n][4 * q] = w.x, x[n][4 * q + 1] = w.y, x[n][4 * q + 2] = w.z, x[n][4 * q + 3] = w.w;
                     }
                 }
         };
-        auto load_plain = [&](int g, uint32_t (&x)[NS][16]) { load(g, x, false); };
-        auto load_paired = [&](int g, uint32_t (&x)[NS][16]) { load(g, x, true); };
         float acc[2][NS][4];
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
         if constexpr (M::kBoth) {
-            if constexpr (KG == 2) gate.template multiply<NS>(row0, g0, g1, load_paired, feed_gate, acc);
-            else gate.template multiply<NS>(row0, g0, g1, load_plain, feed_gate, acc);
+            gate.template multiply<NS, KG == 2>(row0, g0, g1, load, feed_gate, acc);
         } else {
             float one[1][NS][4], two[1][NS][4];
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) one[0][n][i] = two[0][n][i] = 0.f;
-            if constexpr (KG == 2) gate.template multiply<NS>(row0, g0, g1, load_paired, feed_gate, one);
-            else gate.template multiply<NS>(row0, g0, g1, load_plain, feed_gate, one);
-            if constexpr (KU == 2) up.template multiply<NS>(row0, g0, g1, load_paired, feed_up, two);
-            else up.template multiply<NS>(row0, g0, g1, load_plain, feed_up, two);
+            gate.template multiply<NS, KG == 2>(row0, g0, g1, load, feed_gate, one);
+            up.template multiply<NS, KU == 2>(row0, g0, g1, load, feed_up, two);
 #pragma unroll
             for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
         for (int n = 0; n < NS; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
-        w.template multiply<NS>((int64_t)blk_expert(block) * A.H + (int64_t)tile * kDownRows, g0, g1, load_h, feed, acc);
+        w.template multiply<NS, false>((int64_t)blk_expert(block) * A.H + (int64_t)tile * kDownRows, g0, g1, load_h, feed, acc);
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
