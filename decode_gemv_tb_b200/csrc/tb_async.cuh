@@ -1,6 +1,6 @@
 // tb_async.cuh -- sm_100a building blocks of the 4-bit and expert-layer
 // kernels: bounded mbarrier waits, tensor and bulk copies (no multicast),
-// cp.async, clusters, mma.sync and the host side of tensor maps and
+// clusters, tensor memory, and the host side of tensor maps and
 // launches.
 #pragma once
 

@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncwarp();
+    if (S > 1) cluster_arrive();  // every CTA of the cluster has begun before any writes into another
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&tmem_sh)),
                      "r"((uint32_t)C::kTmem)
@@ -137,7 +139,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
     tc5_fence_before();
     __syncthreads();
     tc5_fence_after();
-    if (S > 1) cluster_arrive();  // every CTA of the cluster has begun before any writes into another
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
     int issued = 0, committed = 0;
 
@@ -275,6 +276,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
         }
     }
 
+    // Tensor memory is given back before the cluster waits for its ranks: no CTA holds columns that another CTA of its SM
+    // waits for while it waits itself for one that may be waiting for columns.
+    tc5_fence_before();
+    __syncthreads();
+    tc5_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kTmem)
+                     : "memory");
+
     if (S > 1) {
         // every rank's partial sums have arrived: add this rank's slice of columns in rank order
         __syncwarp();
@@ -300,17 +310,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
 
     // ---------------- drain and exit ----------------
     const bool aborted = __syncthreads_or(*abort) != 0;
-    if (aborted) {
-        if (warp == 0 && lane == 0)
-            for (int k = issued > ST ? issued - ST : 0; k < issued; ++k)
-                mb_drain(sm_addr(&full[k % ST]), (uint32_t)(k / ST) & 1u, A.wait_cycles);
-    }
-    tc5_fence_before();
+    if (aborted && warp == 0 && lane == 0)
+        for (int k = issued > ST ? issued - ST : 0; k < issued; ++k)
+            mb_drain(sm_addr(&full[k % ST]), (uint32_t)(k / ST) & 1u, A.wait_cycles);
     __syncthreads();
-    tc5_fence_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"((uint32_t)C::kTmem)
-                     : "memory");
 }
 
 // ---- prefill: batches of whole tiles -----------------------------------------------------

@@ -309,7 +309,7 @@ def _rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise TBError(f"{name}'s rows must be contiguous")
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else cols  # (a single row's stride reaches nothing)
 
 
 def _bytes(t: torch.Tensor, name: str, need: int) -> int:

@@ -392,7 +392,7 @@ TB_API tb_status_t tb_mx4_dequantize(const void *codes, const uint8_t *scales, i
                                      tb_dtype_t w_dtype, int64_t ldw, tb_stream_t stream);
 
 /* Y = X W^T of two MX4 tensors, 1 <= M <= 65536, on the block-scaled tensor
- * cores: one launch, no workspace, W read once per 256 batch rows.
+ * cores: one launch, no workspace; up to 128 batch rows W is read once.
  *   w_codes, w_scales  [N] rows, x_codes, x_scales  [M] rows, of K values;
  *                      16-byte aligned.
  *   Y                  [M][ldy] fp32 or bf16, ldy >= N; Y[m][n] for n < N
@@ -425,7 +425,7 @@ TB_API tb_status_t tb_mx4_gemm(const void *w_codes, const uint8_t *w_scales, con
  *     p(e) = exp(l[t][e] - max l[t]),  weights[t][j] = p(ids[t][j]) / Z,
  * Z the sum of p over the k chosen (renormalize != 0) or over all E.
  * Logits are summed in 64 bits, so the order is that of the exact values
- * unless they differ by less than H 2^-53 sum |x r|.
+ * unless they differ by less than H (2^-53 sum |x r| + 2^-178).
  *   x        [T][ldx] bf16, ldx >= H, ldx % 8 == 0, 16-byte aligned;
  *            1 <= T <= 65536.
  *   router   [E][H] bf16, 16-byte aligned, finite; 1 <= E <=

@@ -227,3 +227,106 @@ def test_gemm_waits_that_give_up_are_reported():
         assert tb.sync_status() == 6
         assert torch.isnan(Y).all()
         check_gemm(w, ws, x, xs)
+
+
+def test_calls_at_once_on_two_streams():
+    """Split and persistent products of two streams at the same time, beside the scalar grids' product, which takes
+    tensor memory too."""
+    rng = np.random.default_rng(11)
+    shapes = [(5, 4096, 2048), (40, 6000, 1056), (100, 2048, 2048), (300, 9000, 512)]
+    args = []
+    for M, N, K in shapes:
+        w, ws = R.random_mx4(N, K, rng)
+        x, xs = R.random_mx4(M, K, rng)
+        args.append((*R.to_gpu(w, ws), *R.to_gpu(x, xs), M, N, K))
+    want = [tb.tb_mx4_gemm(*a) for a in args]
+    wd, dense = R.random_matrix(4096, 2048, R.INT3, rng)
+    X = torch.from_numpy(rng.standard_normal((64, 2048))).to(torch.bfloat16).to(DEV)
+    y0 = tb.tb_gemm(dense[0], dense[2], dense[1], X, 4096, 2048)
+    wsp = tb.workspace(tb.workspace_bytes(64, 4096, 2048), DEV)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    out, dout = [[], []], []
+    for i in range(6):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                for j in range(4):
+                    out[s].append(tb.tb_mx4_gemm(*args[(j + 2 * s) % 4]))
+        with torch.cuda.stream(streams[2]):
+            dout.append(tb.tb_gemm(dense[0], dense[2], dense[1], X, 4096, 2048, ws=wsp))
+    torch.cuda.synchronize()
+    for s in range(2):
+        for i, y in enumerate(out[s]):
+            assert torch.equal(y, want[(i % 4 + 2 * s) % 4])
+    assert all(torch.equal(y, y0) for y in dout) and tb.sync_status() == 0
+
+
+def test_quantize_replays_with_its_count():
+    """The count is set anew by every replay, beside whatever it held."""
+    W = torch.randn((600, 1024), generator=torch.Generator().manual_seed(12)).to(DEV)
+    W[3, 5], W[599, 1000], W[100, 0] = float("nan"), float("inf"), float("-inf")
+    bad = torch.full((1,), 77, dtype=torch.int32, device=DEV)
+    codes, scales = tb.tb_mx4_quantize(W)
+    c2, s2 = torch.zeros_like(codes), torch.zeros_like(scales)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tb.tb_mx4_quantize(W, codes=c2, scales=s2, bad_count=bad)
+    idx = torch.from_numpy(R.scale_index(600, 1024).reshape(-1)).to(DEV)
+    for n in (3, 3, 2):
+        if n == 2:
+            W[3, 5] = 0.0  # (a NaN's code is that of 0)
+        graph.replay()
+        assert bad.item() == n
+        assert torch.equal(codes, c2) and torch.equal(scales[idx], s2[idx])
+
+
+def test_single_rows_of_wider_buffers():
+    """One row's stride reaches nothing, whatever it is."""
+    W = torch.zeros((1, 163), device=DEV)
+    W[:, :160] = torch.randn((1, 160), generator=torch.Generator().manual_seed(13))
+    c, s = tb.tb_mx4_quantize(W[:, :160])
+    c2, s2 = tb.tb_mx4_quantize(W[:, :160].contiguous())
+    assert torch.equal(c, c2)
+    idx = torch.from_numpy(R.scale_index(1, 160).reshape(-1)).to(DEV)
+    assert torch.equal(s[idx], s2[idx])
+    out = torch.full((1, 163), 3.0, device=DEV)
+    tb.tb_mx4_dequantize(c, s, 1, 160, W=out[:, :160])
+    assert torch.all(out[:, 160:] == 3.0)
+
+
+def test_tensors_past_four_gigabytes():
+    """Values, codes and outputs whose offsets pass 32 bits."""
+    N, K, n = 270000, 32768, 200
+    g = torch.Generator().manual_seed(14)
+    tail = torch.randn((n, K), generator=g).to(torch.bfloat16).to(DEV)
+    W = torch.zeros((N, K), dtype=torch.bfloat16, device=DEV)
+    W[-n:] = tail
+    bad = torch.empty(1, dtype=torch.int32, device=DEV)
+    codes, scales = tb.tb_mx4_quantize(W, bad_count=bad)
+    small = tb.tb_mx4_quantize(tail)
+    assert bad.item() == 0 and codes.numel() > 1 << 32
+    assert torch.equal(codes[-n:], small[0]) and not codes[:-n].any()
+    back = tb.tb_mx4_dequantize(codes, scales, N, K, W=W)
+    assert torch.equal(back[-n:], tb.tb_mx4_dequantize(*small, n, K)) and not back[:-n].any()
+    del back, W
+    X = torch.randn((3, K), generator=g).to(torch.bfloat16).to(DEV)
+    x = tb.tb_mx4_quantize(X)
+    Y = tb.tb_mx4_gemm(codes, scales, *x, 3, N, K)
+    a, b = (R.values(*R.quantize(t.double().cpu().numpy())[:2]) for t in (X, tail))
+    err = np.abs(Y[:, -n:].double().cpu().numpy() - a @ b.T)
+    assert np.all(err <= (K / 64 + 12) * 2.0 ** -23 * (np.abs(a) @ np.abs(b).T)) and not Y[:, :-n].any()
+
+
+def test_gemm_outputs_past_four_gigabytes():
+    rng = np.random.default_rng(15)
+    M, N, K, n = 65536, 65600, 32, 300
+    w, ws = R.random_mx4(N, K, rng)
+    x, xs = R.random_mx4(M, K, rng)
+    Y = tb.tb_mx4_gemm(*R.to_gpu(w, ws), *R.to_gpu(x, xs), M, N, K, out_dtype=torch.bfloat16)
+    assert M * N > 1 << 32
+    a, b = R.values(x, xs), R.values(w, ws)
+    for r in (slice(0, n), slice(M // 2, M // 2 + n), slice(M - n, M)):
+        for c in (slice(0, n), slice(N - n, N)):
+            ref = a[r] @ b[c].T
+            tol = (K / 64 + 12) * 2.0 ** -23 * (np.abs(a[r]) @ np.abs(b[c]).T) + 2.0 ** -8 * np.abs(ref)
+            assert np.all(np.abs(Y[r, c].double().cpu().numpy() - ref) <= tol)
