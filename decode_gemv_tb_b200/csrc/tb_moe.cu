@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
                 if (have[n]) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q));
+                        const uint4 w = *reinterpret_cast<const uint4*>(xr[n] + g * 128 + 8 * q);
                         x[n][4 * q] = w.x, x[n][4 * q + 1] = w.y, x[n][4 * q + 2] = w.z, x[n][4 * q + 3] = w.w;
                     }
                 }
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
             for (int i = 0; i < 4; ++i) {
                 const int col = 8 * n + 2 * t + (i & 1);
                 if ((i & (S - 1)) != s || col >= count) continue;
-                // (the fast functions' few 2^-23 are far below the rounding of h)
+                // (the fast functions' errors, at most 2^-16, are far below the rounding of h)
                 const float gv = acc[0][n][i], h = __fdividef(gv, 1.f + __expf(-gv)) * acc[1][n][i];
                 // h in the order in which the down kernel's lanes read a 128-group: 16-byte pieces (q, t)
                 int c = (tile & 7) * 16 + tile_row(lane) + 8 * (i >> 1);

@@ -322,3 +322,131 @@ def test_routed_layer_run():
     assert torch.equal(ids.long(), rid)
     ref, tol = R.moe(G, U, D, E, x, ids, w)
     assert torch.all((y.double() - ref).abs() <= tol)
+
+
+# ---- calls beside one another, padded batches --------------------------------------------
+def test_moe_layers_in_a_row_hand_over_their_activations():
+    """Layers that read what the layer before wrote, through two buffers in turn and without a wait between them: the
+    same bits as one by one with fresh buffers, eagerly and in a graph."""
+    g = torch.Generator().manual_seed(21)
+    T, E, k, H, I, depth = 3, 8, 2, 512, 128, 12
+    mats, layer = make_layer(E, H, I, (2, 1, 4), 22)
+    x0 = torch.randn((T, H), generator=g).to(torch.bfloat16).to(DEV)
+    ids = [draw_ids(T, k, E, g).to(DEV) for _ in range(depth)]
+    w = torch.rand((T, k), generator=g).to(DEV)
+    # weights that keep the activations near one from layer to layer
+    scale, want = [], x0
+    for i in range(depth):
+        f = 1.0 / tb.tb_moe(layer, want, ids[i], w).abs().mean().item()
+        scale.append((w * f).contiguous())
+        want = tb.tb_moe(layer, want, ids[i], scale[i], out_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+    assert torch.isfinite(want).all() and want.abs().max() > 0
+    ws = tb.workspace(tb.moe_workspace_bytes(layer, T, k), DEV)
+    buf = [x0.clone(), torch.empty_like(x0)]
+
+    def run():
+        for i in range(depth):
+            tb.tb_moe(layer, buf[i & 1], ids[i], scale[i], y=buf[~i & 1], ws=ws)
+
+    for _ in range(5):
+        buf[0].copy_(x0)
+        run()
+        assert torch.equal(buf[depth & 1], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        buf[0].copy_(x0)
+        graph.replay()
+        assert torch.equal(buf[depth & 1], want)
+    assert tb.sync_status() == 0
+
+
+def test_calls_at_once_on_two_streams():
+    """Two streams, each with its own workspace, route and apply experts at the same time."""
+    g = torch.Generator().manual_seed(23)
+    T, E, k, H, I = 24, 16, 4, 512, 256
+    mats, layer = make_layer(E, H, I, (0, 2, 4), 24)
+    r = torch.randn((E, H), generator=g).to(torch.bfloat16).to(DEV)
+    xs = [torch.randn((T, H), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    want = []
+    for x in xs:
+        ids, w = tb.tb_moe_route(x, r, k)
+        want.append(tb.tb_moe(layer, x, ids, w))
+    ws = [tb.workspace(tb.moe_workspace_bytes(layer, T, k), DEV) for _ in range(2)]
+    ids = [torch.empty((T, k), dtype=torch.int32, device=DEV) for _ in range(2)]
+    w = [torch.empty((T, k), device=DEV) for _ in range(2)]
+    ys = [[torch.zeros((T, H), device=DEV) for _ in range(10)] for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(10):
+        for s in range(2):
+            with torch.cuda.stream(streams[s]):
+                tb.tb_moe_route(xs[s], r, k, ids=ids[s], weights=w[s])
+                tb.tb_moe(layer, xs[s], ids[s], w[s], y=ys[s][i], ws=ws[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for y in ys[s]:
+            assert torch.equal(y, want[s])
+    assert tb.sync_status() == 0
+
+
+def test_moe_padded_batch():
+    """Padding rows (no expert; activations and weights that are no numbers) give 0 and change nothing."""
+    g = torch.Generator().manual_seed(25)
+    mats, layer = make_layer(6, 256, 128, (2, 0, 4), 26)
+    x = torch.randn((11, 256), generator=g).to(torch.bfloat16)
+    ids, w = draw_ids(11, 3, 6, g), torch.rand((11, 3), generator=g)
+    want = check_moe(mats, layer, x, ids, w)[:, :256]
+    xp = torch.full((64, 256), float("nan"), dtype=torch.bfloat16)
+    ip, wp = torch.full((64, 3), -1, dtype=torch.int32), torch.full((64, 3), float("nan"))
+    xp[:11], ip[:11], wp[:11] = x, ids, w
+    y = tb.tb_moe(layer, xp.to(DEV), ip.to(DEV), wp.to(DEV))
+    ref, tol = R.moe(*mats, 6, x.to(DEV), ids, w.to(DEV))  # (another grouping may be taken: within the bound)
+    assert torch.all((y[:11].double() - ref).abs() <= tol) and torch.all(y[11:] == 0)
+    assert torch.all((want.double() - ref).abs() <= tol)
+
+
+def test_single_rows_of_wider_buffers():
+    """One row's stride reaches nothing, whatever it is."""
+    g = torch.Generator().manual_seed(27)
+    mats, layer = make_layer(4, 256, 128, (2, 2, 4), 28)
+    wide = torch.zeros((1, 259), dtype=torch.bfloat16, device=DEV)
+    wide[:, :256] = torch.randn((1, 256), generator=g)
+    x, r = wide[:, :256], torch.randn((4, 256), generator=g).to(torch.bfloat16).to(DEV)
+    ids, w = tb.tb_moe_route(x, r, 2)
+    ids2, w2 = tb.tb_moe_route(x.contiguous(), r, 2)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+    assert torch.equal(tb.tb_moe(layer, x, ids, w), tb.tb_moe(layer, x.contiguous(), ids, w))
+
+
+def test_route_long_batch():
+    """More clusters than the GPU holds at once, the last of them not full."""
+    g = torch.Generator().manual_seed(29)
+    x = torch.randn((1501, 96), generator=g).to(torch.bfloat16)
+    check_route(x, torch.randn((33, 96), generator=g).to(torch.bfloat16), 5, True)
+
+
+def test_moe_experts_past_four_gigabytes():
+    """The last of so many experts that its codes begin past 2^32 bytes."""
+    E, H, I = 172, 8192, 8192
+    rng = np.random.default_rng(30)
+    mats, parts = [], []
+    for rows, cols, grid in ((I, H, R.MX4), (I, H, R.INT3), (H, I, R.MX4)):
+        m, (packed, scales, _) = R.random_matrix(rows, cols, grid, rng)
+        packed, scales = packed.reshape(-1), scales.reshape(-1)
+        assert (E - 1) * packed.numel() * packed.element_size() > 1 << 32
+        P = torch.zeros(E * packed.numel(), dtype=packed.dtype, device=DEV)
+        S = torch.zeros(E * scales.numel(), dtype=scales.dtype, device=DEV)
+        P[-packed.numel():], S[-scales.numel():] = packed, scales
+        mats.append(m)
+        parts.append((P, S, grid))
+    layer = tb.moe_layer(*parts, E, H, I)
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn((2, H), generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.rand((2, 2), generator=g).to(DEV)
+    y = tb.tb_moe(layer, x, torch.tensor([[E - 1, -1], [0, E - 1]], dtype=torch.int32, device=DEV), w)
+    # every other expert is 0: the rest of the layer does not count
+    ref, tol = R.moe(*mats, 1, x, torch.tensor([[0, -1], [-1, 0]], dtype=torch.int32), w)
+    assert torch.all((y.double() - ref).abs() <= tol) and ref.abs().max() > 0
