@@ -1,9 +1,10 @@
-"""Build libtb_b200.so in-tree with nvcc for sm_100a.
+"""Build libtb_b200.so in-tree with nvcc for sm_100a, and _tb_bind.so beside it.
 
     python -m decode_gemv_tb_b200.build [--verbose]
 
 The shared library is self-contained (static CUDA runtime) and exports only
-the C interface of include/tb.h.
+the C interface of include/tb.h; _tb_bind.so holds the Python calls that go
+through the CPython API and torch's C++ interface instead of ctypes.
 """
 from __future__ import annotations
 
@@ -11,11 +12,13 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libtb_b200.so")
+BIND = os.path.join(PKG, "_tb_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -27,16 +30,36 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     deps.append(os.path.join(ROOT, "include", "tb.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(LIB, deps)
+
+
+def _build_bind(force: bool):
+    src = os.path.join(CSRC, "tb_bind.cpp")
+    if not force and not _older(BIND, [src, os.path.join(ROOT, "include", "tb.h")]):
+        return
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    dirs = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), os.path.join(cuda, "include"),
+            *cpp_extension.include_paths()]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{d}" for d in dirs), src,
+           "-o", BIND + ".tmp", *(f"-L{d}" for d in cpp_extension.library_paths()),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    subprocess.run(cmd, check=True)
+    os.replace(BIND + ".tmp", BIND)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_bind(force)
     if not force and not _stale():
         return LIB
     cmd = [NVCC, *ARCH, *FLAGS, "-I", os.path.join(ROOT, "include")]

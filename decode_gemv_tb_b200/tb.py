@@ -58,6 +58,10 @@ SIGNATURES = {
 }
 
 
+# entry points called by _tb_bind.so, and the text of their statuses, in the order that its init takes
+BOUND = ("tb_mx4_quantize", "tb_mx4_dequantize", "tb_mx4_gemm", "tb_moe_route", "tb_moe", "tb_status_string")
+
+
 class Linear(ctypes.Structure):
     """tb_linear_t"""
     _fields_ = [("packed", _P), ("scales", _P), ("x", _P), ("y", _P), ("N", _I64), ("K", _I64),
@@ -76,11 +80,12 @@ class TBError(RuntimeError):
 
 
 _lib = None
+_bind = None  # _tb_bind.so, the calls that do not go through ctypes
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the shared library (raises if it is missing)."""
-    global _lib
+    global _lib, _bind
     if _lib is None:
         if not os.path.exists(path):
             raise TBError(f"libtb_b200.so not built at {path}; run `python -m decode_gemv_tb_b200.build`")
@@ -89,7 +94,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             f = getattr(lib, name)
             f.restype = res
             f.argtypes = args
-        _lib = lib
+        try:
+            from decode_gemv_tb_b200 import _tb_bind
+        except ImportError as e:
+            raise TBError(f"_tb_bind.so: {e}; run `python -m decode_gemv_tb_b200.build`") from e
+        _tb_bind.init(TBError, *(ctypes.cast(getattr(lib, name), _P).value for name in BOUND))
+        _bind, _lib = _tb_bind, lib
     return _lib
 
 
@@ -296,22 +306,6 @@ def _same_device(first: torch.Tensor, *rest) -> int:
     return dev
 
 
-def _raw_stream(dev: int) -> int:
-    """The current stream of a device, as torch's own generated code asks for it (the Stream object of
-    torch.cuda.current_stream takes longer to make than a small kernel runs)."""
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
-    """Row stride of a [rows][cols] tensor whose rows are contiguous."""
-    if t.shape != (rows, cols):
-        raise TBError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise TBError(f"{name}'s rows must be contiguous")
-    return ld if rows > 1 else cols  # (a single row's stride reaches nothing)
-
-
 def _bytes(t: torch.Tensor, name: str, need: int) -> int:
     if t.dtype != torch.uint8 or t.numel() < need:
         raise TBError(f"{name} must hold at least {need} bytes as uint8")
@@ -337,34 +331,26 @@ def _mx4_sizes(N: int, K: int):
 def tb_mx4_quantize(W: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                     bad_count: torch.Tensor | None = None, stream: int | None = None):
     """W [N][K] (rows may be strided) -> codes [N][K/2] uint8 and the scale tiles (uint8)."""
-    N, K = W.shape
-    ldw = _rows(W, "W", N, K)
-    nc, ns = _mx4_sizes(N, K)
-    dev = _same_device(W, codes, scales, bad_count)
-    if codes is None:
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-    if scales is None:
-        scales = torch.empty(ns, dtype=torch.uint8, device=W.device)
-    if bad_count is not None and bad_count.dtype != torch.int32:
-        raise TBError("bad_count must be int32")
-    bc = 0 if bad_count is None else _dev(bad_count, "bad_count")
-    _check(load().tb_mx4_quantize(W.data_ptr(), _wdtype(W), ldw, N, K, _bytes(codes, "codes", nc),
-                                  _bytes(scales, "scales", ns), bc, _raw_stream(dev) if stream is None else stream),
-           "tb_mx4_quantize")
+    load()
+    if codes is None or scales is None:
+        N, K = W.shape
+        _, ns = _mx4_sizes(N, K)
+        if codes is None:
+            codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+        if scales is None:
+            scales = torch.empty(ns, dtype=torch.uint8, device=W.device)
+    _bind.mx4_quantize(W, codes, scales, bad_count, stream)
     return codes, scales
 
 
 def tb_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, W: torch.Tensor | None = None,
                       out_dtype=torch.bfloat16, stream: int | None = None) -> torch.Tensor:
     """The values that MX4 codes stand for, [N][K] fp32 or bf16."""
-    nc, ns = _mx4_sizes(N, K)
-    dev = _same_device(codes, scales, W)
+    load()
     if W is None:
+        _mx4_sizes(N, K)
         W = torch.empty((N, K), dtype=out_dtype, device=codes.device)
-    ldw = _rows(W, "W", N, K)
-    _check(load().tb_mx4_dequantize(_bytes(codes, "codes", nc), _bytes(scales, "scales", ns), N, K, W.data_ptr(),
-                                    _ydtype(W.dtype), ldw, _raw_stream(dev) if stream is None else stream),
-           "tb_mx4_dequantize")
+    _bind.mx4_dequantize(codes, scales, N, K, W, stream)
     return W
 
 
@@ -372,16 +358,10 @@ def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Te
                 M: int, N: int, K: int, Y: torch.Tensor | None = None, out_dtype=torch.float32, flags: int = 0,
                 stream: int | None = None) -> torch.Tensor:
     """Y [M][N] = X W^T of two MX4 tensors (N rows of W, M rows of X, K columns)."""
-    wc, wsb = _mx4_sizes(N, K)
-    xc, xsb = _mx4_sizes(M, K)
-    dev = _same_device(w_codes, w_scales, x_codes, x_scales, Y)
+    load()
     if Y is None:
         Y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
-    ldy = _rows(Y, "Y", M, N)
-    _check(load().tb_mx4_gemm(_bytes(w_codes, "w_codes", wc), _bytes(w_scales, "w_scales", wsb),
-                              _bytes(x_codes, "x_codes", xc), _bytes(x_scales, "x_scales", xsb), Y.data_ptr(),
-                              _ydtype(Y.dtype), ldy, M, N, K, flags, _raw_stream(dev) if stream is None else stream),
-           "tb_mx4_gemm")
+    _bind.mx4_gemm(w_codes, w_scales, x_codes, x_scales, M, N, K, Y, flags, stream)
     return Y
 
 
@@ -390,36 +370,16 @@ def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Te
 MOE_MAX_TOKENS, MOE_MAX_TOPK, MOE_MAX_EXPERTS = 64, 16, 512
 
 
-def _bf16_rows(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
-        raise TBError(f"{name} must hold bf16 bit patterns")
-    return _rows(t, name, rows, cols)
-
-
-def _pairs(ids: torch.Tensor, weights: torch.Tensor, T: int, k: int):
-    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
-        if t.dtype != dt or t.shape != (T, k) or not t.is_contiguous():
-            raise TBError(f"{name} must be contiguous [{T}][{k}] {dt}, got {tuple(t.shape)} {t.dtype}")
-    return ids.data_ptr(), weights.data_ptr()
-
-
 def tb_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: bool = True,
                  ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream: int | None = None):
     """x [T][H] (rows may be strided), router [E][H], both bf16 -> the k best experts of every token, ids [T][k]
     int32, and their softmax weights [T][k] fp32."""
-    T, H = x.shape
-    ldx = _bf16_rows(x, "x", T, H)
-    E = router.shape[0]
-    if _bf16_rows(router, "router", E, H) != H:
-        raise TBError("router must be contiguous")
-    dev = _same_device(x, router, ids, weights)
+    load()
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        ids = torch.empty((x.shape[0], k), dtype=torch.int32, device=x.device)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    ip, wp = _pairs(ids, weights, T, k)
-    _check(load().tb_moe_route(x.data_ptr(), ldx, router.data_ptr(), T, E, H, k, 1 if renormalize else 0, ip, wp,
-                               _raw_stream(dev) if stream is None else stream), "tb_moe_route")
+        weights = torch.empty((x.shape[0], k), dtype=torch.float32, device=x.device)
+    _bind.moe_route(x, router, k, renormalize, ids, weights, stream)
     return ids, weights
 
 
@@ -456,18 +416,10 @@ def moe_workspace_bytes(layer: MoELayer, T: int, k: int) -> int:
 def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, y: torch.Tensor | None = None,
            out_dtype=torch.float32, ws: torch.Tensor | None = None, flags: int = 0, stream: int | None = None) -> torch.Tensor:
     """y [T][H] = the routed experts' MLP of x [T][H] (bf16, rows may be strided), summed with the weights."""
-    T, k = ids.shape
-    H = layer.H
-    ldx = _bf16_rows(x, "x", T, H)
-    ip, wp = _pairs(ids, weights, T, k)
-    dev = _same_device(x, ids, weights, y, ws)
-    if dev != layer.device:
-        raise TBError(f"x on cuda:{dev}, the layer on cuda:{layer.device}")
+    load()
     if y is None:
-        y = torch.empty((T, H), dtype=out_dtype, device=x.device)
-    ldy = _rows(y, "y", T, H)
+        y = torch.empty((ids.shape[0], layer.H), dtype=out_dtype, device=x.device)
     if ws is None:
-        ws = workspace(moe_workspace_bytes(layer, T, k), x.device)
-    _check(load().tb_moe(layer.ptr, x.data_ptr(), ldx, ip, wp, T, k, y.data_ptr(), _ydtype(y.dtype), ldy, flags,
-                         _dev(ws, "workspace"), ws.numel(), _raw_stream(dev) if stream is None else stream), "tb_moe")
+        ws = workspace(moe_workspace_bytes(layer, *ids.shape), x.device)
+    _bind.moe(layer.ptr, layer.H, layer.device, x, ids, weights, y, ws, flags, stream)
     return y
