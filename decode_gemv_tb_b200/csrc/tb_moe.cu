@@ -36,6 +36,7 @@
 #include "tb_internal.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -72,6 +73,7 @@ namespace {
 constexpr int kMoeWarps = 8;
 constexpr int kMoeThreads = kMoeWarps * 32;
 constexpr int kStages = 2;  // of a warp's ring
+constexpr int kCtasPerSM = 2;  // of both kernels: 128 registers a thread
 constexpr float kMoeNaN = __builtin_nanf("");
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxK;
 constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / 8;
@@ -82,8 +84,6 @@ constexpr int kMaxBlocks = kMoeMaxExperts + kMaxPairs / 8;
 __host__ __device__ constexpr int group_bytes(int kind) { return kind == 0 ? 32 : (kind == 1 ? 48 : 64); }
 __host__ __device__ constexpr int stage_groups(int kind) { return kind == 0 ? 4 : (kind == 1 ? 3 : 2); }
 __host__ __device__ constexpr int row_stride(int kind) { return kind == 1 ? 144 : 128; }
-// a unit's bf16 scales are copied whole up to this many groups; longer rows read them one by one
-constexpr int kMaxScaleGroups = 64;
 // the row of a 16-row tile that a lane holds first (the second is eight on): lane / 4, its three bits reversed
 __device__ __forceinline__ int tile_row(int lane) { return (lane >> 2 & 1) << 2 | (lane >> 2 & 2) | lane >> 4; }
 
@@ -222,13 +222,14 @@ struct Stream {
     static constexpr int kGroups = stage_groups(KIND);
     static constexpr int kCodes = 16 * row_stride(KIND);                  // of a tile in a stage
     static constexpr int kScales = KIND == 2 ? 256 * kGroups : 0;         // 4-bit: its scale rows
-    static constexpr int kStageCodes = (TILES * kCodes + 1023) & ~1023;   // (swizzled tiles begin at multiples of 1 KB)
-    static constexpr int kBars = 8 * 2 * kStages;                         // a stage's, a scale buffer's
+    // (swizzled tiles, 2 KB, begin at multiples of 1 KB)
+    static constexpr int kStageCodes = TILES * kCodes;
+    static constexpr int kBars = 8 * kStages;
     static constexpr int kRing = kStages * kStageCodes;
-    // scales beside the ring: per stage, or per unit (two in turn) the bf16 scales of its rows
-    __host__ __device__ static constexpr int side(int G) {
-        return (kStages * TILES * (KIND == 2 ? kScales : (G <= kMaxScaleGroups ? 32 * G : 0)) + 127) & ~127;
-    }
+    // 4-bit scales beside the ring.  (bf16 scales are read where they are used, two bytes a row and group: copied into
+    // shared memory by units they took as long, and the room of a second CTA: 61 tokens x 84 experts of 3584 x 1408,
+    // 2- and 3-bit, 237 us against 186.)
+    static constexpr int kSide = kStages * TILES * kScales;
 
     const MoeMat& m0;
     const MoeMat& m1;
@@ -237,17 +238,17 @@ struct Stream {
     long long limit;
     int off1;  // rows from tile 0 to tile 1: 0 (two matrices), or 16 from a row0 that is a multiple of 32
     bool stall, dead;
-    uint32_t pn, pu, cn, cu;  // stages and units requested, read
+    uint32_t pn, cn;          // stages requested, read
     int64_t prow;             // the open unit's first row, its next group and their end
     int pg, pend;
 
     __device__ __forceinline__ Stream(const MoeMat& a, const MoeMat& b, int off, uint8_t* ring_, uint8_t* scl_,
                                       uint32_t bars_, const MoeArgs& A)
         : m0(a), m1(b), ring(ring_), scl(scl_), bars(bars_), limit(A.wait_cycles), off1(off), stall(A.stall != 0),
-          dead(false), pn(0), pu(0), cn(0), cu(0), prow(0), pg(0), pend(0) {
+          dead(false), pn(0), cn(0), prow(0), pg(0), pend(0) {
         if (bars != 0 && (threadIdx.x & 31) == 0) {  // (0: a stream that is never used)
 #pragma unroll
-            for (int i = 0; i < 2 * kStages; ++i) mb_init(bars + 8 * i, 1);
+            for (int i = 0; i < kStages; ++i) mb_init(bars + 8 * i, 1);
             if (threadIdx.x == 0) {
                 prefetch_map(&a.codes);
                 if (TILES == 2) prefetch_map(&b.codes);
@@ -258,21 +259,10 @@ struct Stream {
             }
         }
     }
-    __device__ __forceinline__ bool wide() const { return KIND != 2 && m0.G > kMaxScaleGroups; }
     __device__ __forceinline__ bool open() const { return pg < pend; }
 
     // begins the requests of a unit
-    __device__ __forceinline__ void start(int64_t row0, int g0, int g1) {
-        prow = row0, pg = g0, pend = g1;
-        if (KIND != 2 && !wide() && (threadIdx.x & 31) == 0 && !stall) {
-            const uint32_t bar = bars + 8 * (kStages + pu % kStages), n = 32u * (uint32_t)m0.G;
-            const uint32_t dst = sm_addr(scl) + (pu % kStages) * TILES * n;
-            mb_arrive_expect(bar, TILES * n);
-            bulk_load(dst, m0.scales + row0 * m0.G, n, bar);
-            if (TILES == 2) bulk_load(dst + n, m1.scales + (row0 + off1) * m0.G, n, bar);
-        }
-        ++pu;
-    }
+    __device__ __forceinline__ void start(int64_t row0, int g0, int g1) { prow = row0, pg = g0, pend = g1; }
     // requests the next stage of the open unit
     __device__ __forceinline__ void request() {
         if ((threadIdx.x & 31) == 0 && !stall) {
@@ -300,9 +290,6 @@ struct Stream {
         if (!dead || (threadIdx.x & 31) != 0 || stall) return;
         for (uint32_t i = pn > kStages ? pn - kStages : 0; i < pn; ++i)
             mb_drain(bars + 8 * (i % kStages), i / kStages & 1u, limit);
-        if (KIND != 2 && !wide())
-            for (uint32_t i = pu > kStages ? pu - kStages : 0; i < pu; ++i)
-                mb_drain(bars + 8 * (kStages + i % kStages), i / kStages & 1u, limit);
     }
 
     // acc += the unit's rows times the columns that load_x(g, x) gives, groups g0 .. g1 - 1; feed() requests the next
@@ -314,14 +301,10 @@ struct Stream {
         // the lane's codes of a stage's first group, and what the swizzle makes of the others'
         const uint32_t first = KIND == 1 ? row * 144 + t * 12
                                          : row * 128 + (KIND == 0 ? (((t >> 1) ^ row) << 4) + (t & 1) * 8 : (t ^ row) << 4);
-        const uint8_t* su = nullptr;  // the unit's scales
-        if constexpr (KIND == 2) {
-            su = scl + row * 16 + (int)(row0 >> 5 & 3) * 4 + t;
-        } else if (!wide()) {
-            wait(bars + 8 * (kStages + cu % kStages), cu / kStages & 1u);
-            su = scl + (cu % kStages) * TILES * 32 * G + row * 2 * G;
-        }
-        ++cu;
+        // the lane's first scale: 4-bit of the ring's first stage, else of tile 0 (of tile 1: `beside`)
+        const uint8_t* const su = KIND == 2 ? scl + row * 16 + (int)(row0 >> 5 & 3) * 4 + t : nullptr;
+        const uint16_t* const sg = KIND == 2 ? nullptr : m0.scales + (row0 + row) * G;
+        const uint16_t* const beside = KIND == 2 || TILES == 1 ? nullptr : m1.scales + (row0 + off1 + row) * G;
         constexpr int kBuf = NS == 1 ? 2 : 1;
         uint32_t x[kBuf][NS][16];  // columns without a token stay 0: load_x leaves them alone
 #pragma unroll
@@ -354,13 +337,9 @@ struct Stream {
                     if constexpr (KIND == 2) {
                         const uint8_t* p = su + (s * TILES + w) * kScales + i * 256;
                         s0 = p[0], s1 = p[128];
-                    } else if (wide()) {
-                        const uint16_t* p = (w ? m1 : m0).scales + (row0 + w * off1 + row) * G + g + i;
-                        s0 = __ldg(p), s1 = __ldg(p + 8 * G);
                     } else {
-                        const uint8_t* p = su + w * 32 * G + 2 * (g + i);
-                        s0 = *reinterpret_cast<const uint16_t*>(p);
-                        s1 = *reinterpret_cast<const uint16_t*>(p + 16 * G);
+                        const uint16_t* p = (w ? beside : sg) + g + i;
+                        s0 = __ldg(p), s1 = __ldg(p + 8 * G);
                     }
                     const uint32_t at = KIND == 1 ? first + i * 48 : first ^ (uint32_t)(i * group_bytes(KIND));
                     if constexpr (PAIR) group_product<KIND, NS>(codes + w * kCodes + at, s0, s1, xp, acc[w]);
@@ -374,10 +353,12 @@ struct Stream {
 };
 
 // ---- the pairs grouped by expert ---------------------------------------------------
-struct MoeList {
+struct MoeMasks {
     uint32_t mask[2][kMoeMaxExperts];  // tokens of each expert: the first 32, the others
-    uint32_t blk[kMaxBlocks];          // expert, first slot << 10, tokens << 20
     uint16_t first[kMoeMaxExperts];    // first slot of each expert
+};
+struct MoeList {
+    uint32_t blk[kMaxBlocks];  // expert, first slot << 10, tokens << 20
     uint8_t slot_token[kMaxPairs];
     int scan[2][kMoeWarps];
     int blocks, slots;
@@ -390,13 +371,13 @@ __device__ __forceinline__ int pair_token(int p, const MoeArgs& A) { return (int
 
 // blocks of up to BT tokens
 template <int BT>
-__device__ void build_list(MoeList& L, const MoeArgs& A) {
+__device__ void build_list(MoeList& L, MoeMasks& X, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < A.E; e += kMoeThreads) L.mask[0][e] = L.mask[1][e] = 0u;
+    for (int e = tid; e < A.E; e += kMoeThreads) X.mask[0][e] = X.mask[1][e] = 0u;
     __syncthreads();
     for (int p = tid; p < A.T * A.k; p += kMoeThreads) {
         const int e = A.ids[p], t = pair_token(p, A);
-        if (e >= 0 && e < A.E) atomicOr(&L.mask[t >> 5][e], 1u << (t & 31));  // a set: the order does not matter
+        if (e >= 0 && e < A.E) atomicOr(&X.mask[t >> 5][e], 1u << (t & 31));  // a set: the order does not matter
     }
     __syncthreads();
     constexpr int kPer = kMoeMaxExperts / kMoeThreads;  // experts of a thread
@@ -404,7 +385,7 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
-        const int c = e < A.E ? __popc(L.mask[0][e]) + __popc(L.mask[1][e]) : 0;
+        const int c = e < A.E ? __popc(X.mask[0][e]) + __popc(X.mask[1][e]) : 0;
         slots += c;
         blocks += (c + BT - 1) / BT;
     }
@@ -435,8 +416,8 @@ __device__ void build_list(MoeList& L, const MoeArgs& A) {
     for (int i = 0; i < kPer; ++i) {
         const int e = tid * kPer + i;
         if (e >= A.E) break;
-        L.first[e] = (uint16_t)s;
-        unsigned long long m = (unsigned long long)L.mask[1][e] << 32 | L.mask[0][e];
+        X.first[e] = (uint16_t)s;
+        unsigned long long m = (unsigned long long)X.mask[1][e] << 32 | X.mask[0][e];
         for (int left = __popcll(m); left > 0; left -= BT) {
             const int n = min(BT, left);
             L.blk[b++] = (uint32_t)e | (uint32_t)s << 10 | (uint32_t)n << 20;
@@ -456,11 +437,17 @@ struct MoeUp {
     static constexpr bool kBoth = KG == KU;
     using Gate = Stream<KG, kBoth ? 2 : 1>;
     using Up = Stream<KU, 1>;
-    static constexpr int kWarpRing = Gate::kRing + (kBoth ? 0 : Up::kRing);
+    // a warp's rings: a swizzled one begins at a multiple of 1 KB, so it comes first
+    static constexpr bool kUpFirst = !kBoth && KG == 1;
+    static constexpr int kGateAt = kUpFirst ? Up::kRing : 0, kUpAt = kBoth || kUpFirst ? 0 : Gate::kRing;
+    static constexpr int kRings = Gate::kRing + (kBoth ? 0 : Up::kRing);
+    static constexpr int kWarpRing = kBoth && KG == 1 ? kRings : (kRings + 1023) & ~1023;
     static constexpr int kBars = Gate::kBars + (kBoth ? 0 : Up::kBars);
-    static constexpr int kPart = kMoeWarps * NS * 1024;  // partial sums of split units
-    __host__ __device__ static constexpr int side(int G) { return Gate::side(G) + (kBoth ? 0 : Up::side(G)); }
-    __host__ __device__ static int smem(int G) { return kMoeWarps * (kWarpRing + side(G) + kBars) + kPart + 1024; }
+    static constexpr int kPart = kMoeWarps * 1024;  // partial sums of split units, a set at a time; first the masks
+    static_assert(sizeof(MoeMasks) <= kPart);
+    static constexpr int kSide = Gate::kSide + (kBoth ? 0 : Up::kSide);
+    static constexpr int kSmem = kMoeWarps * (kWarpRing + kSide + kBars) + kPart + 1024;
+    static_assert(2 * (kSmem + (int)sizeof(MoeList) + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 // the S warps of unit `ui` of a CTA (constant barrier numbers: with a variable one a CTA holds all sixteen of its SM's)
@@ -472,7 +459,7 @@ __device__ __forceinline__ void unit_sync(int ui, int S) {
 }
 
 template <int KG, int KU, int NS>
-__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_up(const __grid_constant__ MoeArgs A) {
     using M = MoeUp<KG, KU, NS>;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
@@ -481,14 +468,14 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
     uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
     uint8_t* const ring = base + warp * M::kWarpRing;
     float* const part = reinterpret_cast<float*>(base + kMoeWarps * M::kWarpRing);
-    uint8_t* const side = base + kMoeWarps * M::kWarpRing + M::kPart + warp * M::side(G);
-    const uint32_t bars = sm_addr(base + kMoeWarps * (M::kWarpRing + M::side(G)) + M::kPart) + warp * M::kBars;
-    typename M::Gate gate(A.gate, M::kBoth ? A.up : A.gate, 0, ring, side, bars, A);
-    typename M::Up up(A.up, A.up, 0, ring + M::Gate::kRing, side + M::Gate::side(G),
+    uint8_t* const side = base + kMoeWarps * M::kWarpRing + M::kPart + warp * M::kSide;
+    const uint32_t bars = sm_addr(base + kMoeWarps * (M::kWarpRing + M::kSide) + M::kPart) + warp * M::kBars;
+    typename M::Gate gate(A.gate, M::kBoth ? A.up : A.gate, 0, ring + M::kGateAt, side, bars, A);
+    typename M::Up up(A.up, A.up, 0, ring + M::kUpAt, side + M::Gate::kSide,
                       M::kBoth ? 0u : bars + M::Gate::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
-    build_list<8 * NS>(L, A);
+    build_list<8 * NS>(L, *reinterpret_cast<MoeMasks*>(part), A);
     pdl_trigger();
 
     // warps that share a unit, each a part of K: the number whose rounds over all units end first (in half groups; a unit
@@ -594,31 +581,30 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_up(const __grid_constant
                 for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = kMoeNaN;
         }
         if (S > 1) {
-            float* mine = part + (warp * NS) * 256 + lane;
+            float* mine = part + warp * 256 + lane;
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
+            for (int n = 0; n < NS; ++n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mine[n * 256 + i * 32] = acc[0][n][i];
-                    mine[n * 256 + 128 + i * 32] = acc[1][n][i];
+                    mine[i * 32] = acc[0][n][i];
+                    mine[128 + i * 32] = acc[1][n][i];
                 }
-            unit_sync(ui, S);
-            // warp s of the unit finishes registers s, s + S, ... of every set
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
+                unit_sync(ui, S);
+                // warp s of the unit finishes registers s, s + S, ... of every set
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if ((i & (S - 1)) != s) continue;
                     float sg = 0.f, su = 0.f;
                     for (int w = 0; w < S; ++w) {
-                        const float* q = part + ((ui * S + w) * NS + n) * 256 + i * 32 + lane;
+                        const float* q = part + (ui * S + w) * 256 + i * 32 + lane;
                         sg += q[0];
                         su += q[128];
                     }
                     acc[0][n][i] = sg;
                     acc[1][n][i] = su;
                 }
-            unit_sync(ui, S);
+                unit_sync(ui, S);
+            }
         }
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -644,14 +630,14 @@ constexpr int kDownRows = 32;  // of a CTA: each warp holds all of them, two til
 
 // Slices of a block's groups, as far as z holds them: the number whose rounds over the tile's warps end first (in groups;
 // a task costs about two more to begin and end).
-__device__ __forceinline__ int down_slices(int G, int warps, int blocks, int slots, int zrows) {
-    int best = 1, least = 0x7FFFFFFF;
-    for (int k = 1; k <= G && k <= 8 && k * slots <= zrows; ++k) {
+struct DownSplit {
+    int slices, cost;
+};
+__host__ __device__ __forceinline__ DownSplit down_split(int G, int warps, int blocks, int slots, int zrows) {
+    DownSplit best{1, 0x7FFFFFFF};
+    for (int k = 1; k <= G && k <= 8 && (k == 1 || k * slots <= zrows); ++k) {
         const int cost = (blocks * k + warps - 1) / warps * ((G + k - 1) / k + 2);
-        if (cost < least) {
-            least = cost;
-            best = k;
-        }
+        if (cost < best.cost) best = {k, cost};
     }
     return best;
 }
@@ -659,27 +645,30 @@ __device__ __forceinline__ int down_slices(int G, int warps, int blocks, int slo
 template <int KIND>
 struct MoeDown {
     using W = Stream<KIND, 2>;
-    __host__ __device__ static int smem(int G) { return kMoeWarps * (W::kRing + W::side(G) + W::kBars) + 1024; }
+    static constexpr int kFixed = sizeof(MoeList) + sizeof(MoeMasks) + kMaxPairs * 6;
+    static constexpr int kSmem = kMoeWarps * (W::kRing + W::kSide + W::kBars) + 1024;
+    static_assert(2 * (kSmem + kFixed + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 template <int KIND, int NS>
-__global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_constant__ MoeArgs A) {
+__global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_down(const __grid_constant__ MoeArgs A) {
     using W = typename MoeDown<KIND>::W;
     extern __shared__ uint8_t raw[];
     __shared__ MoeList L;
+    __shared__ MoeMasks X;
     __shared__ float slot_w[kMaxPairs];
     __shared__ int16_t pair_slot[kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, C = A.C, G = A.down.G;
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
     uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
-    W w(A.down, A.down, 16, base + warp * W::kRing, base + kMoeWarps * W::kRing + warp * W::side(G),
-        sm_addr(base + kMoeWarps * (W::kRing + W::side(G))) + warp * W::kBars, A);
+    W w(A.down, A.down, 16, base + warp * W::kRing, base + kMoeWarps * W::kRing + warp * W::kSide,
+        sm_addr(base + kMoeWarps * (W::kRing + W::kSide)) + warp * W::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
     // the kernel before waited for its inputs: ids and weights are final, only h is not
-    build_list<8 * NS>(L, A);
+    build_list<8 * NS>(L, X, A);
     float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
-    const int step = C * kMoeWarps, KS = down_slices(G, step, L.blocks, L.slots, A.zrows), tasks = L.blocks * KS;
+    const int step = C * kMoeWarps, KS = down_split(G, step, L.blocks, L.slots, A.zrows).slices, tasks = L.blocks * KS;
     const int q0 = rank * kMoeWarps + warp;
     int pq = q0;  // the next task to request
     auto feed = [&]() {
@@ -699,7 +688,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
         int slot = -1;
         if (e >= 0 && e < A.E) {
             const uint32_t below = (1u << (tok & 31)) - 1u;
-            slot = L.first[e] + (tok < 32 ? __popc(L.mask[0][e] & below) : __popc(L.mask[0][e]) + __popc(L.mask[1][e] & below));
+            slot = X.first[e] + (tok < 32 ? __popc(X.mask[0][e] & below) : __popc(X.mask[0][e]) + __popc(X.mask[1][e] & below));
             float v = A.weights[p];
             for (int q = tok * A.k; q < (tok + 1) * A.k; ++q)
                 if (q != p && A.ids[q] == e) {
@@ -797,25 +786,25 @@ __global__ void __launch_bounds__(kMoeThreads, 2) k_moe_down(const __grid_consta
 }
 
 // One split of the SM's memory for both kernels: with one of its own each, an SM is emptied and set up anew between them.
-cudaError_t shape_kernel(const void* fn) {
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+cudaError_t shape_kernel(const void* fn, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
-// A kernel, its shared memory for rows of G groups and its setup on the current device.
+// A kernel, its shared memory and its setup on the current device.
 struct MoeKernel {
     const void* fn;
-    int (*smem)(int G);
+    int smem;
     cudaError_t (*setup)();
 };
 template <int KG, int KU, int NS>
 cudaError_t up_setup() {
-    return once_per_device<MoeUp<KG, KU, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>)); });
+    return once_per_device<MoeUp<KG, KU, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), MoeUp<KG, KU, NS>::kSmem); });
 }
 template <int KG, int KU, int NS>
 MoeKernel up_of() {
-    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), &MoeUp<KG, KU, NS>::smem, &up_setup<KG, KU, NS>};
+    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), MoeUp<KG, KU, NS>::kSmem, &up_setup<KG, KU, NS>};
 }
 template <int NS>
 MoeKernel up_kernel(int kg, int ku) {
@@ -828,20 +817,45 @@ template <int KIND, int NS>
 struct DownOf;  // names a kernel
 template <int KIND, int NS>
 cudaError_t down_setup() {
-    return once_per_device<DownOf<KIND, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_down<KIND, NS>)); });
+    return once_per_device<DownOf<KIND, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), MoeDown<KIND>::kSmem); });
 }
 template <int KIND, int NS>
 MoeKernel down_of() {
-    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), &MoeDown<KIND>::smem, &down_setup<KIND, NS>};
+    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), MoeDown<KIND>::kSmem, &down_setup<KIND, NS>};
 }
 template <int NS>
 MoeKernel down_kernel(int kind) {
     static const MoeKernel table[3] = {down_of<0, NS>(), down_of<1, NS>(), down_of<2, NS>()};
     return table[kind];
 }
-// CTAs of so much shared memory on an SM: two by the kernels' registers, fewer by the SM's 228 KB (each CTA takes 1 KB
-// more, and up to 15 KB of static shared memory)
-int ctas_per_sm(int smem) { return std::max(1, std::min(2, (228 * 1024) / (smem + 16 * 1024))); }
+// Clusters of c CTAs that the device holds at once.  They stay within a group of SMs, and what is left over in each
+// group stays empty: 71 clusters of four, not 74; a 72nd doubled the kernel's time.
+int64_t clusters_at_once(const MoeKernel& kernel, int c, int sms) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (c == 1) return (int64_t)sms * kCtasPerSM;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][c].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)c;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)(c * sms));
+        cfg.blockDim = dim3(kMoeThreads);
+        cfg.dynamicSmemBytes = (size_t)kernel.smem;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel.fn, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        known[dev][c].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K) {
     TensorMapEncodeFn enc = tensor_map_encoder();
@@ -912,27 +926,30 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     const int NS = T * k > 5 * E ? 2 : 1;
     const MoeKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
     const MoeKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
-    const int up_smem = ku.smem(A.gate.G), down_smem = kd.smem(A.down.G);
-    if (up_smem > 160 * 1024 || down_smem > 160 * 1024) return cudaErrorInvalidConfiguration;
     cudaError_t e = ku.setup();
     if (e != cudaSuccess) return e;
     e = kd.setup();
     if (e != cudaSuccess) return e;
-    const int per_sm = ctas_per_sm(up_smem), down_per_sm = ctas_per_sm(down_smem);
-    // CTAs per cluster of the down kernel: the count whose waves, each as long as a warp's share of the blocks that
-    // the tokens are expected to fill (in sixteenths of a block), end first
-    const double filled = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T)) + T * k / (16.0 * NS);
-    double best = 0;
+    // CTAs per cluster of the down kernel: the count whose waves end first (in groups of a warp, about 0.6 us: a wave costs
+    // its warps' share of the blocks that the tokens are expected to fill and four more, a cluster's barrier three, each
+    // of its CTAs a half).  Over 120 layers of the supported range within 2.4 % of the best count of each; always two
+    // loses 8 %, always four 13 %.
+    const double taken = E * (1.0 - std::pow(1.0 - std::min(1.0, (double)k / E), T));  // experts
+    const double filled = taken + std::max(0.0, (T * k - taken * 4 * NS) / (8 * NS));  // blocks: more from half of one on
+    int64_t best = INT64_MAX;
     for (int c = 1; c <= 8; ++c) {
-        const int64_t waves = (H / kDownRows * c + (int64_t)sms * down_per_sm - 1) / ((int64_t)sms * down_per_sm);
-        const double cost = (double)waves * (std::ceil(16 * filled / (c * kMoeWarps)) + 4);
-        if (c == 1 || cost < best) {
+        const int64_t held = clusters_at_once(kd, c, sms);
+        if (held < 1) continue;
+        const int64_t waves = (H / kDownRows + held - 1) / held;
+        const int share = down_split((int)(I / kGroup), c * kMoeWarps, std::max(1, (int)(filled + 0.5)), T * k, A.zrows).cost;
+        const int64_t cost = 2 * waves * (share + 4) + (c > 1 ? 6 : 0) + c;
+        if (cost < best) {
             best = cost;
             A.C = c;
         }
     }
     // no more CTAs than the units that the pairs can make at most
-    const int64_t ctas = std::min<int64_t>((int64_t)std::min(T * k, E + T * k / 8) * (I / 16), (int64_t)sms * per_sm);
+    const int64_t ctas = std::min<int64_t>((int64_t)std::min(T * k, E + T * k / 8) * (I / 16), (int64_t)sms * kCtasPerSM);
 
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
@@ -942,7 +959,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     cfg.stream = st;
     cfg.blockDim = dim3(kMoeThreads);
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.dynamicSmemBytes = (size_t)up_smem;
+    cfg.dynamicSmemBytes = (size_t)ku.smem;
     // (the up kernel begins before the work in front of it has ended and waits for it before its first read)
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -952,7 +969,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
     cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = (size_t)down_smem;
+    cfg.dynamicSmemBytes = (size_t)kd.smem;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)A.C;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
