@@ -53,10 +53,9 @@ constexpr int kABytes = kRows * kChunkK / 2;
 template <int NT_, int STAGES_, int EPI_>
 struct MxCfg {
     static constexpr int NT = NT_, STAGES = STAGES_, EPI = EPI_;
-    static constexpr int NB = NT > 128 ? 2 : 1;  // 128-row scale tiles of X per unit
     static constexpr int kB = NT * kChunkK / 2;
-    static constexpr int kStage = kABytes + kB + 1024 + 1024 * NB;
-    static constexpr int kSfCols = 8 + 8 * NB;  // per stage: W's two tiles of 4 columns, X's
+    static constexpr int kStage = kABytes + kB + 2048;
+    static constexpr int kSfCols = 16;  // per stage: W's two tiles of 4 columns, X's
     static constexpr int kDCols = NT < 32 ? 32 : NT;
     static constexpr int kCols = kDCols + STAGES * kSfCols;
     static constexpr int kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
@@ -71,6 +70,7 @@ struct MxCfg {
 using Mx16 = MxCfg<16, 4, 4>;
 using Mx32 = MxCfg<32, 4, 8>;
 using Mx64 = MxCfg<64, 3, 8>;
+using Mx64Alone = MxCfg<64, 7, 8>;  // with an SM to itself: 61 rows x 17408 x 5120 14.7 -> 12.8 us
 using Mx128 = MxCfg<128, 4, 8>;
 
 constexpr float kMxNaN = __builtin_nanf("");
@@ -105,7 +105,7 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_constant__ MxArgs A, int S) {
-    constexpr int NT = C::NT, ST = C::STAGES, NB = C::NB;
+    constexpr int NT = C::NT, ST = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], dfull, dfree;
     __shared__ uint32_t tmem_sh;
@@ -157,16 +157,12 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
                     }
                     const uint32_t st = base + s * C::kStage, bar = sm_addr(&full[s]);
                     const uint32_t sfb = 512u * (uint32_t)min(2, A.KT - 2 * c);  // bytes of a row tile's scales
-                    const bool two = NB == 2 && (int64_t)b * NT + 128 < A.M;
-                    mb_arrive_expect(bar, (uint32_t)(kABytes + C::kB) + sfb * (two ? 3u : 2u));
+                    mb_arrive_expect(bar, (uint32_t)(kABytes + C::kB) + 2u * sfb);
                     tma_load_2d(st, &A.wmap, c * (kChunkK / 2), (int)(t * kRows), bar);
                     tma_load_2d(st + kABytes, &A.xmap, c * (kChunkK / 2), (int)(b * NT), bar);
                     bulk_load(st + kABytes + C::kB, A.wsf + ((int64_t)t * A.KT + 2 * c) * 512, sfb, bar);
                     bulk_load(st + kABytes + C::kB + 1024,
-                              A.xsf + ((int64_t)(b * (uint32_t)NT / 128u) * A.KT + 2 * c) * 512, sfb, bar);
-                    if (two)
-                        bulk_load(st + kABytes + C::kB + 2048,
-                                  A.xsf + ((int64_t)(b * (uint32_t)NT / 128u + 1) * A.KT + 2 * c) * 512, sfb, bar);
+                              A.xsf + ((int64_t)b * A.KT + 2 * c) * 512, sfb, bar);
                     ++issued;
                 }
             }
@@ -194,16 +190,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
                     for (int kt = 0; kt < 2; ++kt)
                         if (kt * 2 < nk) {
                             cp_scales(ta + kt * 4, desc_scales(sf + kt * 512));
-#pragma unroll
-                            for (int nb = 0; nb < NB; ++nb)
-                                cp_scales(tb + kt * 4 * NB + nb * 4, desc_scales(sf + 1024 + nb * 1024 + kt * 512));
+                            cp_scales(tb + kt * 4, desc_scales(sf + 1024 + kt * 512));
                         }
                     const uint64_t da = desc_sw128(sa), db = desc_sw128(sb);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (j < nk)
                             mma_mx(tmem, da + 2 * j, db + 2 * j, mx_idesc(NT, 2 * (j & 1)), ta + (j >> 1) * 4,
-                                   tb + (j >> 1) * 4 * NB, (c > c0 || j > 0) ? 1u : 0u);
+                                   tb + (j >> 1) * 4, (c > c0 || j > 0) ? 1u : 0u);
                     tc5_commit_one(sm_addr(&empty[s]));
                     ++committed;
                     if (++s == ST) {
@@ -571,22 +565,30 @@ bool encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class C>
-cudaError_t launch(MxArgs& A, int64_t units, cudaStream_t st, int sms) {
-    // CTAs per unit.  A chunk takes a CTA about 0.32 us; adding a cluster's partial sums about 0.6 us and 0.04 us per
-    // column of the unit (measured: 4096 x 4096, M = 1: 8.8 / 6.8 / 5.5 us with 1 / 2 / 4 CTAs, M = 61: 9.4 / 10.4 /
-    // 7.9 us), and clusters that do not all fit one CTA per SM lose more than they gain (8 CTAs: 7.1 and 10.3 us).
-    int S = 1;
-    int64_t best = -1;
-    for (int s = 1; s <= 8 && s <= A.KC; s *= 2) {
-        if (s > 1 && units * s > sms) break;
-        const int64_t slots = (int64_t)sms * C::per_sm(s);
-        const int64_t cost = (units * s + slots - 1) / slots * ((A.KC + s - 1) / s) + (s > 1 ? 2 + C::NT / 8 : 0);
-        if (best < 0 || cost < best) {
-            best = cost;
-            S = s;
+// CTAs that share a unit's K.  In chunks of one CTA, about 0.32 us (measured on one to 4000 rows of products from
+// 100 x 200 to 17408 x 17408): a chunk takes 1.7 times as long for each of two CTAs that share an SM; a cluster costs three
+// more, one per 8 batch rows for adding the partial sums and a quarter per CTA (clusters of eight only where each CTA has an
+// SM of its own).  4096 x 4096, one row: 8.5 / 6.9 / 5.5 / 7.1 us with 1 / 2 / 4 / 8 CTAs; 17408 x 5120, 61 rows: 12.8 with
+// one, 18.5 with two; 5120 x 17408, 61 rows: 26.7 / 19.4 / 18.5 with 1 / 2 / 4.
+int split_of(int nt, int64_t units, int KC, int sms) {
+    const int per_sm = nt < 128 ? 2 : 1;
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= 8 && s <= KC; s *= 2) {
+        if (s > 1 && units * s > (s < 8 ? per_sm : 1) * (int64_t)sms) break;
+        const double share = units * s > sms && per_sm > 1 ? 1.7 : 1.0;
+        const double rounds = (double)((units * s + (int64_t)sms * per_sm - 1) / ((int64_t)sms * per_sm));
+        const double cost = rounds * ((KC + s - 1) / s) * share + (s > 1 ? 3 + nt / 8.0 + s / 4.0 : 0.0);
+        if (cost < least) {
+            least = cost;
+            best = s;
         }
     }
+    return best;
+}
+
+template <class C>
+cudaError_t launch(MxArgs& A, int64_t units, int S, cudaStream_t st, int sms) {
     const int64_t ctas = S > 1 ? units * S : std::min<int64_t>(units, (int64_t)sms * C::per_sm(1));
     A.units = (uint32_t)units;
     const void* fn = reinterpret_cast<const void*>(&k_mx4_gemm<C>);
@@ -684,16 +686,17 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
     A.KT = (int32_t)((K + 127) / 128);
     A.ydt = ydt;
     A.stall = stall ? 1 : 0;
-    const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+    const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));  // below 128 a unit has all batch rows
     A.MB = (int32_t)((M + nt - 1) / nt);
     const int64_t units = T * A.MB;
     if (units > 0x7FFFFFFF || !encode_codes(&A.wmap, w, N, K, kRows) || !encode_codes(&A.xmap, x, M, K, nt))
         return cudaErrorInvalidValue;
+    const int S = split_of(nt, units, A.KC, sms);
     switch (nt) {
-        case 16: return launch<Mx16>(A, units, st, sms);
-        case 32: return launch<Mx32>(A, units, st, sms);
-        case 64: return launch<Mx64>(A, units, st, sms);
-        default: return launch<Mx128>(A, units, st, sms);
+        case 16: return launch<Mx16>(A, units, S, st, sms);
+        case 32: return launch<Mx32>(A, units, S, st, sms);
+        case 64: return units * S <= sms ? launch<Mx64Alone>(A, units, S, st, sms) : launch<Mx64>(A, units, S, st, sms);
+        default: return launch<Mx128>(A, units, S, st, sms);
     }
 }
 

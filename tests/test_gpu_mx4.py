@@ -330,3 +330,12 @@ def test_gemm_outputs_past_four_gigabytes():
             ref = a[r] @ b[c].T
             tol = (K / 64 + 12) * 2.0 ** -23 * (np.abs(a[r]) @ np.abs(b[c]).T) + 2.0 ** -8 * np.abs(ref)
             assert np.all(np.abs(Y[r, c].double().cpu().numpy() - ref) <= tol)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 5120, 8704), (61, 5120, 8704), (64, 9600, 2272), (40, 19200, 544), (33, 128, 17408)])
+def test_gemm_rings_and_splits(M, N, K):
+    """Long K: rings that go round several times, in units of an SM each and of two to an SM, whole and split."""
+    rng = np.random.default_rng(M + N)
+    w, ws = R.random_mx4(N, K, rng)
+    x, xs = R.random_mx4(M, K, rng)
+    check_gemm(w, ws, x, xs)
