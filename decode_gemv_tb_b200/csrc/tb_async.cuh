@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cstring>
 
 namespace tb {
 
@@ -95,6 +96,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// after pdl_wait, before a copy of what an earlier kernel's plain stores wrote
+__device__ __forceinline__ void fence_copies() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // shared -> global; rows and columns past the tensor are not written
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
@@ -179,6 +183,27 @@ cudaError_t once_per_device(F set) {
     e = set();
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
+}
+// A launch, in clusters of `cluster` CTAs where that is above 1, that may begin while the work in front of it in the stream
+// still runs: the kernel waits for it (pdl_wait) before its first access to memory.  Kernels launched so let the next one
+// begin early too (pdl_trigger), which takes about a microsecond off every boundary between them.
+inline cudaError_t launch_early(const void* fn, int64_t grid, int block, size_t smem, int cluster, void** args, cudaStream_t st) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute at[2];
+    std::memset(at, 0, sizeof(at));
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 typedef CUresult (*TensorMapEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_up(const __grid
                       M::kBoth ? 0u : bars + M::Gate::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
+    fence_copies();
     build_list<8 * NS>(L, *reinterpret_cast<MoeMasks*>(part), A);
     pdl_trigger();
 
@@ -665,7 +666,8 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_down(const __gr
         sm_addr(base + kMoeWarps * (W::kRing + W::kSide)) + warp * W::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
-    // the kernel before waited for its inputs: ids and weights are final, only h is not
+    // the kernel before waited for its inputs: ids, weights and the experts are final, only h is not
+    fence_copies();
     build_list<8 * NS>(L, X, A);
     float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
     const int step = C * kMoeWarps, KS = down_split(G, step, L.blocks, L.slots, A.zrows).slices, tasks = L.blocks * KS;
@@ -951,30 +953,10 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     // no more CTAs than the units that the pairs can make at most
     const int64_t ctas = std::min<int64_t>((int64_t)std::min(T * k, E + T * k / 8) * (I / 16), (int64_t)sms * kCtasPerSM);
 
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute at[2];
-    std::memset(at, 0, sizeof(at));
-    cfg.attrs = at;
-    cfg.stream = st;
-    cfg.blockDim = dim3(kMoeThreads);
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.dynamicSmemBytes = (size_t)ku.smem;
-    // (the up kernel begins before the work in front of it has ended and waits for it before its first read)
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
     void* args[] = {&A};
-    e = cudaLaunchKernelExC(&cfg, ku.fn, args);
+    e = launch_early(ku.fn, ctas, kMoeThreads, (size_t)ku.smem, 1, args, st);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(H / kDownRows * A.C));
-    cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = (size_t)kd.smem;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)A.C;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelExC(&cfg, kd.fn, args);
+    return launch_early(kd.fn, H / kDownRows * A.C, kMoeThreads, (size_t)kd.smem, A.C, args, st);
 }
 
 unsigned int take_moe_timeouts() {

@@ -114,7 +114,7 @@ constexpr int kRtWarps = 16;
 constexpr int kRtThreads = kRtWarps * 32;
 
 template <int TB>
-__global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(rt_cluster(TB), 1, 1) k_moe_route(const RouteArgs A) {
+__global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) {
     constexpr int kRtCluster = rt_cluster(TB);
     extern __shared__ __align__(16) uint8_t smem[];
     double* logits = reinterpret_cast<double*>(smem);                 // [E]: of this CTA's token
@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(rt_cluster(TB)
     const int64_t t0 = (int64_t)(blockIdx.x / kRtCluster) * TB;
     const int nt = (int)min((int64_t)TB, A.T - t0);
     cluster_arrive();
+    pdl_trigger();
+    pdl_wait();
     const int H8 = A.H / 8;  // eights of x: their first four words in one plane, the others in a second
     for (int i0 = threadIdx.x; i0 < TB * H8; i0 += 4 * kRtThreads) {
         uint4 v[4];
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(rt_cluster(TB)
             for (int q = 0; q < U; ++q)
 #pragma unroll
                 for (int b = 0; b < EB; ++b)
-                    next[q][b] = h0 + 32 * q < H8 ? __ldg(w[b] + h0 + 32 * q) : make_uint4(0u, 0u, 0u, 0u);
+                    next[q][b] = h0 + 32 * q < H8 ? w[b][h0 + 32 * q] : make_uint4(0u, 0u, 0u, 0u);
         };
         load(lane);
         for (int h0 = lane; h0 < H8; h0 += 32 * U) {
@@ -232,14 +234,15 @@ __global__ void __launch_bounds__(kRtThreads, 1) __cluster_dims__(rt_cluster(TB)
 size_t route_smem(int TB, int E, int H) { return (size_t)8 * ((E + 1) & ~1) + (size_t)TB * H * 4; }
 
 template <int TB>
-cudaError_t launch(const RouteArgs& A, cudaStream_t st) {
+cudaError_t launch(RouteArgs& A, cudaStream_t st) {
     const size_t smem = route_smem(TB, A.E, A.H);
     const cudaError_t e = once_per_device<std::integral_constant<int, TB>>([] {
         return cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
     });
     if (e != cudaSuccess) return e;
-    k_moe_route<TB><<<(unsigned)((A.T + TB - 1) / TB) * rt_cluster(TB), kRtThreads, smem, st>>>(A);
-    return cudaGetLastError();
+    void* args[] = {&A};
+    return launch_early(reinterpret_cast<const void*>(&k_moe_route<TB>), (int64_t)((A.T + TB - 1) / TB) * rt_cluster(TB),
+                        kRtThreads, smem, rt_cluster(TB), args, st);
 }
 
 }  // namespace

@@ -50,9 +50,10 @@ struct QuantArgs {
     int32_t own_bad;    // the only CTA: it writes the count itself
 };
 
-// The count that the quantiser adds to, set to 0 while that kernel already runs.
+// The count that the quantiser adds to, set to 0.
 __global__ void k_mx4_zero(int32_t* bad) {
     pdl_trigger();
+    pdl_wait();
     *bad = 0;
 }
 
@@ -64,6 +65,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     int bad = 0;
+    pdl_trigger();
+    pdl_wait();
     if (id < A.warps) {
         const int64_t row = A.warps <= 0x7FFFFFFF ? (uint32_t)id / A.pieces : id / A.pieces;
         const int64_t k0 = (id - row * A.pieces) * (S * kLoads) + lane * V;
@@ -138,7 +141,6 @@ __global__ void __launch_bounds__(kThreads) k_mx4_quantize(const QuantArgs A) {
                 *A.bad = t;
             }
         } else {
-            pdl_wait();  // the count is 0
             if ((threadIdx.x & 31) == 0 && bad) atomicAdd(A.bad, bad);  // of integers: the order does not matter
         }
     }
@@ -158,6 +160,8 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
     constexpr int S = 32 * V;              // values of a warp's store
     const int lane = threadIdx.x & 31;
     const int64_t id = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    pdl_trigger();
+    pdl_wait();
     if (id >= A.warps) return;
     const int64_t row = A.warps <= 0x7FFFFFFF ? (uint32_t)id / A.pieces : id / A.pieces;
     const int64_t k0 = (id - row * A.pieces) * (S * kStores) + lane * V;
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_mx4_dequantize(const DequantArgs A
         const bool in = i * S < left;
         if constexpr (DT == kF32) c[i] = in ? __ldcs(reinterpret_cast<const uint16_t*>(codes + i * (S / 2))) : 0u;
         else c[i] = in ? __ldcs(reinterpret_cast<const uint32_t*>(codes + i * (S / 2))) : 0u;
-        e[i] = in ? __ldg(scale + i * (S / 128) * 512) : 0u;
+        e[i] = in ? scale[i * (S / 128) * 512] : 0u;
     }
 #pragma unroll
     for (int i = 0; i < kStores; ++i) {
@@ -222,24 +226,15 @@ cudaError_t launch_mx4_quantize(const void* W, int w_dtype, int64_t ldw, int64_t
     const int64_t blocks = (A.warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     A.own_bad = blocks == 1;
-    const bool zero = bad && blocks > 1;
-    if (zero) k_mx4_zero<<<1, 1, 0, st>>>(bad);
-    // with a count to be set to 0 the quantiser begins beside that kernel (which began after all work in front of it)
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = zero ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
+    if (bad && blocks > 1) {
+        void* args[] = {&bad};
+        const cudaError_t e = launch_early(reinterpret_cast<const void*>(&k_mx4_zero), 1, 1, 0, 1, args, st);
+        if (e != cudaSuccess) return e;
+    }
     void* args[] = {&A};
-    return cudaLaunchKernelExC(&cfg,
-                               w_dtype == kF32 ? reinterpret_cast<const void*>(&k_mx4_quantize<kF32>)
-                                               : reinterpret_cast<const void*>(&k_mx4_quantize<kBF16>),
-                               args);
+    return launch_early(w_dtype == kF32 ? reinterpret_cast<const void*>(&k_mx4_quantize<kF32>)
+                                        : reinterpret_cast<const void*>(&k_mx4_quantize<kBF16>),
+                        blocks, kThreads, 0, 1, args, st);
 }
 
 cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int64_t N, int64_t K, void* W,
@@ -256,9 +251,10 @@ cudaError_t launch_mx4_dequantize(const void* codes, const uint8_t* scales, int6
     A.warps = N * A.pieces;
     const int64_t blocks = (A.warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    if (w_dtype == kF32) k_mx4_dequantize<kF32><<<(unsigned)blocks, kThreads, 0, st>>>(A);
-    else k_mx4_dequantize<kBF16><<<(unsigned)blocks, kThreads, 0, st>>>(A);
-    return cudaGetLastError();
+    void* args[] = {&A};
+    return launch_early(w_dtype == kF32 ? reinterpret_cast<const void*>(&k_mx4_dequantize<kF32>)
+                                        : reinterpret_cast<const void*>(&k_mx4_dequantize<kBF16>),
+                        blocks, kThreads, 0, 1, args, st);
 }
 
 }  // namespace tb

@@ -140,6 +140,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_consta
     __syncthreads();
     tc5_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
+    pdl_trigger();
+    pdl_wait();
+    fence_copies();
     int issued = 0, committed = 0;
 
     if (warp == 0) {
@@ -383,6 +386,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) k_mx4_prefill(const __grid_con
     __syncthreads();
     tc5_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_sh, 0);
+    pdl_trigger();
+    pdl_wait();
+    fence_copies();
     int issued = 0;
 
     if (warp == 0) {
@@ -597,20 +603,8 @@ cudaError_t launch(MxArgs& A, int64_t units, int S, cudaStream_t st, int sms) {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2));
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     void* args[] = {&A, &S};
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return launch_early(fn, ctas, C::kThreads, (size_t)smem, S, args, st);
 }
 
 // outputs: rows of N, boxes of 128 bytes x 128 rows
@@ -641,8 +635,9 @@ cudaError_t launch_prefill(PreArgs& A, const void* w, const void* x, int64_t K, 
         return cudaFuncSetAttribute(k_mx4_prefill<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess) return e;
-    k_mx4_prefill<C><<<(unsigned)std::min<int64_t>(units, sms), kPreThreads, C::kSmem, st>>>(A);
-    return cudaGetLastError();
+    void* args[] = {&A};
+    return launch_early(reinterpret_cast<const void*>(&k_mx4_prefill<C>), std::min<int64_t>(units, sms), kPreThreads, C::kSmem, 1,
+                        args, st);
 }
 
 }  // namespace

@@ -450,3 +450,44 @@ def test_moe_experts_past_four_gigabytes():
     # every other expert is 0: the rest of the layer does not count
     ref, tol = R.moe(*mats, 1, x, torch.tensor([[0, -1], [-1, 0]], dtype=torch.int32), w)
     assert torch.all((y.double() - ref).abs() <= tol) and ref.abs().max() > 0
+
+
+def test_experts_requantised_between_calls():
+    """Layers whose 4-bit experts are quantised into the same buffers right before each call, and whose router reads
+    what the layer before wrote: nothing is read before it is final."""
+    g = torch.Generator().manual_seed(32)
+    T, E, k, H, I, depth = 5, 6, 2, 256, 128, 6
+    W = [[torch.randn((E * r, c), generator=g).mul_(0.1).to(torch.bfloat16).to(DEV) for r, c in ((I, H), (I, H), (H, I))]
+         for _ in range(depth)]
+    R_ = torch.randn((depth, E, H), generator=g).to(torch.bfloat16).to(DEV)
+    x0 = torch.randn((T, H), generator=g).to(torch.bfloat16).to(DEV)
+    x = x0
+    for i in range(depth):  # one by one
+        layer = tb.moe_layer(*((*tb.tb_mx4_quantize(w), tb.MX4) for w in W[i]), E, H, I)
+        x = tb.tb_moe(layer, x, *tb.tb_moe_route(x, R_[i], k), out_dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+    assert torch.isfinite(x).all() and x.abs().max() > 0
+    codes = [tb.tb_mx4_quantize(w) for w in W[0]]
+    layer = tb.moe_layer(*((*c, tb.MX4) for c in codes), E, H, I)
+    ws = tb.workspace(tb.moe_workspace_bytes(layer, T, k), DEV)
+    ids, wt = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    buf = [x0.clone(), torch.empty_like(x0)]
+
+    def run():
+        for i in range(depth):
+            for w, (c, s) in zip(W[i], codes):
+                tb.tb_mx4_quantize(w, codes=c, scales=s)
+            tb.tb_moe_route(buf[i & 1], R_[i], k, ids=ids, weights=wt)
+            tb.tb_moe(layer, buf[i & 1], ids, wt, y=buf[~i & 1], ws=ws)
+
+    for _ in range(4):
+        buf[0].copy_(x0)
+        run()
+        assert torch.equal(buf[depth & 1], x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(4):
+        buf[0].copy_(x0)
+        graph.replay()
+        assert torch.equal(buf[depth & 1], x)

@@ -339,3 +339,44 @@ def test_gemm_rings_and_splits(M, N, K):
     w, ws = R.random_mx4(N, K, rng)
     x, xs = R.random_mx4(M, K, rng)
     check_gemm(w, ws, x, xs)
+
+
+def test_chains_without_waits():
+    """Calls that begin while the one before still runs: activations quantised into one buffer again and again, each
+    batch multiplied and restored before the next overwrites it; eagerly and in a graph, the same bits as one by one."""
+    g = torch.Generator().manual_seed(16)
+    N, K, n = 2048, 2048, 12
+    wc, ws = tb.tb_mx4_quantize(torch.randn((N, K), generator=g).to(DEV))
+    for M in (1, 40, 300):
+        X = torch.randn((n, M, K), generator=g).to(torch.bfloat16).to(DEV)
+        want, back = [], []
+        for i in range(n):
+            xc, xs = tb.tb_mx4_quantize(X[i])
+            want.append(tb.tb_mx4_gemm(wc, ws, xc, xs, M, N, K))
+            back.append(tb.tb_mx4_dequantize(xc, xs, M, K))
+            torch.cuda.synchronize()
+        xc, xs = torch.empty_like(xc), torch.empty_like(xs)
+        bad = torch.empty(1, dtype=torch.int32, device=DEV)
+        Y, B = torch.empty((n, M, N), device=DEV), torch.empty((n, M, K), dtype=torch.bfloat16, device=DEV)
+
+        def run():
+            for i in range(n):
+                tb.tb_mx4_quantize(X[i], codes=xc, scales=xs, bad_count=bad)
+                tb.tb_mx4_gemm(wc, ws, xc, xs, M, N, K, Y=Y[i])
+                tb.tb_mx4_dequantize(xc, xs, M, K, W=B[i])
+
+        def check():
+            assert all(torch.equal(Y[i], want[i]) and torch.equal(B[i], back[i]) for i in range(n))
+
+        for _ in range(4):
+            Y.fill_(-1), B.fill_(-1)
+            run()
+            check()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(4):
+            Y.fill_(-1), B.fill_(-1)
+            graph.replay()
+            check()
+    assert tb.sync_status() == 0
