@@ -4,9 +4,16 @@
 //     h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   y[t] = sum_j w[t,j] Wd[ids[t,j]] h[t,ids[t,j]]
 //
 // Every expert that some token takes is read once per eight or sixteen of its
-// tokens:
-// with few tokens the layer is bound by the bytes of the experts it touches
-// and by decoding them.
+// tokens: the layer would be bound by the bytes of the experts it touches, and
+// is by the instructions that decode them, at 16 warps per SM (128 registers):
+// 64 tokens x 128 experts of 4096 x 1536 in MX4 419 us (3.0 TB/s of codes; byte
+// floor 193), issue slots 64 % and the ALU pipe 62 % busy in the up kernel; 16
+// tokens x 64 experts of 2048 x 1408 in 2 and 3 bits 64 us (floor 19); one
+// token x 8 of 128 experts of 2048 x 768, ternary, 13.8 us (floor 1.5), of
+// which two launches, the expert lists and the first copies take about 10.
+// A 16 x 128 tile takes a scheduler 153 (2 bits), 178 (3 bits) and 262 cycles
+// (MX4), 64 of them its MMAs; HBM delivers one in 93, 137
+// and 187.
 //
 // Both kernels group the (token, choice) pairs by expert themselves, in
 // shared memory (a 64-bit token mask per expert, a prefix sum over the
@@ -22,15 +29,17 @@
 // stream through a private ring per warp, filled by tensor copies of 16 rows
 // x 128 (144) bytes.  (With cp.async, 32 rows' scattered 16- and 4-byte
 // pieces per group, both kernels were bound by the L1's request rate: more
-// warps changed nothing, 64 tokens x 4-bit experts took 466 us.)
+// warps changed nothing, 64 tokens x 4-bit experts took 466 us when tensor
+// copies took 451.)
 //
 // h is rounded to bf16 between the two products, as tb_gate_up_silu's is: the
 // MMA's operand, and half the activations a second part would cost.
 //
 // k_moe_up: a unit is (block, 16 rows of gate and of up); S warps of a CTA
-// split K where that evens out the warps' shares.  k_moe_down: a cluster of C CTAs holds 64 rows
-// of H, its CTAs split the blocks; each warp adds its rows' results per
-// token in shared memory, the ranks are added in order (deterministic).
+// split K where that evens out the warps' shares.  k_moe_down: a cluster of C
+// CTAs holds 32 rows of H and deals the blocks, cut into slices of K where
+// that evens out the shares, to its warps; each writes its weighted results
+// to the workspace, and the cluster adds a token's in order (deterministic).
 #include "tb_async.cuh"
 #include "tb_device.cuh"
 #include "tb_internal.h"

@@ -4,17 +4,27 @@
 //     Y[m][n] = sum over blocks b of 32 k:  Sw[n][b] Sx[m][b] sum_{k in b} w[n][k] x[m][k]
 //
 // The MMA reads the packed nibbles and the scale bytes as they are stored:
-// nothing is decoded, so a batch of one streams W at the copy engine's pace
+// nothing is decoded, so a small batch streams W at the copy engine's pace
 // and a prefill batch runs at the 4-bit rate.  Every product is exact; the
 // sums are the MMA's fp32 accumulation.
 //
-// Work.  The weights are the MMA's A (128 rows of W, so a few batch rows
-// waste no tensor rows) and the batch its B (NT = 16 .. 256 rows of X).  A
-// unit is (128 rows of W, NT rows of X); K goes by chunks of 256 (128-byte
-// rows, the swizzle span).  Units too few for the GPU split their chunks
-// over a cluster of S CTAs, which add their partial sums through distributed
-// shared memory in rank order (deterministic; no workspace, no spinning on
-// global memory); enough units run persistently, S = 1.
+// k_mx4_gemm, small batches and outputs that tensor stores cannot write.  The
+// weights are the MMA's A (128 rows of W, so a few batch rows waste no tensor
+// rows) and the batch its B (NT = 16 .. 128 rows of X).  A unit is (128 rows
+// of W, NT rows of X); K goes by chunks of 256 (128-byte rows, the swizzle
+// span).  Units too few for the GPU split their chunks over a cluster of S
+// CTAs, which add their partial sums through distributed shared memory in
+// rank order (deterministic; no workspace, no spinning on global memory);
+// units enough run one after the other in persistent CTAs, S = 1.  Bound by
+// W's bytes and, below about 10 us, by the fixed parts (launch, first copy,
+// cluster sum, about 3 us): 4096 x 4096, one row, 4.6 us; 17408 x 5120, 61
+// rows, 11.6 us (4.1 TB/s of W; the byte floor is 7.6).
+// Below 128 rows a unit has all of them: the MMA takes X's scales from the
+// first column of a tile of 128 rows, and no unit may begin inside one.
+//
+// k_mx4_prefill, whole tiles of large batches: below.  17408 x 5120, 4096
+// rows: 162 us, 4.5 PFLOP/s (2.7 times the measured bf16 rate), the tensor
+// pipe busy 56 % of the time.
 //
 // A CTA: a producer warp (per chunk two tensor copies, W and X, 128-byte
 // swizzled, and bulk copies of the scale tiles), an MMA warp (scale tiles
