@@ -932,9 +932,10 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     A.I = (int32_t)I;
     A.ydt = ydt;
     A.hperm = A.down.kind == 2 ? 1 : 0;
-    // Sets of eight columns that share a decode: one while an expert's tokens seldom exceed eight, else two (a second
-    // set costs about a tenth of a product, a second decode a whole one)
-    const int NS = T * k > 5 * E ? 2 : 1;
+    // Sets of eight columns that share a decode: one up to ten pairs per expert, then two.  (The second set's activations
+    // take the registers of the prefetch, so it pays late: over 130 layers of the supported range two are 5 to 25 %
+    // slower below six pairs per expert, even at nine, 5 to 20 % faster above twenty.)
+    const int NS = T * k > 10 * E ? 2 : 1;
     const MoeKernel ku = NS == 1 ? up_kernel<1>(A.gate.kind, A.up.kind) : up_kernel<2>(A.gate.kind, A.up.kind);
     const MoeKernel kd = NS == 1 ? down_kernel<1>(A.down.kind) : down_kernel<2>(A.down.kind);
     cudaError_t e = ku.setup();
