@@ -7,6 +7,7 @@ missing or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -306,6 +307,12 @@ def _same_device(first: torch.Tensor, *rest) -> int:
     return dev
 
 
+def _allocating(stream: int | None):
+    """What is allocated for a call on `stream` belongs to that stream: its memory is not one that other work still uses,
+    and is not given to other work while the call runs."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(torch.cuda.ExternalStream(stream))
+
+
 def _bytes(t: torch.Tensor, name: str, need: int) -> int:
     if t.dtype != torch.uint8 or t.numel() < need:
         raise TBError(f"{name} must hold at least {need} bytes as uint8")
@@ -335,10 +342,11 @@ def tb_mx4_quantize(W: torch.Tensor, codes: torch.Tensor | None = None, scales: 
     if codes is None or scales is None:
         N, K = W.shape
         _, ns = _mx4_sizes(N, K)
-        if codes is None:
-            codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-        if scales is None:
-            scales = torch.empty(ns, dtype=torch.uint8, device=W.device)
+        with _allocating(stream):
+            if codes is None:
+                codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+            if scales is None:
+                scales = torch.empty(ns, dtype=torch.uint8, device=W.device)
     _bind.mx4_quantize(W, codes, scales, bad_count, stream)
     return codes, scales
 
@@ -349,7 +357,8 @@ def tb_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int,
     load()
     if W is None:
         _mx4_sizes(N, K)
-        W = torch.empty((N, K), dtype=out_dtype, device=codes.device)
+        with _allocating(stream):
+            W = torch.empty((N, K), dtype=out_dtype, device=codes.device)
     _bind.mx4_dequantize(codes, scales, N, K, W, stream)
     return W
 
@@ -360,7 +369,8 @@ def tb_mx4_gemm(w_codes: torch.Tensor, w_scales: torch.Tensor, x_codes: torch.Te
     """Y [M][N] = X W^T of two MX4 tensors (N rows of W, M rows of X, K columns)."""
     load()
     if Y is None:
-        Y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
+        with _allocating(stream):
+            Y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
     _bind.mx4_gemm(w_codes, w_scales, x_codes, x_scales, M, N, K, Y, flags, stream)
     return Y
 
@@ -375,10 +385,12 @@ def tb_moe_route(x: torch.Tensor, router: torch.Tensor, k: int, renormalize: boo
     """x [T][H] (rows may be strided), router [E][H], both bf16 -> the k best experts of every token, ids [T][k]
     int32, and their softmax weights [T][k] fp32."""
     load()
-    if ids is None:
-        ids = torch.empty((x.shape[0], k), dtype=torch.int32, device=x.device)
-    if weights is None:
-        weights = torch.empty((x.shape[0], k), dtype=torch.float32, device=x.device)
+    if ids is None or weights is None:
+        with _allocating(stream):
+            if ids is None:
+                ids = torch.empty((x.shape[0], k), dtype=torch.int32, device=x.device)
+            if weights is None:
+                weights = torch.empty((x.shape[0], k), dtype=torch.float32, device=x.device)
     _bind.moe_route(x, router, k, renormalize, ids, weights, stream)
     return ids, weights
 
@@ -417,9 +429,11 @@ def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.T
            out_dtype=torch.float32, ws: torch.Tensor | None = None, flags: int = 0, stream: int | None = None) -> torch.Tensor:
     """y [T][H] = the routed experts' MLP of x [T][H] (bf16, rows may be strided), summed with the weights."""
     load()
-    if y is None:
-        y = torch.empty((ids.shape[0], layer.H), dtype=out_dtype, device=x.device)
-    if ws is None:
-        ws = workspace(moe_workspace_bytes(layer, *ids.shape), x.device)
+    if y is None or ws is None:
+        with _allocating(stream):
+            if y is None:
+                y = torch.empty((ids.shape[0], layer.H), dtype=out_dtype, device=x.device)
+            if ws is None:
+                ws = workspace(moe_workspace_bytes(layer, *ids.shape), x.device)
     _bind.moe(layer.ptr, layer.H, layer.device, x, ids, weights, y, ws, flags, stream)
     return y

@@ -491,3 +491,32 @@ def test_experts_requantised_between_calls():
         buf[0].copy_(x0)
         graph.replay()
         assert torch.equal(buf[depth & 1], x)
+
+
+def test_calls_on_a_given_stream_allocate_there():
+    """A stream's address instead of the current stream: outputs and workspace that the call allocates are that stream's,
+    while the current one is busy with memory it has just freed."""
+    g = torch.Generator().manual_seed(33)
+    T, E, k, H, I = 6, 8, 2, 512, 256
+    mats, layer = make_layer(E, H, I, (2, 0, 4), 34)
+    x = torch.randn((T, H), generator=g).to(torch.bfloat16).to(DEV)
+    r = torch.randn((E, H), generator=g).to(torch.bfloat16).to(DEV)
+    want = tb.tb_moe(layer, x, *tb.tb_moe_route(x, r, k))
+    wc, ws = tb.tb_mx4_quantize(x)
+    wy, wv = tb.tb_mx4_gemm(wc, ws, wc, ws, T, T, H), tb.tb_mx4_dequantize(wc, ws, T, H)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    n = tb.moe_workspace_bytes(layer, T, k)
+    for _ in range(5):
+        busy = torch.empty(1 << 26, device=DEV)
+        for _ in range(4):
+            busy.fill_(1.0)  # the current stream is behind ...
+        for size in (n, T * H * 4, T * k * 4, 512 * 4, T * H // 2):
+            torch.empty(size, dtype=torch.uint8, device=DEV).fill_(255)  # ... with blocks that are free to allocate
+        s = side.cuda_stream
+        ids, w = tb.tb_moe_route(x, r, k, stream=s)
+        y = tb.tb_moe(layer, x, ids, w, stream=s)
+        c, t = tb.tb_mx4_quantize(x, stream=s)
+        Y, v = tb.tb_mx4_gemm(c, t, c, t, T, T, H, stream=s), tb.tb_mx4_dequantize(c, t, T, H, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(Y, wy) and torch.equal(v, wv) and torch.equal(c, wc)
