@@ -184,6 +184,36 @@ cudaError_t once_per_device(F set) {
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
+// Clusters of c <= 8 CTAs that the device holds at once, by kernels named K (as many CTAs per SM in all of them; asked once).
+// They stay within a group of SMs, and what is left over in each group stays empty: at two CTAs per SM 71 clusters of four,
+// not 74 -- a 72nd doubled a kernel's time.  0 on error.
+template <class K>
+int clusters_at_once(const void* fn, int block, size_t smem, int c) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][c].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute at[1];
+    std::memset(at, 0, sizeof(at));
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(c * 1024));
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[dev][c].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // A launch, in clusters of `cluster` CTAs where that is above 1, that may begin while the work in front of it in the stream
 // still runs: the kernel waits for it (pdl_wait) before its first access to memory.  Kernels launched so let the next one
 // begin early too (pdl_trigger), which takes about a microsecond off every boundary between them.

@@ -6,7 +6,7 @@
 // Every expert that some token takes is read once per eight or sixteen of its
 // tokens: the layer would be bound by the bytes of the experts it touches, and
 // is by the instructions that decode them, at 16 warps per SM (128 registers):
-// 64 tokens x 128 experts of 4096 x 1536 in MX4 419 us (3.0 TB/s of codes; byte
+// 64 tokens x 128 experts of 4096 x 1536 in MX4 421 us (3.0 TB/s of codes; byte
 // floor 193), issue slots 64 % and the ALU pipe 62 % busy in the up kernel; 16
 // tokens x 64 experts of 2048 x 1408 in 2 and 3 bits 64 us (floor 19); one
 // token x 8 of 128 experts of 2048 x 768, ternary, 13.8 us (floor 1.5), of
@@ -45,7 +45,6 @@
 #include "tb_internal.h"
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -839,35 +838,6 @@ MoeKernel down_kernel(int kind) {
     static const MoeKernel table[3] = {down_of<0, NS>(), down_of<1, NS>(), down_of<2, NS>()};
     return table[kind];
 }
-// Clusters of c CTAs that the device holds at once.  They stay within a group of SMs, and what is left over in each
-// group stays empty: 71 clusters of four, not 74; a 72nd doubled the kernel's time.
-int64_t clusters_at_once(const MoeKernel& kernel, int c, int sms) {
-    static std::atomic<int> known[64][9];
-    int dev = 0;
-    if (c == 1) return (int64_t)sms * kCtasPerSM;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    int n = known[dev][c].load(std::memory_order_relaxed);
-    if (n == 0) {
-        cudaLaunchConfig_t cfg;
-        std::memset(&cfg, 0, sizeof(cfg));
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)c;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        cfg.gridDim = dim3((unsigned)(c * sms));
-        cfg.blockDim = dim3(kMoeThreads);
-        cfg.dynamicSmemBytes = (size_t)kernel.smem;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel.fn, &cfg) != cudaSuccess || n < 1) {
-            (void)cudaGetLastError();
-            return 0;
-        }
-        known[dev][c].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
 bool make_mat(MoeMat* m, const MoeWeights& w, int64_t N, int64_t K) {
     TensorMapEncodeFn enc = tensor_map_encoder();
     if (!enc) return false;
@@ -950,7 +920,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     const double filled = taken + std::max(0.0, (T * k - taken * 4 * NS) / (8 * NS));  // blocks: more from half of one on
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8; ++c) {
-        const int64_t held = clusters_at_once(kd, c, sms);
+        const int64_t held = c == 1 ? (int64_t)sms * kCtasPerSM : clusters_at_once<MoeKernel>(kd.fn, kMoeThreads, (size_t)kd.smem, c);
         if (held < 1) continue;
         const int64_t waves = (H / kDownRows + held - 1) / held;
         const int share = down_split((int)(I / kGroup), c * kMoeWarps, std::max(1, (int)(filled + 0.5)), T * k, A.zrows).cost;

@@ -18,8 +18,8 @@
 // the tokens of the cluster.
 //
 // Bound by instructions, 4.7 per DFMA: 64 tokens x 256 experts x 4096 take
-// 17.4 us (issue slots 64 % busy; the DFMAs alone would take 3.7 us, the bytes
-// 0.4); one token x 128 experts x 2048 takes 4.7 us, mostly launch, the
+// 16.5 us (issue slots 64 % busy; the DFMAs alone would take 3.7 us, the bytes
+// 0.4); one token x 128 experts x 2048 takes 4.6 us, mostly launch, the
 // cluster's barriers and the selection.
 //
 // A cluster of CTAs handles TB tokens: its warps take two experts
@@ -31,7 +31,6 @@
 #include "tb_internal.h"
 
 #include <cstring>
-#include <type_traits>
 
 namespace tb {
 
@@ -42,6 +41,7 @@ struct RouteArgs {
     float* weights;     // [T][k]
     int64_t ldx;
     int32_t T, E, H, k, renorm;
+    int32_t C;  // CTAs of a cluster
 };
 
 namespace {
@@ -112,21 +112,18 @@ __device__ void select_experts(const double* l, const RouteArgs& A, int64_t t) {
     }
 }
 
-// CTAs of a cluster: eight finish one token soonest; the clusters of a batch have four, which the SM groups hold on more
-// SMs at once (64 tokens x 256 experts: 26 us with clusters of eight, one or two CTAs per SM)
-__host__ __device__ constexpr int rt_cluster(int tb) { return tb == 1 ? 8 : 4; }
 constexpr int kRtWarps = 16;
 constexpr int kRtThreads = kRtWarps * 32;
+constexpr int kRtMaxSmem = 224 * 1024;
 
 template <int TB>
 __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) {
-    constexpr int kRtCluster = rt_cluster(TB);
     extern __shared__ __align__(16) uint8_t smem[];
     double* logits = reinterpret_cast<double*>(smem);                 // [E]: of this CTA's token
     uint32_t* xs = reinterpret_cast<uint32_t*>(smem + 8 * ((A.E + 1) & ~1));  // [TB][H] high words of x
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const int64_t t0 = (int64_t)(blockIdx.x / kRtCluster) * TB;
+    const int64_t t0 = (int64_t)(blockIdx.x / A.C) * TB;
     const int nt = (int)min((int64_t)TB, A.T - t0);
     cluster_arrive();
     pdl_trigger();
@@ -159,12 +156,13 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
     __syncthreads();
     cluster_wait();  // every CTA of the cluster has begun
     constexpr int EB = TB > 1 ? 2 : 1;  // experts of a warp's pass
-    constexpr int U = kRtUnroll / EB, kStep = kRtCluster * kRtWarps;
-    for (int e0 = (int)rank * kRtWarps + warp; e0 < A.E; e0 += EB * kStep) {
+    constexpr int U = kRtUnroll / EB;
+    const int step = A.C * kRtWarps;
+    for (int e0 = (int)rank * kRtWarps + warp; e0 < A.E; e0 += EB * step) {
         const uint4* w[EB];
 #pragma unroll
         for (int b = 0; b < EB; ++b)  // a pass without a second expert takes the first again
-            w[b] = reinterpret_cast<const uint4*>(A.R + (int64_t)(e0 + b * kStep < A.E ? e0 + b * kStep : e0) * A.H);
+            w[b] = reinterpret_cast<const uint4*>(A.R + (int64_t)(e0 + b * step < A.E ? e0 + b * step : e0) * A.H);
         double acc[EB][TB];
 #pragma unroll
         for (int b = 0; b < EB; ++b)
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 // 2^896: 1023 + 896 in the exponent field
-                const int e = e0 + b * kStep;
+                const int e = e0 + b * step;
                 if (lane == 0 && e < A.E)
                     st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), s * from_hi(1919u << 20));
             }
@@ -239,20 +237,45 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
 size_t route_smem(int TB, int E, int H) { return (size_t)8 * ((E + 1) & ~1) + (size_t)TB * H * 4; }
 
 template <int TB>
-cudaError_t launch(RouteArgs& A, cudaStream_t st) {
+struct RouteKernel {
+    static const void* fn() { return reinterpret_cast<const void*>(&k_moe_route<TB>); }
+    static cudaError_t setup() {
+        return once_per_device<RouteKernel>(
+            [] { return cudaFuncSetAttribute(fn(), cudaFuncAttributeMaxDynamicSharedMemorySize, kRtMaxSmem); });
+    }
+};
+
+// Cost of a choice: waves of clusters, each about 2.7 us and 3.1, 3.3 or 5.3 per expert of a warp at 4096 columns (TB of 1,
+// 2 and 4; two experts share a pass above 1).  Measured, us at best / at the tokens per cluster and CTAs that a rule on T
+// alone took: 16 tokens x 256 experts x 4096 10.0 / 17.2, 24 the same 10.1 / 15.3, 64 the same 16.2.
+template <int TB>
+cudaError_t consider(const RouteArgs& A, double* least, int* tb, int* c) {
     const size_t smem = route_smem(TB, A.E, A.H);
-    const cudaError_t e = once_per_device<std::integral_constant<int, TB>>([] {
-        return cudaFuncSetAttribute(k_moe_route<TB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
-    });
+    if (smem > kRtMaxSmem) return cudaSuccess;
+    const cudaError_t e = RouteKernel<TB>::setup();
     if (e != cudaSuccess) return e;
+    constexpr int EB = TB > 1 ? 2 : 1;
+    constexpr double per = TB == 1 ? 3.1 : (TB == 2 ? 3.3 : 5.3);
+    for (int C = 4; C <= 8; C += 4) {
+        const int held = clusters_at_once<RouteKernel<TB>>(RouteKernel<TB>::fn(), kRtThreads, smem, C);
+        if (held < 1) return cudaErrorInvalidConfiguration;
+        const int waves = ((A.T + TB - 1) / TB + held - 1) / held, experts = C * kRtWarps * EB;
+        const double cost = waves * (2.7 + (A.E + experts - 1) / experts * EB * per * A.H / 4096);
+        if (cost < *least) *least = cost, *tb = TB, *c = C;
+    }
+    return cudaSuccess;
+}
+
+template <int TB>
+cudaError_t launch(RouteArgs& A, cudaStream_t st) {
     void* args[] = {&A};
-    return launch_early(reinterpret_cast<const void*>(&k_moe_route<TB>), (int64_t)((A.T + TB - 1) / TB) * rt_cluster(TB),
-                        kRtThreads, smem, rt_cluster(TB), args, st);
+    return launch_early(RouteKernel<TB>::fn(), (int64_t)((A.T + TB - 1) / TB) * A.C, kRtThreads, route_smem(TB, A.E, A.H), A.C,
+                        args, st);
 }
 
 }  // namespace
 
-bool moe_route_supported(int E, int64_t H) { return H <= INT32_MAX && route_smem(1, E, (int)H) <= 224 * 1024; }
+bool moe_route_supported(int E, int64_t H) { return H <= INT32_MAX && route_smem(1, E, (int)H) <= kRtMaxSmem; }
 
 cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t T, int E, int64_t H, int k,
                              bool renorm, int32_t* ids, float* weights, cudaStream_t st) {
@@ -268,10 +291,12 @@ cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* rou
     A.H = (int32_t)H;
     A.k = k;
     A.renorm = renorm ? 1 : 0;
-    // tokens per cluster: one for a few tokens, two while the clusters of four hold them all at once, then four, which
-    // share a weight's conversion and its read from L2
-    int tb = T <= 16 ? 1 : (T <= 64 ? 2 : 4);
-    while (tb > 1 && route_smem(tb, E, (int)H) > 224 * 1024) tb /= 2;
+    double least = 1e300;
+    int tb = 1;
+    cudaError_t e = consider<1>(A, &least, &tb, &A.C);
+    if (e == cudaSuccess && T > 1) e = consider<2>(A, &least, &tb, &A.C);
+    if (e == cudaSuccess && T > 2) e = consider<4>(A, &least, &tb, &A.C);
+    if (e != cudaSuccess) return e;
     return tb == 1 ? launch<1>(A, st) : (tb == 2 ? launch<2>(A, st) : launch<4>(A, st));
 }
 

@@ -10,8 +10,8 @@
 // instruction rounds half to even.
 //
 // Both kernels are bound by HBM: 2 or 4 bytes per weight on the wide side,
-// 0.53 on the narrow one (17408 x 5120: fp32 to codes 68.8 us, 5.9 TB/s, codes
-// to bf16 36.7 us, 6.1 TB/s; 4096 bf16 values 1.6 us, launch latency).  A warp holds a piece of one row, each lane 16 bytes
+// 0.53 on the narrow one (17408 x 5120: fp32 to codes 66.5 us, 6.1 TB/s, codes
+// to bf16 36.8 us, 6.1 TB/s; 4096 bf16 values 1.6 us, launch latency).  A warp holds a piece of one row, each lane 16 bytes
 // of it per load (contiguous over the lanes), kLoads loads in flight; what is
 // addressed after the first load is a constant away.  (With a division and
 // 64-bit addresses per load the quantiser was bound by its instructions, 98 us

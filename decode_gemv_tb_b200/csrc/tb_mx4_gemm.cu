@@ -18,12 +18,12 @@
 // units enough run one after the other in persistent CTAs, S = 1.  Bound by
 // W's bytes and, below about 10 us, by the fixed parts (launch, first copy,
 // cluster sum, about 3 us): 4096 x 4096, one row, 4.6 us; 17408 x 5120, 61
-// rows, 11.6 us (4.1 TB/s of W; the byte floor is 7.6).
+// rows, 11.5 us (4.1 TB/s of W; the byte floor is 7.6).
 // Below 128 rows a unit has all of them: the MMA takes X's scales from the
 // first column of a tile of 128 rows, and no unit may begin inside one.
 //
 // k_mx4_prefill, whole tiles of large batches: below.  17408 x 5120, 4096
-// rows: 162 us, 4.5 PFLOP/s (2.7 times the measured bf16 rate), the tensor
+// rows: 161 us, 4.5 PFLOP/s (2.7 times the measured bf16 rate), the tensor
 // pipe busy 56 % of the time.
 //
 // A CTA: a producer warp (per chunk two tensor copies, W and X, 128-byte
