@@ -18,8 +18,8 @@
 // the tokens of the cluster.
 //
 // Bound by instructions, 4.7 per DFMA: 64 tokens x 256 experts x 4096 take
-// 16.5 us (issue slots 64 % busy; the DFMAs alone would take 3.7 us, the bytes
-// 0.4); one token x 128 experts x 2048 takes 4.6 us, mostly launch, the
+// 16.1 us (issue slots 64 % busy; the DFMAs alone would take 3.7 us, the bytes
+// 0.4); one token x 128 experts x 2048 takes 4.4 us, mostly launch, the
 // cluster's barriers and the selection.
 //
 // A cluster of CTAs handles TB tokens: its warps take two experts
@@ -246,8 +246,8 @@ struct RouteKernel {
 };
 
 // Cost of a choice: waves of clusters, each about 2.7 us and 3.1, 3.3 or 5.3 per expert of a warp at 4096 columns (TB of 1,
-// 2 and 4; two experts share a pass above 1).  Measured, us at best / at the tokens per cluster and CTAs that a rule on T
-// alone took: 16 tokens x 256 experts x 4096 10.0 / 17.2, 24 the same 10.1 / 15.3, 64 the same 16.2.
+// 2 and 4; two experts share a pass above 1).  Measured, us by this choice / by one
+// on T alone, 256 experts x 4096: 16 tokens 10.0 / 17.2, 24 tokens 10.1 / 15.3, 64 tokens 16.1 by both.
 template <int TB>
 cudaError_t consider(const RouteArgs& A, double* least, int* tb, int* c) {
     const size_t smem = route_smem(TB, A.E, A.H);
