@@ -13,6 +13,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,10 +41,26 @@ def _stale() -> bool:
     return _older(LIB, deps)
 
 
-def _build_bind(force: bool):
-    src = os.path.join(CSRC, "tb_bind.cpp")
-    if not force and not _older(BIND, [src, os.path.join(ROOT, "include", "tb.h")]):
-        return
+def bind_tag() -> str:
+    """What _tb_bind.so is built for; the file holds it, as the module's `built_for`."""
+    import torch
+
+    return f"torch {torch.__version__}, python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def _bind_stale() -> bool:
+    if _older(BIND, [os.path.join(CSRC, "tb_bind.cpp"), os.path.join(ROOT, "include", "tb.h")]):
+        return True
+    with open(BIND, "rb") as f:
+        return bind_tag().encode() + b"\0" not in f.read()
+
+
+def build_bind(force: bool = False) -> str:
+    """_tb_bind.so, which needs g++ and the headers of the torch that will load it."""
+    if not force and not _bind_stale():
+        return BIND
+    if os.path.exists(BIND):  # what cannot be built anew is not left behind for another torch or another tb.h
+        os.remove(BIND)
     import torch
     from torch.utils import cpp_extension
 
@@ -51,23 +68,34 @@ def _build_bind(force: bool):
     dirs = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), os.path.join(cuda, "include"),
             *cpp_extension.include_paths()]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{d}" for d in dirs), src,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DTB_BUILT_FOR="{bind_tag()}"',
+           *(f"-isystem{d}" for d in dirs), os.path.join(CSRC, "tb_bind.cpp"),
            "-o", BIND + ".tmp", *(f"-L{d}" for d in cpp_extension.library_paths()),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     subprocess.run(cmd, check=True)
     os.replace(BIND + ".tmp", BIND)
+    return BIND
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    _build_bind(force)
+def _build_lib(force: bool, verbose: bool):
     if not force and not _stale():
-        return LIB
+        return
     cmd = [NVCC, *ARCH, *FLAGS, "-I", os.path.join(ROOT, "include")]
     if verbose:
         cmd += ["-Xptxas", "-v"]
     cmd += ["-o", LIB + ".tmp", *sources()]
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Both libraries.  The CUDA library needs nvcc alone; without the other only the 4-bit and expert-layer calls of
+    the Python binding raise, so a failure to build that one is a warning."""
+    _build_lib(force, verbose)
+    try:
+        build_bind(force)
+    except (OSError, ImportError, subprocess.CalledProcessError) as e:
+        warnings.warn(f"_tb_bind.so not built, the 4-bit and expert-layer calls will raise: {e}")
     return LIB
 
 

@@ -275,4 +275,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tb_bind", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tb_bind(void) { return PyModule_Create(&module); }
+// built_for: the torch and Python whose headers this was compiled with (no other may run it)
+PyMODINIT_FUNC PyInit__tb_bind(void) {
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", TB_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -9,9 +9,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
 
 import torch
+
+from decode_gemv_tb_b200.build import bind_tag
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtb_b200.so")
@@ -84,8 +87,31 @@ _lib = None
 _bind = None  # _tb_bind.so, the calls that do not go through ctypes
 
 
+class _NoBind:
+    """In the place of _tb_bind.so where that cannot be loaded: its calls raise, the others do not need it."""
+
+    def __init__(self, why: str):
+        self._why = f"_tb_bind.so: {why}; run `python -m decode_gemv_tb_b200.build`"
+
+    def __getattr__(self, name):
+        raise TBError(self._why)
+
+
+def _load_bind(lib: ctypes.CDLL):
+    try:
+        bind = importlib.import_module("decode_gemv_tb_b200._tb_bind")
+    except ImportError as e:
+        return _NoBind(str(e))
+    built_for = getattr(bind, "built_for", "another version of this package")
+    if built_for != bind_tag():
+        return _NoBind(f"built for {built_for}, not for {bind_tag()}")
+    bind.init(TBError, *(ctypes.cast(getattr(lib, name), _P).value for name in BOUND))
+    return bind
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load the shared library (raises if it is missing)."""
+    """Load the shared library (raises if it is missing).  _tb_bind.so is loaded beside it where it can be; without it
+    the 4-bit and expert-layer calls raise."""
     global _lib, _bind
     if _lib is None:
         if not os.path.exists(path):
@@ -95,12 +121,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             f = getattr(lib, name)
             f.restype = res
             f.argtypes = args
-        try:
-            from decode_gemv_tb_b200 import _tb_bind
-        except ImportError as e:
-            raise TBError(f"_tb_bind.so: {e}; run `python -m decode_gemv_tb_b200.build`") from e
-        _tb_bind.init(TBError, *(ctypes.cast(getattr(lib, name), _P).value for name in BOUND))
-        _bind, _lib = _tb_bind, lib
+        _bind, _lib = _load_bind(lib), lib
     return _lib
 
 
