@@ -215,8 +215,9 @@ int clusters_at_once(const void* fn, int block, size_t smem, int c) {
 }
 
 // A launch, in clusters of `cluster` CTAs where that is above 1, that may begin while the work in front of it in the stream
-// still runs: the kernel waits for it (pdl_wait) before its first access to memory.  Kernels launched so let the next one
-// begin early too (pdl_trigger), which takes about a microsecond off every boundary between them.
+// still runs: the kernel waits for it (pdl_wait) before its first access to memory (k_moe_down reads some of its inputs
+// earlier, and says there why it may).  Kernels launched so let the next one begin early too (pdl_trigger), which takes about
+// a microsecond off every boundary between them.
 inline cudaError_t launch_early(const void* fn, int64_t grid, int block, size_t smem, int cluster, void** args, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));

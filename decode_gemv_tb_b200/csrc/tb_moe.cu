@@ -377,15 +377,17 @@ __device__ __forceinline__ int blk_count(uint32_t b) { return (int)(b >> 20); }
 // the token of pair p < 1024: p / k by a multiplication (exact, k <= 16)
 __device__ __forceinline__ int pair_token(int p, const MoeArgs& A) { return (int)((uint32_t)p * A.per_k >> 16); }
 
-// blocks of up to BT tokens
+// blocks of up to BT tokens; `pair_expert` (or null): the expert of every pair, -1 for none.  The ids are read past the
+// L1: see k_moe_down.
 template <int BT>
-__device__ void build_list(MoeList& L, MoeMasks& X, const MoeArgs& A) {
+__device__ void build_list(MoeList& L, MoeMasks& X, int16_t* pair_expert, const MoeArgs& A) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < A.E; e += kMoeThreads) X.mask[0][e] = X.mask[1][e] = 0u;
     __syncthreads();
     for (int p = tid; p < A.T * A.k; p += kMoeThreads) {
-        const int e = A.ids[p], t = pair_token(p, A);
-        if (e >= 0 && e < A.E) atomicOr(&X.mask[t >> 5][e], 1u << (t & 31));  // a set: the order does not matter
+        const int id = __ldcg(A.ids + p), t = pair_token(p, A), e = id >= 0 && id < A.E ? id : -1;
+        if (e >= 0) atomicOr(&X.mask[t >> 5][e], 1u << (t & 31));  // a set: the order does not matter
+        if (pair_expert) pair_expert[p] = (int16_t)e;
     }
     __syncthreads();
     constexpr int kPer = kMoeMaxExperts / kMoeThreads;  // experts of a thread
@@ -484,8 +486,8 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_up(const __grid
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_wait();
     fence_copies();
-    build_list<8 * NS>(L, *reinterpret_cast<MoeMasks*>(part), A);
-    pdl_trigger();
+    build_list<8 * NS>(L, *reinterpret_cast<MoeMasks*>(part), nullptr, A);
+    pdl_trigger();  // not before pdl_wait: k_moe_down begins with what the kernels before this one wrote
 
     // warps that share a unit, each a part of K: the number whose rounds over all units end first (in half groups; a unit
     // costs about one to begin and end, two where its parts are added)
@@ -654,7 +656,7 @@ __host__ __device__ __forceinline__ DownSplit down_split(int G, int warps, int b
 template <int KIND>
 struct MoeDown {
     using W = Stream<KIND, 2>;
-    static constexpr int kFixed = sizeof(MoeList) + sizeof(MoeMasks) + kMaxPairs * 6;
+    static constexpr int kFixed = sizeof(MoeList) + sizeof(MoeMasks) + kMaxPairs * 8;
     static constexpr int kSmem = kMoeWarps * (W::kRing + W::kSide + W::kBars) + 1024;
     static_assert(2 * (kSmem + kFixed + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_down(const __gr
     __shared__ MoeList L;
     __shared__ MoeMasks X;
     __shared__ float slot_w[kMaxPairs];
-    __shared__ int16_t pair_slot[kMaxPairs];
+    __shared__ int16_t pair_expert[kMaxPairs], pair_slot[kMaxPairs];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3, C = A.C, G = A.down.G;
     const int rank = C > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / C;
     uint8_t* const base = raw + ((1024u - (sm_addr(raw) & 1023u)) & 1023u);
@@ -674,9 +676,13 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_down(const __gr
         sm_addr(base + kMoeWarps * (W::kRing + W::kSide)) + warp * W::kBars, A);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     pdl_trigger();
-    // the kernel before waited for its inputs: ids, weights and the experts are final, only h is not
+    // Ahead of this kernel's own wait, ids, weights and the experts' codes and scale tiles are read, and nothing else.  They
+    // are final: k_moe_up lets this kernel begin only after its own wait, behind which every kernel before it has completed
+    // and its writes have reached the L2.  This SM's L1 may still hold older lines (it need not have had a CTA of
+    // k_moe_up), so ids and weights are read past it, as the tensor copies read the experts.  bf16 scales, which are read
+    // through the L1, and h come after the wait.
     fence_copies();
-    build_list<8 * NS>(L, X, A);
+    build_list<8 * NS>(L, X, pair_expert, A);
     float* z = A.z + (int64_t)tile * A.zrows * kDownRows;  // the cluster's [slots][KS][kDownRows]
     const int step = C * kMoeWarps, KS = down_split(G, step, L.blocks, L.slots, A.zrows).slices, tasks = L.blocks * KS;
     const int q0 = rank * kMoeWarps + warp;
@@ -694,16 +700,16 @@ __global__ void __launch_bounds__(kMoeThreads, kCtasPerSM) k_moe_down(const __gr
     for (int i = 0; i < kStages; ++i) feed();
     // a pair's slot, or -1: none, or its token names the expert before; the slot's weight: that of all such pairs
     for (int p = threadIdx.x; p < A.T * A.k; p += kMoeThreads) {
-        const int e = A.ids[p], tok = pair_token(p, A);
+        const int e = pair_expert[p], tok = pair_token(p, A);
         int slot = -1;
-        if (e >= 0 && e < A.E) {
+        if (e >= 0) {
             const uint32_t below = (1u << (tok & 31)) - 1u;
             slot = X.first[e] + (tok < 32 ? __popc(X.mask[0][e] & below) : __popc(X.mask[0][e]) + __popc(X.mask[1][e] & below));
-            float v = A.weights[p];
+            float v = __ldcg(A.weights + p);
             for (int q = tok * A.k; q < (tok + 1) * A.k; ++q)
-                if (q != p && A.ids[q] == e) {
+                if (q != p && pair_expert[q] == e) {
                     if (q < p) slot = -1;
-                    v += A.weights[q];
+                    v += __ldcg(A.weights + q);
                 }
             if (slot >= 0) slot_w[slot] = v;
         }
