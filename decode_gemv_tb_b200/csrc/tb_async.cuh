@@ -184,9 +184,10 @@ cudaError_t once_per_device(F set) {
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
-// Clusters of c <= 8 CTAs that the device holds at once, by kernels named K (as many CTAs per SM in all of them; asked once).
-// They stay within a group of SMs, and what is left over in each group stays empty: at two CTAs per SM 71 clusters of four,
-// not 74 -- a 72nd doubled a kernel's time.  0 on error.
+// Clusters of c <= 8 CTAs that the device holds at once.  K names one kernel with one block size and one amount of shared
+// memory (of a kernel that is launched with several: the largest), so that the answer, asked once, holds for every call.
+// Clusters stay within a group of SMs, and what is left over in each group stays empty: at two CTAs per SM 71 clusters of
+// four, not 74 -- a 72nd doubled a kernel's time.  0 on error.
 template <class K>
 int clusters_at_once(const void* fn, int block, size_t smem, int c) {
     static std::atomic<int> known[64][9];

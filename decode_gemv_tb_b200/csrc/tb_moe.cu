@@ -813,6 +813,7 @@ struct MoeKernel {
     const void* fn;
     int smem;
     cudaError_t (*setup)();
+    int (*held)(int c);  // k_moe_down: clusters of c CTAs at once
 };
 template <int KG, int KU, int NS>
 cudaError_t up_setup() {
@@ -820,7 +821,7 @@ cudaError_t up_setup() {
 }
 template <int KG, int KU, int NS>
 MoeKernel up_of() {
-    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), MoeUp<KG, KU, NS>::kSmem, &up_setup<KG, KU, NS>};
+    return {reinterpret_cast<const void*>(&k_moe_up<KG, KU, NS>), MoeUp<KG, KU, NS>::kSmem, &up_setup<KG, KU, NS>, nullptr};
 }
 template <int NS>
 MoeKernel up_kernel(int kg, int ku) {
@@ -836,8 +837,14 @@ cudaError_t down_setup() {
     return once_per_device<DownOf<KIND, NS>>([] { return shape_kernel(reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), MoeDown<KIND>::kSmem); });
 }
 template <int KIND, int NS>
+int down_held(int c) {
+    return clusters_at_once<DownOf<KIND, NS>>(reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), kMoeThreads,
+                                              (size_t)MoeDown<KIND>::kSmem, c);
+}
+template <int KIND, int NS>
 MoeKernel down_of() {
-    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), MoeDown<KIND>::kSmem, &down_setup<KIND, NS>};
+    return {reinterpret_cast<const void*>(&k_moe_down<KIND, NS>), MoeDown<KIND>::kSmem, &down_setup<KIND, NS>,
+            &down_held<KIND, NS>};
 }
 template <int NS>
 MoeKernel down_kernel(int kind) {
@@ -926,7 +933,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
     const double filled = taken + std::max(0.0, (T * k - taken * 4 * NS) / (8 * NS));  // blocks: more from half of one on
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8; ++c) {
-        const int64_t held = c == 1 ? (int64_t)sms * kCtasPerSM : clusters_at_once<MoeKernel>(kd.fn, kMoeThreads, (size_t)kd.smem, c);
+        const int64_t held = c == 1 ? (int64_t)sms * kCtasPerSM : kd.held(c);
         if (held < 1) continue;
         const int64_t waves = (H / kDownRows + held - 1) / held;
         const int share = down_split((int)(I / kGroup), c * kMoeWarps, std::max(1, (int)(filled + 0.5)), T * k, A.zrows).cost;

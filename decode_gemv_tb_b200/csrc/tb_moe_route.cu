@@ -257,8 +257,9 @@ cudaError_t consider(const RouteArgs& A, double* least, int* tb, int* c) {
     constexpr int EB = TB > 1 ? 2 : 1;
     constexpr double per = TB == 1 ? 3.1 : (TB == 2 ? 3.3 : 5.3);
     for (int C = 4; C <= 8; C += 4) {
-        const int held = clusters_at_once<RouteKernel<TB>>(RouteKernel<TB>::fn(), kRtThreads, smem, C);
-        if (held < 1) return cudaErrorInvalidConfiguration;
+        // (asked at the largest shared memory: one answer for every shape, whichever is called first)
+        const int held = clusters_at_once<RouteKernel<TB>>(RouteKernel<TB>::fn(), kRtThreads, kRtMaxSmem, C);
+        if (held < 1) continue;
         const int waves = ((A.T + TB - 1) / TB + held - 1) / held, experts = C * kRtWarps * EB;
         const double cost = waves * (2.7 + (A.E + experts - 1) / experts * EB * per * A.H / 4096);
         if (cost < *least) *least = cost, *tb = TB, *c = C;
@@ -297,6 +298,7 @@ cudaError_t launch_moe_route(const uint16_t* x, int64_t ldx, const uint16_t* rou
     if (e == cudaSuccess && T > 1) e = consider<2>(A, &least, &tb, &A.C);
     if (e == cudaSuccess && T > 2) e = consider<4>(A, &least, &tb, &A.C);
     if (e != cudaSuccess) return e;
+    if (A.C == 0) return cudaErrorInvalidConfiguration;  // the device holds no cluster of any of them
     return tb == 1 ? launch<1>(A, st) : (tb == 2 ? launch<2>(A, st) : launch<4>(A, st));
 }
 
