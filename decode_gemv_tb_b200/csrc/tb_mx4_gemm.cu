@@ -114,7 +114,7 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, 1) k_mx4_gemm(const __grid_constant__ MxArgs A, int S) {
+__global__ void __launch_bounds__(C::kThreads, C::per_sm(2)) k_mx4_gemm(const __grid_constant__ MxArgs A, int S) {
     constexpr int NT = C::NT, ST = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[ST], empty[ST], dfull, dfree;
@@ -581,20 +581,45 @@ bool encode_codes(CUtensorMap* map, const void* codes, int64_t rows, int64_t K, 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs that share a unit's K.  In chunks of one CTA, about 0.32 us (measured on one to 4000 rows of products from
-// 100 x 200 to 17408 x 17408): a chunk takes 1.7 times as long for each of two CTAs that share an SM; a cluster costs three
-// more, one per 8 batch rows for adding the partial sums and a quarter per CTA (clusters of eight only where each CTA has an
-// SM of its own).  4096 x 4096, one row: 8.5 / 6.9 / 5.5 / 7.1 us with 1 / 2 / 4 / 8 CTAs; 17408 x 5120, 61 rows: 12.8 with
-// one, 18.5 with two; 5120 x 17408, 61 rows: 26.7 / 19.4 / 18.5 with 1 / 2 / 4.
+// Asked how many clusters of k_mx4_gemm the device holds, the runtime answers as for one CTA per SM, since the kernel
+// allocates tensor memory: 148 / 74 / 33 / 15 clusters of 1 / 2 / 4 / 8.  By its shared memory and its columns two fit (up to
+// 64 batch rows), and two run: 71 clusters of four (71 units of 4096 values of K, one row) take 6.6 us, 72 take 9.3.  This
+// kernel has none, and is asked instead.
+__global__ void k_mx4_room() {}
+
+// CTAs of S > 1 to a unit: units that run at once
+template <class C>
+int64_t units_held(int S) {
+    struct Room;
+    const void* fn = reinterpret_cast<const void*>(&k_mx4_room);
+    if (once_per_device<Room>(
+            [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); }) != cudaSuccess)
+        return 0;
+    return clusters_at_once<C>(fn, C::kThreads, (size_t)C::smem(S), S);
+}
+
+// CTAs that share a unit's K.  In chunks of one CTA, about 0.32 us: a chunk takes 1.6 times as long for each of two CTAs that
+// share an SM; a cluster costs 1 + 0.3 S for its barriers and (0.09 + 0.1 / S) per batch row for adding the partial sums,
+// 3.5 for each round after the first.  Measured on 515 products of 1 to 128 rows, from 70 x 128 to 17408 x 17408: within
+// 1.2 % of the best of 1, 2, 4 and 8 on average, 22 % at worst.  4096 x 4096, one row: 8.5 / 6.9 / 4.9 / 7.1 us with 1 / 2 /
+// 4 / 8 CTAs; 9216 x 4096, one row: 7.7 / 5.9 / 9.3 / 12.0 (72 clusters of four are one too many); 2048 x 5120, 40 rows:
+// 8.6 / 9.2 / 6.7 / 10.9 (16 of eight likewise); 17408 x 5120, 61 rows: 11.5 with one, 18.5 with two.
 int split_of(int nt, int64_t units, int KC, int sms) {
-    const int per_sm = nt < 128 ? 2 : 1;
     int best = 1;
     double least = 1e300;
     for (int s = 1; s <= 8 && s <= KC; s *= 2) {
-        if (s > 1 && units * s > (s < 8 ? per_sm : 1) * (int64_t)sms) break;
-        const double share = units * s > sms && per_sm > 1 ? 1.7 : 1.0;
-        const double rounds = (double)((units * s + (int64_t)sms * per_sm - 1) / ((int64_t)sms * per_sm));
-        const double cost = rounds * ((KC + s - 1) / s) * share + (s > 1 ? 3 + nt / 8.0 + s / 4.0 : 0.0);
+        const bool alone = nt == 128 || (nt == 64 && units * s <= sms);
+        const int64_t held = s == 1        ? (int64_t)sms * (alone ? 1 : 2)
+                             : nt == 16    ? units_held<Mx16>(s)
+                             : nt == 32    ? units_held<Mx32>(s)
+                             : nt == 128   ? units_held<Mx128>(s)
+                             : alone       ? units_held<Mx64Alone>(s)
+                                           : units_held<Mx64>(s);
+        if (held < 1 || (s > 1 && units > 4 * held)) continue;  // (of many rounds, whole units are the shortest)
+        const double rounds = (double)((units + held - 1) / held);
+        const double chunks = ((KC + s - 1) / s) * (units * s > sms && !alone ? 1.6 : 1.0);
+        const double cost = s == 1 ? rounds * chunks
+                                   : rounds * (chunks + 1 + 0.3 * s + nt * (0.09 + 0.1 / s)) + 3.5 * (rounds - 1);
         if (cost < least) {
             least = cost;
             best = s;
