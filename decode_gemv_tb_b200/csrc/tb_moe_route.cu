@@ -13,13 +13,16 @@
 // mantissa bits into 11 and 20), so x is converted once into high words in
 // shared memory, and a weight's bits shifted right by 3 are, as the high
 // word of a double, w 2^-896 exactly (both exponent fields start at 0, so
-// zeros and subnormals map alike); the sums carry that factor.  A product
+// zeros and subnormals map alike); the sums carry that factor.  (Exponent 255
+// is mapped as if it were a number's.  A weight that is infinite or no number
+// shows in a sum of the weights' products in pairs, one instruction for four
+// weights; its row is summed again with the weights as they are.)  A product
 // costs one DFMA, two and a half integer operations per weight shared by
 // the tokens of the cluster.
 //
-// Bound by instructions, 4.7 per DFMA: 64 tokens x 256 experts x 4096 take
-// 16.1 us (issue slots 64 % busy; the DFMAs alone would take 3.7 us, the bytes
-// 0.4); one token x 128 experts x 2048 takes 4.4 us, mostly launch, the
+// Bound by instructions, about 4.8 per DFMA: 64 tokens x 256 experts x 4096 take
+// 17.0 us (16.2 without the watch on the weights; the DFMAs alone would take
+// 3.7 us, the bytes 0.4); one token x 128 experts x 2048 takes 4.4 us, mostly launch, the
 // cluster's barriers and the selection.
 //
 // A cluster of CTAs handles TB tokens: its warps take two experts
@@ -51,6 +54,18 @@ constexpr int kRtUnroll = 4;  // 16-byte loads of the router in flight per lane
 __device__ __forceinline__ double from_hi(uint32_t hi) { return __hiloint2double((int)hi, 0); }
 // high word of w 2^-896 for the bf16 in the upper half of u
 __device__ __forceinline__ uint32_t scaled_hi(uint32_t u) { return (uint32_t)((int32_t)u >> 3) & 0x8FFFE000u; }
+
+// A sum of products of pairs of weights, which serves one question: it stops being finite as soon as one of the weights is
+// not (an infinity times 0 is no number), and never becomes finite again.  (It may overflow without one: the row is then
+// summed again for nothing.)
+__device__ __forceinline__ uint32_t watch(uint32_t u0, uint32_t u1, uint32_t before) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(u0), "r"(u1), "r"(before));
+    return d;
+}
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+    return (pair & 0x7F800000u) == 0x7F800000u || (pair & 0x7F80u) == 0x7F80u;
+}
 
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
@@ -112,6 +127,25 @@ __device__ void select_experts(const double* l, const RouteArgs& A, int64_t t) {
     }
 }
 
+// The sum of row w over token t's activations, its weights converted as they are: rows with weights that are not finite.
+__device__ __noinline__ double plain_sum(const uint4* w, const uint4* x, int H8) {
+    double s = 0.0;
+    for (int h = threadIdx.x & 31; h < H8; h += 32) {
+        const uint4 v = w[h];
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint4 a = x[half * H8 + h];
+            const uint32_t hi[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s = fma((double)__uint_as_float(j & 1 ? u[2 * half + (j >> 1)] & 0xFFFF0000u : u[2 * half + (j >> 1)] << 16),
+                        from_hi(hi[j]), s);
+        }
+    }
+    return s;
+}
+
 constexpr int kRtWarps = 16;
 constexpr int kRtThreads = kRtWarps * 32;
 constexpr int kRtMaxSmem = 224 * 1024;
@@ -158,6 +192,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
     constexpr int EB = TB > 1 ? 2 : 1;  // experts of a warp's pass
     constexpr int U = kRtUnroll / EB;
     const int step = A.C * kRtWarps;
+    uint32_t again = 0u;  // the warp's experts whose rows are not finite
     for (int e0 = (int)rank * kRtWarps + warp; e0 < A.E; e0 += EB * step) {
         const uint4* w[EB];
 #pragma unroll
@@ -168,6 +203,9 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
         for (int b = 0; b < EB; ++b)
 #pragma unroll
             for (int t = 0; t < TB; ++t) acc[b][t] = 0.0;
+        uint32_t odd[EB];  // not finite as soon as a weight of the row is not
+#pragma unroll
+        for (int b = 0; b < EB; ++b) odd[b] = 0u;
         uint4 next[U][EB];
         auto load = [&](int h0) {
 #pragma unroll
@@ -198,6 +236,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
                         wd[b][1] = from_hi(scaled_hi(u0));
                         wd[b][2] = from_hi(scaled_hi(u1 << 16));
                         wd[b][3] = from_hi(scaled_hi(u1));
+                        odd[b] = watch(u0, u1, odd[b]);
                     }
 #pragma unroll
                     for (int t = 0; t < TB; ++t) {
@@ -212,17 +251,29 @@ __global__ void __launch_bounds__(kRtThreads, 1) k_moe_route(const RouteArgs A) 
             }
         }
 #pragma unroll
-        for (int b = 0; b < EB; ++b)
+        for (int b = 0; b < EB; ++b) {
+            const int e = e0 + b * step;
+            if (__any_sync(0xffffffffu, not_finite(odd[b]))) again |= 1u << ((uint32_t)e / (uint32_t)step);
 #pragma unroll
             for (int t = 0; t < TB; ++t) {
                 double s = acc[b][t];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                 // 2^896: 1023 + 896 in the exponent field
-                const int e = e0 + b * step;
                 if (lane == 0 && e < A.E)
                     st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), s * from_hi(1919u << 20));
             }
+        }
+    }
+    for (; again != 0u; again &= again - 1u) {
+        const int e = (int)rank * kRtWarps + warp + (__ffs((int)again) - 1) * step;
+        if (e >= A.E) break;  // (the first expert, taken again)
+        for (int t = 0; t < TB; ++t) {
+            double s = plain_sum(reinterpret_cast<const uint4*>(A.R + (int64_t)e * A.H),
+                                 reinterpret_cast<const uint4*>(xs) + t * 2 * H8, H8);
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) st_cluster_f64(map_rank(sm_addr(logits + e), (uint32_t)t), s);
+        }
     }
     __syncwarp();
     cluster_arrive();
@@ -246,8 +297,9 @@ struct RouteKernel {
 };
 
 // Cost of a choice: waves of clusters, each about 2.7 us and 3.1, 3.3 or 5.3 per expert of a warp at 4096 columns (TB of 1,
-// 2 and 4; two experts share a pass above 1).  Measured, us by this choice / by one
-// on T alone, 256 experts x 4096: 16 tokens 10.0 / 17.2, 24 tokens 10.1 / 15.3, 64 tokens 16.1 by both.
+// 2 and 4; two experts share a pass above 1).  Measured without the watch on the weights, us by this choice / by
+// one on T alone, 256 experts x 4096: 16 tokens 10.0 / 17.2, 24 tokens 10.1 / 15.3, 64 tokens 16.1 by both (with it 10.6, 10.6
+// and 17.0).
 template <int TB>
 cudaError_t consider(const RouteArgs& A, double* least, int* tb, int* c) {
     const size_t smem = route_smem(TB, A.E, A.H);

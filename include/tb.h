@@ -428,9 +428,10 @@ TB_API tb_status_t tb_mx4_gemm(const void *w_codes, const uint8_t *w_scales, con
  * unless they differ by less than H (2^-53 sum |x r| + 2^-178).
  *   x        [T][ldx] bf16, ldx >= H, ldx % 8 == 0, 16-byte aligned;
  *            1 <= T <= 65536.
- *   router   [E][H] bf16, 16-byte aligned, finite; 1 <= E <=
- *            TB_MOE_MAX_EXPERTS, H % 8 == 0 (H <= 56000, or
- *            TB_ERR_UNSUPPORTED).
+ *   router   [E][H] bf16, 16-byte aligned; 1 <= E <= TB_MOE_MAX_EXPERTS,
+ *            H % 8 == 0 (H <= 56000, or TB_ERR_UNSUPPORTED).
+ * Values of x and router that are infinite or NaN give the logits and weights
+ * that the formulas give in IEEE arithmetic.
  *   k        1 .. min(E, TB_MOE_MAX_TOPK).
  *   ids      [T][k] int32, weights [T][k] fp32, written. */
 TB_API tb_status_t tb_moe_route(const uint16_t *x, int64_t ldx, const uint16_t *router, int64_t T, int64_t E, int64_t H,
