@@ -398,10 +398,12 @@ TB_API tb_status_t tb_mx4_dequantize(const void *codes, const uint8_t *scales, i
  *   Y                  [M][ldy] fp32 or bf16, ldy >= N; Y[m][n] for n < N
  *                      written.
  *   flags              0 (test hook: TB_FLAG_TEST_STALL).
- * Every product is exact; the running sum is rounded to fp32 once per 64 k:
- *   |y - y_exact| <= (K/64 + 12) 2^-23 sum_k |x_k w_k| (plus 2^-8 |y| for bf16
- *   outputs);
- * results are bitwise deterministic.  A NaN scale makes the outputs of its
+ * Every product is exact down to multiples of 2^-149; the running sum is
+ * rounded to fp32 once per 64 k.  While sum_k |x_k w_k| < 2^127:
+ *   |y - y_exact| <= (K/64 + 12) 2^-23 sum_k |x_k w_k| + K 2^-149 (plus
+ *   2^-8 |y| + 2^-134 for bf16 outputs);
+ * sums past fp32's range are infinite or, of infinities of both signs, NaN.
+ * Results are bitwise deterministic.  A NaN scale makes the outputs of its
  * row (of W or X) NaN. */
 TB_API tb_status_t tb_mx4_gemm(const void *w_codes, const uint8_t *w_scales, const void *x_codes,
                                const uint8_t *x_scales, void *Y, tb_dtype_t y_dtype, int64_t ldy, int64_t M,
@@ -466,11 +468,13 @@ TB_API size_t tb_moe_workspace_bytes(const tb_moe_t *layer, int64_t T, int k);
  *   flags      0 (test hook: TB_FLAG_TEST_STALL).
  *   workspace  tb_moe_workspace_bytes(layer, T, k) bytes (rules above).
  * Codes (times their scale, for MX4) are decoded exactly, sums are fp32;
- * bitwise deterministic.  With u = 2^-24 and A(v)
- * the same sums over absolute values:
- *     |dg|, |du| <= (H/8 + 16) u A(x),
- *     |dh| <= 1.1 |dg| (|u| + |du|) + |silu(g)| |du| + 2^-8 |h|,
- *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/8 + k + 24) u A_down(|h| + |dh|))
+ * bitwise deterministic.  (MX4 scale bytes up to 252, the quantizer's largest.
+ * Above it values past fp32's range are infinite, as tb_mx4_dequantize gives
+ * them, and NaN times an activation of 0.)  While the sums over absolute
+ * values, A(v), and |silu(g) u| stay below 2^127, with u = 2^-24:
+ *     |dg|, |du| <= (H/8 + 16) u A(x) + 2^-126,
+ *     |dh| <= 1.1 |dg| (|u| + |du|) + |silu(g)| |du| + 2^-8 |h| + 2^-126,
+ *     |dy| <= sum_j |weights[t][j]| (A_down(|dh|) + (I/8 + k + 24) u A_down(|h| + |dh|) + 2^-126) + 2^-126
  * (plus 2^-8 |y| for bf16 outputs). */
 TB_API tb_status_t tb_moe(const tb_moe_t *layer, const uint16_t *x, int64_t ldx, const int32_t *ids, const float *weights,
                           int64_t T, int k, void *y, tb_dtype_t y_dtype, int64_t ldy, unsigned flags,
