@@ -52,6 +52,14 @@ int64_t integer(PyObject* o) {
     }
     return v;
 }
+bool truth(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Refused(std::string(name) + " must be true or false");
+    }
+    return v != 0;
+}
 unsigned flag_bits(PyObject* o) {
     const int64_t v = integer(o);
     if (v < 0 || v > 0xFFFFFFFFll) throw Refused("flags must fit in 32 bits");
@@ -189,11 +197,12 @@ void route(Args a) {
     matrix(x, "x");
     matrix(r, "router");
     const int64_t T = x.size(0), H = x.size(1), E = r.size(0), k = integer(a[2]), ldx = bf16_rows(x, "x", T, H);
+    const bool renormalize = truth(a[3], "renormalize");
     if (bf16_rows(r, "router", E, H) != H) throw Refused("router must be contiguous");
     const int dev = same_device(x, r, ids, w);
     if (k < 1 || k > TB_MOE_MAX_TOPK) check(TB_ERR_ARG, "tb_moe_route");
     check(f_route(static_cast<const uint16_t*>(x.data_ptr()), ldx, static_cast<const uint16_t*>(r.data_ptr()), T, E, H,
-                  (int)k, PyObject_IsTrue(a[3]) == 1, pairs<int32_t>(ids, "ids", at::kInt, T, k),
+                  (int)k, renormalize, pairs<int32_t>(ids, "ids", at::kInt, T, k),
                   pairs<float>(w, "weights", at::kFloat, T, k), stream(a[6], dev)),
           "tb_moe_route");
 }
