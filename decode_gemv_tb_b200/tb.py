@@ -455,6 +455,7 @@ def tb_moe(layer: MoELayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.T
             if y is None:
                 y = torch.empty((ids.shape[0], layer.H), dtype=out_dtype, device=x.device)
             if ws is None:
-                ws = workspace(moe_workspace_bytes(layer, *ids.shape), x.device)
+                # data only: nothing of it has to be zero, and no other call shares it
+                ws = torch.empty(moe_workspace_bytes(layer, *ids.shape), dtype=torch.uint8, device=x.device)
     _bind.moe(layer.ptr, layer.H, layer.device, x, ids, weights, y, ws, flags, stream)
     return y
