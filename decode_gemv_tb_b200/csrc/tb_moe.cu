@@ -9,7 +9,7 @@
 // 64 tokens x 128 experts of 4096 x 1536 in MX4 421 us (3.0 TB/s of codes; byte
 // floor 193), issue slots 64 % and the ALU pipe 62 % busy in the up kernel; 16
 // tokens x 64 experts of 2048 x 1408 in 2 and 3 bits 64 us (floor 19); one
-// token x 8 of 128 experts of 2048 x 768, ternary, 13.8 us (floor 1.5), of
+// token x 8 of 128 experts of 2048 x 768, ternary, 13.5 us (floor 1.5), of
 // which two launches, the expert lists and the first copies take about 10.
 // A 16 x 128 tile takes a scheduler 153 (2 bits), 178 (3 bits) and 262 cycles
 // (MX4), 64 of them its MMAs; HBM delivers one in 93, 137
@@ -33,7 +33,8 @@
 // copies took 451.)
 //
 // h is rounded to bf16 between the two products, as tb_gate_up_silu's is: the
-// MMA's operand, and half the activations a second part would cost.
+// MMA's operand, and half the activations a second part would cost (494 us
+// against 416 at 64 tokens of the MX4 layer).
 //
 // k_moe_up: a unit is (block, 16 rows of gate and of up); S warps of a CTA
 // split K where that evens out the warps' shares.  k_moe_down: a cluster of C

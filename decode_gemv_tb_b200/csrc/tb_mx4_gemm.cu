@@ -23,8 +23,11 @@
 // first column of a tile of 128 rows, and no unit may begin inside one.
 //
 // k_mx4_prefill, whole tiles of large batches: below.  17408 x 5120, 4096
-// rows: 161 us, 4.5 PFLOP/s (2.7 times the measured bf16 rate), the tensor
-// pipe busy 56 % of the time.
+// rows: 162 us alone, 4.5 PFLOP/s (2.7 times the measured bf16 rate; the 4-bit
+// rate is four times it), the tensor pipe busy 56 % of the time; 183 to 191
+// back to back under the power cap.  Where rows of Y are not multiples of 16
+// bytes the small-batch kernel runs instead, in blocks of 128 rows: 17407 x
+// 5120, 4096 rows, 245 to 258 us.
 //
 // A CTA: a producer warp (per chunk two tensor copies, W and X, 128-byte
 // swizzled, and bulk copies of the scale tiles), an MMA warp (scale tiles
