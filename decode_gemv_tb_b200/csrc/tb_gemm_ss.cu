@@ -754,7 +754,7 @@ cudaError_t launch_gemm_ss(const void* packed, int grid, const uint16_t* scales,
 unsigned int take_ss_timeouts() {
     unsigned int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_ss_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-    if (cudaMemcpyToSymbol(g_ss_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (v != 0 && cudaMemcpyToSymbol(g_ss_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
     return v;
 }
 

@@ -874,7 +874,7 @@ cudaError_t launch_gemv8(const G8Launch& L, bool two, bool overlap, cudaStream_t
 unsigned int take_g8_timeouts() {
     unsigned int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_g8_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-    if (cudaMemcpyToSymbol(g_g8_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (v != 0 && cudaMemcpyToSymbol(g_g8_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
     return v;
 }
 

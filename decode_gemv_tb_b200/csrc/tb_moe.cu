@@ -956,7 +956,7 @@ cudaError_t launch_moe(const MoeWeights& gate, const MoeWeights& up, const MoeWe
 unsigned int take_moe_timeouts() {
     unsigned int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_moe_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-    if (cudaMemcpyToSymbol(g_moe_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (v != 0 && cudaMemcpyToSymbol(g_moe_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
     return v;
 }
 

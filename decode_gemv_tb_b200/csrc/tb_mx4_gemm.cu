@@ -736,7 +736,7 @@ cudaError_t launch_mx4_gemm(const void* w, const uint8_t* w_scales, const void* 
 unsigned int take_mx_timeouts() {
     unsigned int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_mx_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-    if (cudaMemcpyToSymbol(g_mx_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (v != 0 && cudaMemcpyToSymbol(g_mx_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
     return v;
 }
 

@@ -613,7 +613,7 @@ cudaError_t launch_gemm_tc(const void* packed, int grid, const uint16_t* scales,
 unsigned int take_wait_timeouts() {
     unsigned int v = 0, z = 0;
     if (cudaMemcpyFromSymbol(&v, g_wait_timeouts, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-    if (cudaMemcpyToSymbol(g_wait_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
+    if (v != 0 && cudaMemcpyToSymbol(g_wait_timeouts, &z, sizeof(z)) != cudaSuccess) return 0xFFFFFFFFu;
     return v;
 }
 
